@@ -1,5 +1,5 @@
 """Thin ctypes binding of libpsgd (C ABI declared in include/psgd.h,
-include/psgd_rtopk.h and include/psgd_atomo.h).
+include/psgd_rtopk.h, include/psgd_atomo.h and include/psgd_clip.h).
 
 Functions carry the C names.  The step functions take torch tensors on a ROCm device
 and pass their device pointers and the current HIP stream; every step of the
@@ -34,6 +34,10 @@ PSGD_FLAG_CARRY_ERROR_MEAN = 0x2
 PSGD_FLAG_DEFERRED_ERROR = 0x4
 PSGD_FLAG_LOCAL_Q_ERROR = 0x8
 PSGD_RTOPK_FLAG_DEFERRED_ZERO = 0x1
+PSGD_NORM_L2 = 0
+PSGD_NORM_MAX = 1
+PSGD_ADAMW_DECAY_MATRICES_ONLY = 0x1
+PSGD_ADAMW_SKIP_NONFINITE = 0x2
 
 EXPORTED = [
     "psgd_plan_create", "psgd_plan_sizes", "psgd_plan_layer_info", "psgd_plan_destroy",
@@ -46,6 +50,9 @@ EXPORTED = [
     "psgd_rtopk_errors_materialize", "psgd_rtopk_plan_reset_state",
     "psgd_atomo_plan_create", "psgd_atomo_plan_sizes", "psgd_atomo_plan_layer_info", "psgd_atomo_plan_destroy",
     "psgd_atomo_step", "psgd_atomo_plan_set_timing", "psgd_atomo_plan_kernel_stats",
+    "psgd_clip_plan_create", "psgd_clip_plan_sizes", "psgd_clip_plan_layer_info", "psgd_clip_plan_destroy",
+    "psgd_grad_norm", "psgd_grad_clip", "psgd_adamw_apply",
+    "psgd_clip_plan_set_timing", "psgd_clip_plan_kernel_stats",
 ]
 PSGD_ATOMO_MAX_K = 1024
 _STRING_FUNCS = ("psgd_status_string", "psgd_last_error")
@@ -112,6 +119,25 @@ class _AtomoSizes(ctypes.Structure):
                 ("budget", ctypes.c_double)]
 
 
+class _ClipLayerInfo(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("numel", ctypes.c_int64),
+                ("offset", ctypes.c_int64)]
+
+
+class _ClipSizes(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int32), ("n_slices", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("worker_stride", ctypes.c_int64), ("numel", ctypes.c_int64),
+                ("workspace_bytes", ctypes.c_uint64), ("norm_bytes", ctypes.c_uint64),
+                ("clip_bytes", ctypes.c_uint64), ("adamw_bytes", ctypes.c_uint64)]
+
+
+class _AdamwConfig(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("max_norm", ctypes.c_double),
+                ("norm_kind", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
 _lib = None
 
 
@@ -163,6 +189,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.psgd_atomo_step.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.psgd_atomo_plan_set_timing.argtypes = [vp, i32]
     lib.psgd_atomo_plan_kernel_stats.argtypes = [vp, ctypes.POINTER(_KernelStat), i32, ctypes.POINTER(i32), i32]
+    lib.psgd_clip_plan_create.argtypes = [ctypes.POINTER(_Layer), i32, i32, i32, ctypes.c_uint32, ctypes.POINTER(vp)]
+    lib.psgd_clip_plan_sizes.argtypes = [vp, ctypes.POINTER(_ClipSizes)]
+    lib.psgd_clip_plan_layer_info.argtypes = [vp, i32, ctypes.POINTER(_ClipLayerInfo)]
+    lib.psgd_clip_plan_destroy.argtypes = [vp]
+    lib.psgd_grad_norm.argtypes = [vp, vp, i32, vp, vp, vp, vp]
+    lib.psgd_grad_clip.argtypes = [vp, vp, vp, i32, f32, vp, vp, vp, vp]
+    lib.psgd_adamw_apply.argtypes = [vp, ctypes.POINTER(_AdamwConfig), vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.psgd_clip_plan_set_timing.argtypes = [vp, i32]
+    lib.psgd_clip_plan_kernel_stats.argtypes = [vp, ctypes.POINTER(_KernelStat), i32, ctypes.POINTER(i32), i32]
     for name in EXPORTED:
         if name not in _STRING_FUNCS:
             getattr(lib, name).restype = ctypes.c_int
@@ -533,6 +568,165 @@ def atom_factors(plan: AtomoPlan, atoms: np.ndarray, count: np.ndarray, layer: i
     cnt = int(count[worker, L.matrix_index])
     blk = atoms[worker, L.atom_offset:L.atom_offset + cnt * (L.rows + L.cols)].reshape(cnt, L.rows + L.cols)
     return blk[:, :L.rows], blk[:, L.rows:]
+
+
+# ------------------------------------------------------------------------ norms, clipping, AdamW
+@dataclass
+class ClipLayerInfo:
+    rows: int
+    cols: int
+    numel: int
+    offset: int
+
+
+class ClipPlan:
+    """Owns a psgd_clip_plan*; freed by psgd_clip_plan_destroy (or when collected)."""
+
+    def __init__(self, handle: int, shapes: Sequence[Tuple[int, int]]):
+        self.handle = handle
+        self.shapes = [tuple(int(v) for v in s) for s in shapes]
+        self.sizes = psgd_clip_plan_sizes(self)
+        self.layers: List[ClipLayerInfo] = [psgd_clip_plan_layer_info(self, i) for i in range(len(shapes))]
+
+    def __del__(self):
+        if getattr(self, "handle", None):
+            try:
+                psgd_clip_plan_destroy(self)
+            except Exception:
+                pass
+
+
+@dataclass
+class AdamwConfig:
+    """psgd_adamw_config (see include/psgd_clip.h for ranges)."""
+
+    lr: float = 1e-3
+    beta1: float = 0.9
+    beta2: float = 0.999
+    eps: float = 1e-8
+    weight_decay: float = 0.01
+    max_norm: float = 0.0
+    norm_kind: int = PSGD_NORM_L2
+    flags: int = 0
+
+
+def psgd_clip_plan_create(shapes: Sequence[Tuple[int, int]], n_slices: int, grad_dtype: int = PSGD_F32,
+                          flags: int = 0) -> ClipPlan:
+    lib = load_library()
+    n = len(shapes)
+    arr = (_Layer * max(1, n))(*[_Layer(int(r), int(c)) for r, c in shapes])
+    h = ctypes.c_void_p()
+    _check(lib.psgd_clip_plan_create(arr, n, int(n_slices), int(grad_dtype), int(flags), ctypes.byref(h)))
+    return ClipPlan(h.value, shapes)
+
+
+def psgd_clip_plan_sizes(plan: ClipPlan) -> dict:
+    s = _ClipSizes()
+    _check(load_library().psgd_clip_plan_sizes(plan.handle, ctypes.byref(s)))
+    return {name: getattr(s, name) for name, _ in _ClipSizes._fields_}
+
+
+def psgd_clip_plan_layer_info(plan: ClipPlan, layer: int) -> ClipLayerInfo:
+    li = _ClipLayerInfo()
+    _check(load_library().psgd_clip_plan_layer_info(plan.handle, int(layer), ctypes.byref(li)))
+    return ClipLayerInfo(li.rows, li.cols, li.numel, li.offset)
+
+
+def psgd_clip_plan_destroy(plan: ClipPlan) -> None:
+    h, plan.handle = plan.handle, None
+    if h:
+        _check(load_library().psgd_clip_plan_destroy(h))
+
+
+def psgd_clip_plan_set_timing(plan: ClipPlan, enable: bool) -> None:
+    _check(load_library().psgd_clip_plan_set_timing(plan.handle, 1 if enable else 0))
+
+
+def psgd_clip_plan_kernel_stats(plan: ClipPlan, reset: bool = False) -> dict:
+    """{kernel name: (launches, total_ms)}; waits for every timed launch so far."""
+    arr = (_KernelStat * 16)()
+    n = ctypes.c_int32()
+    _check(load_library().psgd_clip_plan_kernel_stats(plan.handle, arr, 16, ctypes.byref(n), 1 if reset else 0))
+    return {arr[i].name.decode(): (arr[i].launches, arr[i].total_ms) for i in range(n.value)}
+
+
+def _buffer(name: str, t, dtypes, numel: int, device) -> int:
+    """The device pointer of a tensor the library will read or write `numel` elements of:
+    what the C side cannot see (element type, length, strides, device) is checked here."""
+    if t.dtype not in dtypes or t.numel() < numel or not t.is_contiguous() or t.device != device:
+        raise PsgdError(PSGD_ERR_INVALID_ARG, f"{name} must be a contiguous tensor of {dtypes[0]} with at least "
+                                              f"{numel} elements on {device}")
+    return t.data_ptr()
+
+
+def _clip_common(plan: ClipPlan, ref):
+    """(element types of the gradient buffers, their length, the device) of a call."""
+    import torch
+
+    if not ref.is_cuda:
+        raise PsgdError(PSGD_ERR_INVALID_ARG, "the buffers must be on a ROCm device")
+    s = plan.sizes
+    return (torch.bfloat16 if s["grad_dtype"] == PSGD_BF16 else torch.float32,), s["n_slices"] * s["worker_stride"], ref.device
+
+
+def _enqueue(fn, device, stream, *args) -> None:
+    """Call a step function with `device` current; the stream is its last argument."""
+    import torch
+
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    st = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, st))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, st))
+
+
+def psgd_grad_norm(plan: ClipPlan, grads, kind: int, norms, tensor_norms, workspace, stream=None) -> None:
+    """Enqueue the norm of every slice (and tensor, if `tensor_norms` is given; see
+    include/psgd_clip.h)."""
+    import torch
+
+    gt, total, dev = _clip_common(plan, grads)
+    s, f32 = plan.sizes, (torch.float32,)
+    _enqueue(load_library().psgd_grad_norm, dev, stream, plan.handle, _buffer("grads", grads, gt, total, dev), int(kind),
+             _buffer("norms", norms, f32, s["n_slices"], dev),
+             None if tensor_norms is None else
+             _buffer("tensor_norms", tensor_norms, f32, s["n_slices"] * s["n_layers"], dev),
+             _buffer("workspace", workspace, (torch.uint8,), s["workspace_bytes"], dev))
+
+
+def psgd_grad_clip(plan: ClipPlan, grads, out, kind: int, max_norm: float, norms, coefs, workspace,
+                   stream=None) -> None:
+    """Enqueue the clipping of every slice by its norm (`out` may be `grads`; see
+    include/psgd_clip.h)."""
+    import torch
+
+    gt, total, dev = _clip_common(plan, grads)
+    s, f32 = plan.sizes, (torch.float32,)
+    _enqueue(load_library().psgd_grad_clip, dev, stream, plan.handle, _buffer("grads", grads, gt, total, dev),
+             _buffer("out", out, gt, total, dev), int(kind), float(max_norm),
+             _buffer("norms", norms, f32, s["n_slices"], dev), _buffer("coefs", coefs, f32, s["n_slices"], dev),
+             _buffer("workspace", workspace, (torch.uint8,), s["workspace_bytes"], dev))
+
+
+def psgd_adamw_apply(plan: ClipPlan, config: AdamwConfig, update, params, exp_avg, exp_avg_sq, params_bf16, step,
+                     norm, workspace, stream=None) -> None:
+    """Enqueue one AdamW step on (optionally clipped) `update` (see include/psgd_clip.h)."""
+    import torch
+
+    gt, _, dev = _clip_common(plan, update)
+    n, f32 = plan.sizes["worker_stride"], (torch.float32,)
+    c = _AdamwConfig(config.lr, config.beta1, config.beta2, config.eps, config.weight_decay, config.max_norm,
+                     config.norm_kind, config.flags)
+    _enqueue(load_library().psgd_adamw_apply, dev, stream, plan.handle, ctypes.byref(c),
+             _buffer("update", update, gt, n, dev), _buffer("params", params, f32, n, dev),
+             _buffer("exp_avg", exp_avg, f32, n, dev), _buffer("exp_avg_sq", exp_avg_sq, f32, n, dev),
+             None if params_bf16 is None else _buffer("params_bf16", params_bf16, (torch.bfloat16,), n, dev),
+             _buffer("step", step, (torch.int64,), 1, dev),
+             None if norm is None else _buffer("norm", norm, f32, 1, dev),
+             _buffer("workspace", workspace, (torch.uint8,), plan.sizes["workspace_bytes"], dev))
 
 
 # ------------------------------------------------------------------------ layout helpers
