@@ -1,14 +1,17 @@
 // Gradient norms, clipping and AdamW over packed tensors: the gfx950 kernels and the host
 // side of psgd_clip.h.
 //
-// A tile is at most kTile consecutive elements of one tensor.  Sums of squares are held in
-// float64; every reduction has a fixed order.
+// A tile is at most kTile consecutive elements of one tensor, a run is a number of
+// consecutive tiles.  Sums of squares are held in float64; every reduction has a fixed
+// order, and a norm is joined the same way wherever it is needed.
 //
-//   cl_norm    per (tile, slice): the tile's sum of squares, or its largest magnitude
-//   cl_final   per slice: the tensors' and the slice's norm, the clip coefficient, and for
-//              AdamW the step count and the step's scalars
-//   cl_scale   per (tile, slice): out = c * g
-//   cl_adamw   per tile: the weight update
+//   cl_norm    per (run, slice): the sum of squares, or the largest magnitude
+//   cl_final   from these partials: the slices' norms and coefficients, the tensors' norms
+//              if asked, and for AdamW the step's scalars
+//   cl_scale   per (part of a tile, slice): out = c * g
+//   cl_adamw   per part of a tile: the weight update
+//
+// No kernel waits for another workgroup, and no state is kept between calls.
 
 #include <hip/hip_runtime.h>
 #include <hip/hip_ext.h>
@@ -27,9 +30,17 @@
 namespace psgd {
 namespace clip {
 
-constexpr int kTile = 16384;  // elements per tile
+constexpr int kTile = 8192;  // elements per tile
 constexpr int kThreads = 256;
-constexpr int kFinalThreads = 1024;
+constexpr int64_t kMaxRuns = 4096;       // cl_norm workgroups per slice
+constexpr int64_t kTileCost = kTile;     // what a tile costs besides its elements, in elements
+// The norm pass leaves the last kKeepBytes it reads in the 256 MB memory-side cache
+// (ordinary loads; the rest is read with non-temporal ones, which run at 6.9 instead of
+// 6.1 TB/s), and the second pass goes backwards and finds them there.  Against no such
+// part: AdamW on a 45 MB update 65.3 instead of 70.2 us, clipping 715 MB 327 instead of
+// 332 us, 1.6 GB 732 instead of 740 us.  0, 64, 128, 160, 192, 224, 256 MB tried.
+constexpr int64_t kKeepBytes = int64_t(224) << 20;
+constexpr int64_t kMaxTiles = 0x1fffff;  // tiles * (kTile / 4) threads fit a launch's 32 bits
 
 struct ClTile {
   int64_t begin;   // element offset of the tile in a slice
@@ -41,20 +52,27 @@ struct ClLayer {
   int32_t tile0, ntiles;  // the tensor's tiles
 };
 
+struct ClRun {
+  int32_t tile0, tile1;  // tiles [tile0, tile1)
+};
+
 // The AdamW step's scalars, written by cl_final for cl_adamw.
 struct AwState {
-  float coef;
   float step_size;  // lr / (1 - beta1^t)
   float inv_sqrt;   // 1 / sqrt(1 - beta2^t)
-  int32_t skip;
+  int64_t t;
 };
 
 struct AwArgs {
   double lr, beta1, beta2;
-  int64_t* step;  // NULL: not an AdamW call
+  const int64_t* step;
   AwState* state;
-  int32_t have_norm;  // 0: no norm was taken, c = 1
-  int32_t skip_nonfinite;
+};
+
+// What cl_adamw takes besides its buffers.
+struct AwConfig {
+  float beta1, om_beta1, beta2, om_beta2, eps, decay;
+  int32_t matrices_only, skip_nonfinite;
 };
 
 enum KernelId { kNorm = 0, kFinal, kScale, kAdamw, kNumK };
@@ -69,9 +87,10 @@ struct psgd_clip_plan {
   std::vector<psgd_clip_layer_info> info;
   std::vector<psgd::clip::ClLayer> layers;
   std::vector<psgd::clip::ClTile> tiles;
+  std::vector<psgd::clip::ClRun> runs;
   int64_t worker_stride = 0, numel = 0;
-  uint64_t ws_part = 0, ws_tensor = 0, ws_coef = 0, ws_aw = 0, workspace_bytes = 0;
-  std::map<int, void*> dev;  // device copy of the layer and tile tables, per HIP device
+  uint64_t ws_tile = 0, ws_run = 0, ws_coef = 0, ws_aw = 0, workspace_bytes = 0;
+  std::map<int, void*> dev;  // device copy of the layer, tile and run tables, per HIP device
   bool timing = false;
   std::vector<psgd::PendingTiming> pending;
   std::vector<hipEvent_t> event_pool;
@@ -84,47 +103,39 @@ namespace {
 
 // ------------------------------------------------------------------ device helpers
 typedef float v4f __attribute__((ext_vector_type(4)));
-typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+typedef float v8f __attribute__((ext_vector_type(8)));
 typedef __bf16 v4b __attribute__((ext_vector_type(4)));
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 
-__device__ __forceinline__ v4f load4(const float* p) {
-  return __builtin_nontemporal_load(reinterpret_cast<const v4f*>(p));
+// Vectors of NE elements in memory and in registers (always float32 there).  bfloat16
+// widens exactly and is rounded to nearest even by the hardware conversion, which keeps
+// NaN.  cl_norm and cl_scale move 16 bytes per lane: 4 float32 or 8 bfloat16 (with 4,
+// 8 bytes, scaling bfloat16 ran at 5.2 instead of 6.1 TB/s).
+template <typename T, int NE> struct Vec;
+template <> struct Vec<float, 4> { typedef v4f mem; typedef v4f reg; };
+template <> struct Vec<uint16_t, 4> { typedef v4b mem; typedef v4f reg; };
+template <> struct Vec<uint16_t, 8> { typedef v8b mem; typedef v8f reg; };
+template <typename T> constexpr int kUnit = 16 / int(sizeof(T));
+
+template <int NE, bool KEEP = false, typename T>
+__device__ __forceinline__ typename Vec<T, NE>::reg load(const T* p) {
+  const auto* q = reinterpret_cast<const typename Vec<T, NE>::mem*>(p);
+  return __builtin_convertvector(KEEP ? *q : __builtin_nontemporal_load(q), typename Vec<T, NE>::reg);
 }
 
-// Four bfloat16 values widened exactly to float32.
-__device__ __forceinline__ v4f load4(const uint16_t* p) {
-  const v2u u = __builtin_nontemporal_load(reinterpret_cast<const v2u*>(p));
-  v4f r;
-  r.x = __uint_as_float(u.x << 16);
-  r.y = __uint_as_float(u.x & 0xffff0000u);
-  r.z = __uint_as_float(u.y << 16);
-  r.w = __uint_as_float(u.y & 0xffff0000u);
-  return r;
-}
-
-__device__ __forceinline__ void store4(float* p, v4f v) {
-  __builtin_nontemporal_store(v, reinterpret_cast<v4f*>(p));
-}
-
-// Rounded to nearest even (the hardware conversion; NaN stays NaN).
-__device__ __forceinline__ void store4(uint16_t* p, v4f v) {
-  const v2u u = __builtin_bit_cast(v2u, __builtin_convertvector(v, v4b));
-  __builtin_nontemporal_store(u, reinterpret_cast<v2u*>(p));
-}
-
-__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store1(uint16_t* p, float v) {
-  *p = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
-}
-
-// The first n (1..4) elements of a unit; the rest is padding or another tensor's.
-template <typename T>
-__device__ __forceinline__ void store_upto(T* p, v4f v, int n) {
-  if (n >= 4) {
-    store4(p, v);
+// The first n of NE elements (n >= 1); what follows is padding.
+template <int NE, typename T>
+__device__ __forceinline__ void store(T* p, typename Vec<T, NE>::reg v, int n) {
+  const auto m = __builtin_convertvector(v, typename Vec<T, NE>::mem);
+  if (n >= NE) {
+    __builtin_nontemporal_store(m, reinterpret_cast<typename Vec<T, NE>::mem*>(p));
     return;
   }
-  for (int j = 0; j < n; ++j) store1(p + j, v[j]);
+#pragma unroll
+  for (int j = 0; j < NE - 1; ++j) {
+    const auto x = m[j];
+    if (j < n) p[j] = __builtin_bit_cast(T, x);
+  }
 }
 
 // Partial norms.  L2: a float64 sum of squares.  MAX: the largest magnitude as its bit
@@ -172,108 +183,151 @@ __device__ __forceinline__ float clip_coef(double norm, double max_norm) {
 }
 
 // ------------------------------------------------------------------ kernels
-template <typename GT, typename N>
-__global__ __launch_bounds__(kThreads) void cl_norm(const ClTile* __restrict__ tiles, const GT* __restrict__ grads,
-                                                    typename N::acc_t* __restrict__ part, int64_t stride) {
-  __shared__ typename N::acc_t lds[kThreads / 64];
-  const ClTile t = tiles[blockIdx.x];
-  const GT* g = grads + int64_t(blockIdx.y) * stride + t.begin;
+// This thread's part of a tile's partial.
+template <typename GT, typename N, bool KEEP>
+__device__ __forceinline__ typename N::acc_t tile_sum(const GT* __restrict__ g, int len) {
+  constexpr int NE = kUnit<GT>;
+  constexpr int STEP = kThreads * NE;
   typename N::acc_t acc = N::zero();
+  const int whole = len / STEP * STEP;
+  int e = int(threadIdx.x) * NE;
 #pragma unroll 4
-  for (int e = int(threadIdx.x) * 4; e < t.len; e += kThreads * 4) {
-    const v4f v = load4(g + e);  // a tensor's padding reaches the next multiple of 64 elements
+  for (; e < whole; e += STEP) {
+    const auto v = load<NE, KEEP>(g + e);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (e + j < t.len) N::take(acc, v[j]);
+    for (int j = 0; j < NE; ++j) N::take(acc, v[j]);
   }
-  acc = block_join<N>(acc, lds);
-  if (threadIdx.x == 0) part[int64_t(blockIdx.y) * gridDim.x + blockIdx.x] = acc;
+  if (e < len) {
+    const auto v = load<NE, KEEP>(g + e);  // a tensor's padding reaches the next multiple of 64 elements
+#pragma unroll
+    for (int j = 0; j < NE; ++j)
+      if (e + j < len) N::take(acc, v[j]);
+  }
+  return acc;
 }
 
-template <typename N>
-__global__ __launch_bounds__(kFinalThreads) void cl_final(const ClLayer* __restrict__ layers, int n_layers, int n_tiles,
-                                                          const typename N::acc_t* __restrict__ part,
-                                                          double max_norm, float* __restrict__ norms,
-                                                          float* __restrict__ tensor_norms, float* __restrict__ coefs,
-                                                          float* __restrict__ ws_coef, AwArgs aw) {
-  __shared__ typename N::acc_t lds[kFinalThreads / 64];
-  const int slice = blockIdx.x;
-  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-  double norm = 0.0;
-  float c = 1.0f;
-  if (aw.step == nullptr || aw.have_norm) {
-    typename N::acc_t acc = N::zero();
-    for (int l = wid; l < n_layers; l += kFinalThreads / 64) {
-      const ClLayer L = layers[l];
-      const typename N::acc_t* p = part + int64_t(slice) * n_tiles + L.tile0;
-      typename N::acc_t a = N::zero();
-      for (int i = lane; i < L.ntiles; i += 64) a = N::join(a, p[i]);
-      a = wave_join<N>(a);
-      if (lane == 0) {
-        if (tensor_norms != nullptr) tensor_norms[int64_t(slice) * n_layers + l] = float(N::norm(a));
-        acc = N::join(acc, a);
-      }
+// A workgroup reads one run of one slice (grid.y).  Its partial goes to `part_run`, each
+// tile's to `part_tile` if tensor norms are wanted.
+template <typename GT, typename N>
+__global__ __launch_bounds__(kThreads) void cl_norm(const ClTile* __restrict__ tiles, const ClRun* __restrict__ runs,
+                                                    int n_tiles, const GT* __restrict__ grads, int64_t stride,
+                                                    int64_t keep_from, typename N::acc_t* __restrict__ part_tile,
+                                                    typename N::acc_t* __restrict__ part_run) {
+  typedef typename N::acc_t acc_t;
+  __shared__ acc_t lds[kThreads / 64];
+  const int64_t slice = blockIdx.y;
+  const ClRun r = runs[blockIdx.x];
+  acc_t run = N::zero();
+  for (int i = r.tile0; i < r.tile1; ++i) {
+    const ClTile t = tiles[i];
+    const GT* g = grads + slice * stride + t.begin;
+    const acc_t acc = slice * stride + t.begin >= keep_from ? tile_sum<GT, N, true>(g, t.len)
+                                                            : tile_sum<GT, N, false>(g, t.len);
+    run = N::join(run, acc);
+    if (part_tile != nullptr && r.tile1 - r.tile0 > 1) {
+      const acc_t tile = block_join<N>(acc, lds);
+      if (threadIdx.x == 0) part_tile[slice * n_tiles + i] = tile;
     }
-    acc = block_join<N>(acc, lds);
-    norm = N::norm(acc);
-    c = clip_coef(norm, max_norm);
   }
-  if (threadIdx.x != 0) return;
-  if (norms != nullptr) norms[slice] = float(norm);
-  if (coefs != nullptr) coefs[slice] = c;
-  ws_coef[slice] = c;
-  if (aw.step != nullptr) {
+  run = block_join<N>(run, lds);
+  if (threadIdx.x == 0) {
+    part_run[slice * gridDim.x + blockIdx.x] = run;
+    if (part_tile != nullptr && r.tile1 - r.tile0 == 1) part_tile[slice * n_tiles + r.tile0] = run;
+  }
+}
+
+// Joined value of p[0..n) in every thread of the workgroup.
+template <typename N>
+__device__ __forceinline__ typename N::acc_t join_all(const typename N::acc_t* __restrict__ p, int n,
+                                                      typename N::acc_t* lds) {
+  typename N::acc_t acc = N::zero();
+#pragma unroll 8
+  for (int i = int(threadIdx.x); i < n; i += kThreads) acc = N::join(acc, p[i]);
+  return block_join<N>(acc, lds);
+}
+
+// grid.x: workgroup 0 of a slice (grid.y) takes its norm and coefficient; the next n_layers
+// ones a tensor's norm each (tensor_norms given); the last one the AdamW step's scalars
+// (aw.state given).
+template <typename N>
+__global__ __launch_bounds__(kThreads) void cl_final(const ClLayer* __restrict__ layers, int n_layers, int n_tiles,
+                                                     int n_runs, const typename N::acc_t* __restrict__ part_tile,
+                                                     const typename N::acc_t* __restrict__ part_run, double max_norm,
+                                                     float* __restrict__ norms, float* __restrict__ tensor_norms,
+                                                     float* __restrict__ coefs, float* __restrict__ ws_coef,
+                                                     AwArgs aw) {
+  __shared__ typename N::acc_t lds[kThreads / 64];
+  const int64_t slice = blockIdx.y;
+  const int l = int(blockIdx.x) - 1;
+  if (l < 0) {
+    if (part_run == nullptr) return;
+    const double norm = N::norm(join_all<N>(part_run + slice * n_runs, n_runs, lds));
+    if (threadIdx.x != 0) return;
+    const float c = clip_coef(norm, max_norm);
+    norms[slice] = float(norm);
+    ws_coef[slice] = c;
+    if (coefs != nullptr) coefs[slice] = c;
+  } else if (tensor_norms != nullptr && l < n_layers) {
+    const ClLayer L = layers[l];
+    const double norm = N::norm(join_all<N>(part_tile + slice * n_tiles + L.tile0, L.ntiles, lds));
+    if (threadIdx.x == 0) tensor_norms[slice * n_layers + l] = float(norm);
+  } else if (threadIdx.x == 0) {
     AwState s;
-    s.coef = c;
-    s.skip = aw.skip_nonfinite && !isfinite(float(norm)) ? 1 : 0;
-    const int64_t t = *aw.step + 1;
-    s.step_size = float(aw.lr / (1.0 - pow(aw.beta1, double(t))));
-    s.inv_sqrt = float(1.0 / sqrt(1.0 - pow(aw.beta2, double(t))));
+    s.t = *aw.step + 1;
+    s.step_size = float(aw.lr / (1.0 - pow(aw.beta1, double(s.t))));
+    s.inv_sqrt = float(1.0 / sqrt(1.0 - pow(aw.beta2, double(s.t))));
     *aw.state = s;
-    if (!s.skip) *aw.step = t;
   }
 }
 
 template <typename GT>
 __global__ __launch_bounds__(kThreads) void cl_scale(const ClTile* __restrict__ tiles, const GT* grads, GT* out,
-                                                     const float* __restrict__ ws_coef, int64_t stride) {
-  const float c = ws_coef[blockIdx.y];
+                                                     int64_t stride, const float* __restrict__ ws_coef) {
+  constexpr int NE = kUnit<GT>, parts = kTile / (kThreads * NE);
+  const int64_t slice = gridDim.y - 1 - blockIdx.y;  // last read, first rescaled
+  const unsigned at_part = gridDim.x - 1 - blockIdx.x;
+  const float c = ws_coef[slice];
   if (c == 1.0f && grads == out) return;
-  const ClTile t = tiles[blockIdx.x];
-  const int64_t base = int64_t(blockIdx.y) * stride + t.begin;
-#pragma unroll 4
-  for (int e = int(threadIdx.x) * 4; e < t.len; e += kThreads * 4)
-    store_upto(out + base + e, load4(grads + base + e) * c, t.len - e);
+  const ClTile t = tiles[at_part / parts];
+  const int e = (int(at_part % parts) * kThreads + int(threadIdx.x)) * NE;
+  if (e >= t.len) return;
+  const int64_t at = slice * stride + t.begin + e;
+  store<NE>(out + at, load<NE>(grads + at) * c, t.len - e);
 }
 
+// `norm` and `ws_coef` are NULL without clipping (c = 1).
 template <typename GT>
 __global__ __launch_bounds__(kThreads) void cl_adamw(const ClTile* __restrict__ tiles, const GT* __restrict__ update,
                                                      float* __restrict__ params, float* __restrict__ exp_avg,
                                                      float* __restrict__ exp_avg_sq, uint16_t* __restrict__ copy,
-                                                     const AwState* __restrict__ state, float beta1, float om_beta1,
-                                                     float beta2, float om_beta2, float eps, float decay,
-                                                     int matrices_only) {
+                                                     const AwState* __restrict__ state, AwConfig cf,
+                                                     const float* __restrict__ norm,
+                                                     const float* __restrict__ ws_coef, int64_t* __restrict__ step) {
+  constexpr int parts = kTile / (kThreads * 4);
   const AwState s = *state;
-  if (s.skip) return;
-  const ClTile t = tiles[blockIdx.x];
-  const float d = matrices_only && !t.matrix ? 0.0f : decay;
-  for (int e = int(threadIdx.x) * 4; e < t.len; e += kThreads * 4) {
-    const int64_t at = t.begin + e;
-    const v4f g = load4(update + at) * s.coef;
-    v4f x = load4(params + at), m = load4(exp_avg + at), v = load4(exp_avg_sq + at);
-    m = beta1 * m + om_beta1 * g;
-    v = beta2 * v + om_beta2 * (g * g);
+  const float c = ws_coef != nullptr ? *ws_coef : 1.0f;
+  if (cf.skip_nonfinite && !isfinite(*norm)) return;
+  if (blockIdx.x == 0 && threadIdx.x == 0) step[0] = s.t;
+  const unsigned at_part = gridDim.x - 1 - blockIdx.x;  // last read, first used
+  const ClTile t = tiles[at_part / parts];
+  const float d = cf.matrices_only && !t.matrix ? 0.0f : cf.decay;
+  const int e = (int(at_part % parts) * kThreads + int(threadIdx.x)) * 4;
+  if (e >= t.len) return;
+  const int64_t at = t.begin + e;
+  const v4f g = load<4>(update + at) * c;
+  v4f x = load<4>(params + at), m = load<4>(exp_avg + at), v = load<4>(exp_avg_sq + at);
+  m = cf.beta1 * m + cf.om_beta1 * g;
+  v = cf.beta2 * v + cf.om_beta2 * (g * g);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float den = sqrtf(v[j]) * s.inv_sqrt + eps;
-      x[j] = fmaf(-d, x[j], x[j]) - s.step_size * (m[j] / den);
-    }
-    const int n = t.len - e;
-    store_upto(params + at, x, n);
-    store_upto(exp_avg + at, m, n);
-    store_upto(exp_avg_sq + at, v, n);
-    if (copy != nullptr) store_upto(copy + at, x, n);
+  for (int j = 0; j < 4; ++j) {
+    const float den = sqrtf(v[j]) * s.inv_sqrt + cf.eps;
+    x[j] = fmaf(-d, x[j], x[j]) - s.step_size * (m[j] / den);
   }
+  const int n = t.len - e;
+  store<4>(params + at, x, n);
+  store<4>(exp_avg + at, m, n);
+  store<4>(exp_avg_sq + at, v, n);
+  if (copy != nullptr) store<4>(copy + at, x, n);
 }
 
 // ------------------------------------------------------------------ host helpers
@@ -298,6 +352,7 @@ uint64_t a256(uint64_t x) { return (x + 255) / 256 * 256; }
 struct DevTables {
   const ClLayer* layers;
   const ClTile* tiles;
+  const ClRun* runs;
 };
 
 psgd_status device_tables(const char* fn, psgd_clip_plan* plan, hipStream_t st, DevTables* out) {
@@ -306,6 +361,7 @@ psgd_status device_tables(const char* fn, psgd_clip_plan* plan, hipStream_t st, 
   if (e != hipSuccess) return hip_fail("hipGetDevice", e);
   const uint64_t bl = a256(plan->layers.size() * sizeof(ClLayer));
   const uint64_t bt = a256(plan->tiles.size() * sizeof(ClTile));
+  const uint64_t br = plan->runs.size() * sizeof(ClRun);
   auto it = plan->dev.find(dev);
   if (it == plan->dev.end()) {
     hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
@@ -316,7 +372,7 @@ psgd_status device_tables(const char* fn, psgd_clip_plan* plan, hipStream_t st, 
                                             "call of the plan on this device");
     it = plan->dev.emplace(dev, nullptr).first;
     void* base = nullptr;
-    e = hipMalloc(&base, bl + bt);
+    e = hipMalloc(&base, bl + bt + br);
     if (e != hipSuccess) {
       plan->dev.erase(it);
       return fail(PSGD_ERR_NO_MEMORY, std::string("hipMalloc of the plan's device tables: ") + hipGetErrorString(e));
@@ -325,16 +381,18 @@ psgd_status device_tables(const char* fn, psgd_clip_plan* plan, hipStream_t st, 
     e = hipMemcpy(b, plan->layers.data(), plan->layers.size() * sizeof(ClLayer), hipMemcpyHostToDevice);
     if (e == hipSuccess)
       e = hipMemcpy(b + bl, plan->tiles.data(), plan->tiles.size() * sizeof(ClTile), hipMemcpyHostToDevice);
+    if (e == hipSuccess) e = hipMemcpy(b + bl + bt, plan->runs.data(), br, hipMemcpyHostToDevice);
     if (e != hipSuccess) {
       (void)hipFree(base);
       plan->dev.erase(it);
-      return hip_fail("hipMemcpy of the plan's device tables", e);
+      return hip_fail("upload of the plan's device tables", e);
     }
     it->second = base;
   }
   char* b = static_cast<char*>(it->second);
   out->layers = reinterpret_cast<const ClLayer*>(b);
   out->tiles = reinterpret_cast<const ClTile*>(b + bl);
+  out->runs = reinterpret_cast<const ClRun*>(b + bl + bt);
   return PSGD_OK;
 }
 
@@ -417,34 +475,65 @@ psgd_status check_kind(const char* fn, int kind) {
   return fail(PSGD_ERR_UNSUPPORTED, std::string(fn) + ": unknown norm kind");
 }
 
-// The norm of every slice, and what cl_final derives from it.
-template <typename N>
-psgd_status enqueue_norm(psgd_clip_plan* plan, const DevTables& dt, const void* grads, double max_norm, float* norms,
-                         float* tensor_norms, float* coefs, char* ws, const AwArgs& aw, hipStream_t st) {
+// What a call's norm is taken for.
+struct NormArgs {
+  const void* grads;
+  double max_norm;
+  float *norms, *tensor_norms, *coefs;
+  AwArgs aw;
+  bool again;  // the same call reads the gradients once more
+};
+
+// The norm of every slice, and what else cl_final derives.  N = L2 or Max.
+template <typename GT, typename N>
+psgd_status enqueue_norm_of(psgd_clip_plan* plan, const DevTables& dt, const NormArgs& a, char* ws, hipStream_t st) {
   typedef typename N::acc_t acc_t;
-  acc_t* part = reinterpret_cast<acc_t*>(ws + plan->ws_part);
-  const int n_tiles = int(plan->tiles.size());
-  const dim3 grid(static_cast<unsigned>(n_tiles), static_cast<unsigned>(plan->n_slices));
-  psgd_status s = PSGD_OK;
-  if (aw.step == nullptr || aw.have_norm) {
-    if (plan->dtype == PSGD_BF16)
-      s = launch(plan, kNorm, cl_norm<uint16_t, N>, grid, dim3(kThreads), st, dt.tiles,
-                 static_cast<const uint16_t*>(grads), part, plan->worker_stride);
-    else
-      s = launch(plan, kNorm, cl_norm<float, N>, grid, dim3(kThreads), st, dt.tiles, static_cast<const float*>(grads),
-                 part, plan->worker_stride);
-    if (s != PSGD_OK) return s;
-  }
-  return launch(plan, kFinal, cl_final<N>, dim3(static_cast<unsigned>(plan->n_slices)), dim3(kFinalThreads), st,
-                dt.layers, int(plan->layers.size()), n_tiles, static_cast<const acc_t*>(part), max_norm, norms,
-                tensor_norms, coefs, reinterpret_cast<float*>(ws + plan->ws_coef), aw);
+  const int n_layers = int(plan->layers.size()), n_tiles = int(plan->tiles.size()), n_runs = int(plan->runs.size());
+  const unsigned S = static_cast<unsigned>(plan->n_slices);
+  acc_t* part_tile = a.tensor_norms != nullptr ? reinterpret_cast<acc_t*>(ws + plan->ws_tile) : nullptr;
+  acc_t* part_run = reinterpret_cast<acc_t*>(ws + plan->ws_run);
+  const int64_t total = int64_t(plan->n_slices) * plan->worker_stride;
+  const int64_t keep_from = a.again ? total - kKeepBytes / int64_t(sizeof(GT)) : total;
+  const psgd_status s = launch(plan, kNorm, cl_norm<GT, N>, dim3(static_cast<unsigned>(n_runs), S), dim3(kThreads), st,
+                               dt.tiles, dt.runs, n_tiles, static_cast<const GT*>(a.grads), plan->worker_stride,
+                               keep_from, part_tile, part_run);
+  if (s != PSGD_OK) return s;
+  const unsigned blocks = 1u + (part_tile != nullptr ? unsigned(n_layers) : 0u) + (a.aw.state != nullptr ? 1u : 0u);
+  return launch(plan, kFinal, cl_final<N>, dim3(blocks, S), dim3(kThreads), st, dt.layers, n_layers, n_tiles, n_runs,
+                static_cast<const acc_t*>(part_tile), static_cast<const acc_t*>(part_run), a.max_norm, a.norms,
+                a.tensor_norms, a.coefs, reinterpret_cast<float*>(ws + plan->ws_coef), a.aw);
 }
 
-psgd_status enqueue_norm(psgd_clip_plan* plan, int kind, const DevTables& dt, const void* grads, double max_norm,
-                         float* norms, float* tensor_norms, float* coefs, char* ws, const AwArgs& aw, hipStream_t st) {
+psgd_status enqueue_norm(psgd_clip_plan* plan, int kind, const DevTables& dt, const NormArgs& a, char* ws,
+                         hipStream_t st) {
+  const bool bf = plan->dtype == PSGD_BF16;
   if (kind == PSGD_NORM_MAX)
-    return enqueue_norm<Max>(plan, dt, grads, max_norm, norms, tensor_norms, coefs, ws, aw, st);
-  return enqueue_norm<L2>(plan, dt, grads, max_norm, norms, tensor_norms, coefs, ws, aw, st);
+    return bf ? enqueue_norm_of<uint16_t, Max>(plan, dt, a, ws, st) : enqueue_norm_of<float, Max>(plan, dt, a, ws, st);
+  return bf ? enqueue_norm_of<uint16_t, L2>(plan, dt, a, ws, st) : enqueue_norm_of<float, L2>(plan, dt, a, ws, st);
+}
+
+template <typename GT>
+psgd_status enqueue_scale(psgd_clip_plan* plan, const DevTables& dt, const void* grads, void* out, const char* ws,
+                          hipStream_t st) {
+  const unsigned parts = kTile / (kThreads * kUnit<GT>);
+  const dim3 grid(static_cast<unsigned>(plan->tiles.size()) * parts, static_cast<unsigned>(plan->n_slices));
+  return launch(plan, kScale, cl_scale<GT>, grid, dim3(kThreads), st, dt.tiles, static_cast<const GT*>(grads),
+                static_cast<GT*>(out), plan->worker_stride, reinterpret_cast<const float*>(ws + plan->ws_coef));
+}
+
+struct AwBuffers {
+  const void* update;
+  float *params, *exp_avg, *exp_avg_sq;
+  uint16_t* copy;
+  int64_t* step;
+};
+
+template <typename GT>
+psgd_status enqueue_adamw(psgd_clip_plan* plan, const DevTables& dt, const AwBuffers& b, const AwState* state,
+                          const AwConfig& cf, const float* norm, const float* coef, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(plan->tiles.size()) * (kTile / (kThreads * 4)));
+  return launch(plan, kAdamw, cl_adamw<GT>, grid, dim3(kThreads), st, dt.tiles, static_cast<const GT*>(b.update),
+                b.params, b.exp_avg, b.exp_avg_sq, b.copy, state, cf, norm, coef, b.step);
 }
 
 }  // namespace
@@ -490,7 +579,7 @@ extern "C" psgd_status psgd_clip_plan_create(const psgd_layer* layers, int32_t n
         t.matrix = rows > 1 && cols > 1 ? 1 : 0;
         plan->tiles.push_back(t);
       }
-      if (plan->tiles.size() > size_t(0xffffffu)) {  // tiles * kThreads fits a launch's 32 bits
+      if (int64_t(plan->tiles.size()) > kMaxTiles) {
         delete plan;
         return fail(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_create: too many tiles");
       }
@@ -499,9 +588,26 @@ extern "C" psgd_status psgd_clip_plan_create(const psgd_layer* layers, int32_t n
       off = (off + numel + kAlignElems - 1) / kAlignElems * kAlignElems;
     }
     plan->worker_stride = off;
+    // Runs of about equal cost, so that the workgroups of a launch end together.
+    const int64_t n_tiles = int64_t(plan->tiles.size());
+    const int64_t n_runs = std::min(n_tiles, kMaxRuns);
+    int64_t cost = 0, done = 0;
+    for (const ClTile& t : plan->tiles) cost += t.len + kTileCost;
+    ClRun run{0, 0};
+    for (int64_t i = 0; i < n_tiles; ++i) {
+      done += plan->tiles[size_t(i)].len + kTileCost;
+      run.tile1 = int32_t(i + 1);
+      const int64_t made = int64_t(plan->runs.size()) + 1;
+      if (i + 1 == n_tiles || (made < n_runs && done * n_runs >= cost * made)) {
+        plan->runs.push_back(run);
+        run.tile0 = run.tile1;
+      }
+    }
     uint64_t ws = 0;
-    plan->ws_part = ws;  // one partial per tile and slice
-    ws = a256(ws + uint64_t(n_slices) * plan->tiles.size() * sizeof(double));
+    plan->ws_tile = ws;  // one partial per tile and slice
+    ws = a256(ws + uint64_t(n_slices) * uint64_t(n_tiles) * sizeof(double));
+    plan->ws_run = ws;  // one per run and slice
+    ws = a256(ws + uint64_t(n_slices) * plan->runs.size() * sizeof(double));
     plan->ws_coef = ws;
     ws = a256(ws + uint64_t(n_slices) * sizeof(float));
     plan->ws_aw = ws;
@@ -630,8 +736,8 @@ extern "C" psgd_status psgd_grad_norm(psgd_clip_plan* plan, const void* grads, p
     const hipStream_t st = static_cast<hipStream_t>(stream);
     DevTables dt{};
     if ((s = device_tables(fn, plan, st, &dt)) != PSGD_OK) return s;
-    return enqueue_norm(plan, kind, dt, grads, double(INFINITY), norms, tensor_norms, nullptr,
-                        static_cast<char*>(workspace), AwArgs{}, st);
+    const NormArgs a{grads, double(INFINITY), norms, tensor_norms, nullptr, AwArgs{}, false};
+    return enqueue_norm(plan, kind, dt, a, static_cast<char*>(workspace), st);
   } catch (...) {
     return no_memory();
   }
@@ -659,15 +765,10 @@ extern "C" psgd_status psgd_grad_clip(psgd_clip_plan* plan, const void* grads, v
     DevTables dt{};
     if ((s = device_tables(fn, plan, st, &dt)) != PSGD_OK) return s;
     char* ws = static_cast<char*>(workspace);
-    if ((s = enqueue_norm(plan, kind, dt, grads, double(max_norm), norms, nullptr, coefs, ws, AwArgs{}, st)) != PSGD_OK)
-      return s;
-    const dim3 grid(static_cast<unsigned>(plan->tiles.size()), static_cast<unsigned>(S));
-    const float* c = reinterpret_cast<const float*>(ws + plan->ws_coef);
-    if (plan->dtype == PSGD_BF16)
-      return launch(plan, kScale, cl_scale<uint16_t>, grid, dim3(kThreads), st, dt.tiles,
-                    static_cast<const uint16_t*>(grads), static_cast<uint16_t*>(out), c, plan->worker_stride);
-    return launch(plan, kScale, cl_scale<float>, grid, dim3(kThreads), st, dt.tiles, static_cast<const float*>(grads),
-                  static_cast<float*>(out), c, plan->worker_stride);
+    const NormArgs a{grads, double(max_norm), norms, nullptr, coefs, AwArgs{}, true};
+    if ((s = enqueue_norm(plan, kind, dt, a, ws, st)) != PSGD_OK) return s;
+    return plan->dtype == PSGD_BF16 ? enqueue_scale<uint16_t>(plan, dt, grads, out, ws, st)
+                                    : enqueue_scale<float>(plan, dt, grads, out, ws, st);
   } catch (...) {
     return no_memory();
   }
@@ -716,29 +817,27 @@ extern "C" psgd_status psgd_adamw_apply(psgd_clip_plan* plan, const psgd_adamw_c
     DevTables dt{};
     if ((s = device_tables(fn, plan, st, &dt)) != PSGD_OK) return s;
     char* ws = static_cast<char*>(workspace);
-    AwArgs aw{};
-    aw.lr = cf.lr;
-    aw.beta1 = cf.beta1;
-    aw.beta2 = cf.beta2;
-    aw.step = step;
-    aw.state = reinterpret_cast<AwState*>(ws + plan->ws_aw);
-    aw.have_norm = clipped ? 1 : 0;
-    aw.skip_nonfinite = (cf.flags & PSGD_ADAMW_SKIP_NONFINITE) ? 1 : 0;
-    if ((s = enqueue_norm(plan, clipped ? cf.norm_kind : int(PSGD_NORM_L2), dt, update, cf.max_norm, norm, nullptr,
-                          nullptr, ws, aw, st)) != PSGD_OK)
-      return s;
-    const dim3 grid(static_cast<unsigned>(plan->tiles.size()));
-    const int mo = (cf.flags & PSGD_ADAMW_DECAY_MATRICES_ONLY) ? 1 : 0;
-    const float b1 = float(cf.beta1), o1 = float(1.0 - cf.beta1), b2 = float(cf.beta2), o2 = float(1.0 - cf.beta2);
-    const float eps = float(cf.eps), decay = float(cf.lr * cf.weight_decay);
-    uint16_t* copy = static_cast<uint16_t*>(params_bf16);
-    const AwState* state = aw.state;
-    if (plan->dtype == PSGD_BF16)
-      return launch(plan, kAdamw, cl_adamw<uint16_t>, grid, dim3(kThreads), st, dt.tiles,
-                    static_cast<const uint16_t*>(update), params, exp_avg, exp_avg_sq, copy, state, b1, o1, b2, o2,
-                    eps, decay, mo);
-    return launch(plan, kAdamw, cl_adamw<float>, grid, dim3(kThreads), st, dt.tiles, static_cast<const float*>(update),
-                  params, exp_avg, exp_avg_sq, copy, state, b1, o1, b2, o2, eps, decay, mo);
+    const AwArgs aw{cf.lr, cf.beta1, cf.beta2, step, reinterpret_cast<AwState*>(ws + plan->ws_aw)};
+    const AwConfig ac{float(cf.beta1), float(1.0 - cf.beta1), float(cf.beta2), float(1.0 - cf.beta2),
+                      float(cf.eps), float(cf.lr * cf.weight_decay),
+                      (cf.flags & PSGD_ADAMW_DECAY_MATRICES_ONLY) ? 1 : 0,
+                      (cf.flags & PSGD_ADAMW_SKIP_NONFINITE) ? 1 : 0};
+    const AwBuffers b{update, params, exp_avg, exp_avg_sq, static_cast<uint16_t*>(params_bf16), step};
+    const float* coef = nullptr;
+    if (clipped) {
+      const NormArgs a{update, cf.max_norm, norm, nullptr, nullptr, aw, true};
+      s = enqueue_norm(plan, cf.norm_kind, dt, a, ws, st);
+      coef = reinterpret_cast<const float*>(ws + plan->ws_coef);
+    } else {
+      // only the step's scalars
+      s = launch(plan, kFinal, cl_final<L2>, dim3(2), dim3(kThreads), st, dt.layers, 0, 0, 0,
+                 static_cast<const double*>(nullptr), static_cast<const double*>(nullptr), 0.0,
+                 static_cast<float*>(nullptr), static_cast<float*>(nullptr), static_cast<float*>(nullptr),
+                 static_cast<float*>(nullptr), aw);
+    }
+    if (s != PSGD_OK) return s;
+    return plan->dtype == PSGD_BF16 ? enqueue_adamw<uint16_t>(plan, dt, b, aw.state, ac, norm, coef, st)
+                                    : enqueue_adamw<float>(plan, dt, b, aw.state, ac, norm, coef, st);
   } catch (...) {
     return no_memory();
   }
