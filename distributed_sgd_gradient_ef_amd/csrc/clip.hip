@@ -10,6 +10,10 @@
 //              if asked, and for AdamW the step's scalars
 //   cl_scale   per (part of a tile, slice): out = c * g
 //   cl_adamw   per part of a tile: the weight update
+// Slices of a moderate size leave cl_final out: cl_scale and cl_adamw join the partials
+// themselves (FOLD).  Small ones take a single launch, a workgroup per slice:
+//   cl_small        norms, and clipping
+//   cl_small_adamw  the AdamW step
 //
 // No kernel waits for another workgroup, and no state is kept between calls.
 
@@ -19,6 +23,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
+#include <cstring>
 #include <map>
 #include <new>
 #include <string>
@@ -40,6 +45,21 @@ constexpr int64_t kTileCost = kTile;     // what a tile costs besides its elemen
 // part: AdamW on a 45 MB update 65.3 instead of 70.2 us, clipping 715 MB 327 instead of
 // 332 us, 1.6 GB 732 instead of 740 us.  0, 64, 128, 160, 192, 224, 256 MB tried.
 constexpr int64_t kKeepBytes = int64_t(224) << 20;
+// Joining the partials in cl_scale / cl_adamw instead of a launch of cl_final (us a call in
+// a graph, clipping float32): 1 slice of 2M elements 9.4 against 9.6, of 4M 16.1 against
+// 12.7; 8 slices of 0.5M 12.0 against 12.8, of 1M 22.3 against 21.3.  Called one by one,
+// the launch saved is worth 2 us more.
+constexpr int64_t kFoldRuns = 256;   // per slice
+constexpr int64_t kFoldTotal = 512;  // all slices together
+// A single launch with a workgroup per slice, for plans of at most kMaxItems items, up to
+// kSmallNorm (norms, clipping) or kSmallAdamw elements per slice.  Against the two launches
+// above (us a call in a graph): norm of 16384 4.4 against 5.2, of 32768 6.0 against 5.5;
+// clip 5.8 / 5.9 and 8.3 / 5.8; AdamW of 4096 6.3 / 7.2, of 8192 7.6 / 7.2, of 16384
+// 10.5 / 7.6.  Called one by one the smaller number of launches is worth 3.5 us.
+constexpr int kItem = 512;      // elements per item
+constexpr int kMaxItems = 128;
+constexpr int kSmallThreads = 1024;
+constexpr int64_t kSmallNorm = 16384, kSmallAdamw = 8192;
 constexpr int64_t kMaxTiles = 0x1fffff;  // tiles * (kTile / 4) threads fit a launch's 32 bits
 
 struct ClTile {
@@ -56,7 +76,14 @@ struct ClRun {
   int32_t tile0, tile1;  // tiles [tile0, tile1)
 };
 
-// The AdamW step's scalars, written by cl_final for cl_adamw.
+// A part of a small plan's tensor, for one wave.
+struct ClItem {
+  int32_t begin, len;  // elements of the slice
+  int32_t matrix;
+  int32_t pad;
+};
+
+// The AdamW step's scalars, written by cl_final or cl_norm for cl_adamw.
 struct AwState {
   float step_size;  // lr / (1 - beta1^t)
   float inv_sqrt;   // 1 / sqrt(1 - beta2^t)
@@ -75,8 +102,8 @@ struct AwConfig {
   int32_t matrices_only, skip_nonfinite;
 };
 
-enum KernelId { kNorm = 0, kFinal, kScale, kAdamw, kNumK };
-const char* const kNames[kNumK] = {"cl_norm", "cl_final", "cl_scale", "cl_adamw"};
+enum KernelId { kNorm = 0, kFinal, kScale, kAdamw, kSmall, kSmallAw, kNumK };
+const char* const kNames[kNumK] = {"cl_norm", "cl_final", "cl_scale", "cl_adamw", "cl_small", "cl_small_adamw"};
 
 }  // namespace clip
 }  // namespace psgd
@@ -88,6 +115,8 @@ struct psgd_clip_plan {
   std::vector<psgd::clip::ClLayer> layers;
   std::vector<psgd::clip::ClTile> tiles;
   std::vector<psgd::clip::ClRun> runs;
+  std::vector<psgd::clip::ClItem> items;        // of a small plan; empty otherwise
+  std::vector<psgd::clip::ClLayer> item_layers;  // each tensor's items
   int64_t worker_stride = 0, numel = 0;
   uint64_t ws_tile = 0, ws_run = 0, ws_coef = 0, ws_aw = 0, workspace_bytes = 0;
   std::map<int, void*> dev;  // device copy of the layer, tile and run tables, per HIP device
@@ -182,6 +211,33 @@ __device__ __forceinline__ float clip_coef(double norm, double max_norm) {
   return norm <= max_norm ? 1.0f : float(max_norm / norm);
 }
 
+__device__ __forceinline__ AwState step_scalars(const AwArgs& aw) {
+  AwState s;
+  s.t = *aw.step + 1;
+  s.step_size = float(aw.lr / (1.0 - pow(aw.beta1, double(s.t))));
+  s.inv_sqrt = float(1.0 / sqrt(1.0 - pow(aw.beta2, double(s.t))));
+  return s;
+}
+
+// Four elements' AdamW update: the new x, m and v in place of the old.
+__device__ __forceinline__ void adamw4(v4f g, v4f& x, v4f& m, v4f& v, const AwState& s, const AwConfig& cf, float decay) {
+  m = cf.beta1 * m + cf.om_beta1 * g;
+  v = cf.beta2 * v + cf.om_beta2 * (g * g);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float den = sqrtf(v[j]) * s.inv_sqrt + cf.eps;
+    x[j] = fmaf(-decay, x[j], x[j]) - s.step_size * (m[j] / den);
+  }
+}
+
+// A slice's norm from its runs' partials, by one wave.
+template <typename N>
+__device__ __forceinline__ double fold_norm(const typename N::acc_t* __restrict__ part_run, int n_runs) {
+  typename N::acc_t acc = N::zero();
+  for (int i = int(threadIdx.x & 63); i < n_runs; i += 64) acc = N::join(acc, part_run[i]);
+  return N::norm(wave_join<N>(acc));
+}
+
 // ------------------------------------------------------------------ kernels
 // This thread's part of a tile's partial.
 template <typename GT, typename N, bool KEEP>
@@ -212,11 +268,12 @@ template <typename GT, typename N>
 __global__ __launch_bounds__(kThreads) void cl_norm(const ClTile* __restrict__ tiles, const ClRun* __restrict__ runs,
                                                     int n_tiles, const GT* __restrict__ grads, int64_t stride,
                                                     int64_t keep_from, typename N::acc_t* __restrict__ part_tile,
-                                                    typename N::acc_t* __restrict__ part_run) {
+                                                    typename N::acc_t* __restrict__ part_run, AwArgs aw) {
   typedef typename N::acc_t acc_t;
   __shared__ acc_t lds[kThreads / 64];
   const int64_t slice = blockIdx.y;
   const ClRun r = runs[blockIdx.x];
+  if (aw.state != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *aw.state = step_scalars(aw);
   acc_t run = N::zero();
   for (int i = r.tile0; i < r.tile1; ++i) {
     const ClTile t = tiles[i];
@@ -272,21 +329,42 @@ __global__ __launch_bounds__(kThreads) void cl_final(const ClLayer* __restrict__
     const double norm = N::norm(join_all<N>(part_tile + slice * n_tiles + L.tile0, L.ntiles, lds));
     if (threadIdx.x == 0) tensor_norms[slice * n_layers + l] = float(norm);
   } else if (threadIdx.x == 0) {
-    AwState s;
-    s.t = *aw.step + 1;
-    s.step_size = float(aw.lr / (1.0 - pow(aw.beta1, double(s.t))));
-    s.inv_sqrt = float(1.0 / sqrt(1.0 - pow(aw.beta2, double(s.t))));
-    *aw.state = s;
+    *aw.state = step_scalars(aw);
   }
 }
 
-template <typename GT>
+// What cl_scale and cl_adamw take a coefficient from: cl_final's, or (FOLD) the partials.
+template <typename N>
+struct CoefArgs {
+  const float* coef;
+  const typename N::acc_t* part_run;
+  int32_t n_runs;
+  double max_norm;
+  float *norms, *coefs;  // outputs, written with FOLD only
+};
+
+// Coefficient of a slice; *norm gets its norm (FOLD).
+template <typename N, bool FOLD>
+__device__ __forceinline__ float coefficient(const CoefArgs<N>& a, int64_t slice, float* norm) {
+  if (!FOLD) return a.coef[slice];
+  const double d = fold_norm<N>(a.part_run + slice * a.n_runs, a.n_runs);
+  const float c = clip_coef(d, a.max_norm);
+  *norm = float(d);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.norms[slice] = float(d);
+    if (a.coefs != nullptr) a.coefs[slice] = c;
+  }
+  return c;
+}
+
+template <typename GT, typename N, bool FOLD>
 __global__ __launch_bounds__(kThreads) void cl_scale(const ClTile* __restrict__ tiles, const GT* grads, GT* out,
-                                                     int64_t stride, const float* __restrict__ ws_coef) {
+                                                     int64_t stride, CoefArgs<N> ca) {
   constexpr int NE = kUnit<GT>, parts = kTile / (kThreads * NE);
   const int64_t slice = gridDim.y - 1 - blockIdx.y;  // last read, first rescaled
   const unsigned at_part = gridDim.x - 1 - blockIdx.x;
-  const float c = ws_coef[slice];
+  float norm;
+  const float c = coefficient<N, FOLD>(ca, slice, &norm);
   if (c == 1.0f && grads == out) return;
   const ClTile t = tiles[at_part / parts];
   const int e = (int(at_part % parts) * kThreads + int(threadIdx.x)) * NE;
@@ -295,18 +373,22 @@ __global__ __launch_bounds__(kThreads) void cl_scale(const ClTile* __restrict__ 
   store<NE>(out + at, load<NE>(grads + at) * c, t.len - e);
 }
 
-// `norm` and `ws_coef` are NULL without clipping (c = 1).
-template <typename GT>
+// CLIP: 0 no clipping (c = 1), 1 cl_final's coefficient, 2 from the partials.
+template <typename GT, typename N, int CLIP>
 __global__ __launch_bounds__(kThreads) void cl_adamw(const ClTile* __restrict__ tiles, const GT* __restrict__ update,
                                                      float* __restrict__ params, float* __restrict__ exp_avg,
                                                      float* __restrict__ exp_avg_sq, uint16_t* __restrict__ copy,
-                                                     const AwState* __restrict__ state, AwConfig cf,
-                                                     const float* __restrict__ norm,
-                                                     const float* __restrict__ ws_coef, int64_t* __restrict__ step) {
+                                                     const AwState* __restrict__ state, AwConfig cf, CoefArgs<N> ca,
+                                                     int64_t* step) {
   constexpr int parts = kTile / (kThreads * 4);
   const AwState s = *state;
-  const float c = ws_coef != nullptr ? *ws_coef : 1.0f;
-  if (cf.skip_nonfinite && !isfinite(*norm)) return;
+  float c = 1.0f;
+  if (CLIP) {
+    float norm;
+    c = coefficient<N, CLIP == 2>(ca, 0, &norm);
+    if (CLIP == 1) norm = *ca.norms;
+    if (cf.skip_nonfinite && !isfinite(norm)) return;
+  }
   if (blockIdx.x == 0 && threadIdx.x == 0) step[0] = s.t;
   const unsigned at_part = gridDim.x - 1 - blockIdx.x;  // last read, first used
   const ClTile t = tiles[at_part / parts];
@@ -316,18 +398,125 @@ __global__ __launch_bounds__(kThreads) void cl_adamw(const ClTile* __restrict__ 
   const int64_t at = t.begin + e;
   const v4f g = load<4>(update + at) * c;
   v4f x = load<4>(params + at), m = load<4>(exp_avg + at), v = load<4>(exp_avg_sq + at);
-  m = cf.beta1 * m + cf.om_beta1 * g;
-  v = cf.beta2 * v + cf.om_beta2 * (g * g);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float den = sqrtf(v[j]) * s.inv_sqrt + cf.eps;
-    x[j] = fmaf(-d, x[j], x[j]) - s.step_size * (m[j] / den);
-  }
+  adamw4(g, x, m, v, s, cf, d);
   const int n = t.len - e;
   store<4>(params + at, x, n);
   store<4>(exp_avg + at, m, n);
   store<4>(exp_avg_sq + at, v, n);
   if (copy != nullptr) store<4>(copy + at, x, n);
+}
+
+// The norm of one slice by one workgroup (every thread gets it): an item per wave at a
+// time, its partial into `part`, which is whole after the barrier inside.
+template <typename GT, typename N>
+__device__ __forceinline__ double small_norm(const ClItem* items, int n_items, const GT* __restrict__ g,
+                                             typename N::acc_t* part) {
+  constexpr int NE = kUnit<GT>;
+  const int lane = int(threadIdx.x & 63), wave = int(threadIdx.x >> 6);
+  for (int i = wave; i < n_items; i += kSmallThreads / 64) {
+    const ClItem it = items[i];
+    typename N::acc_t acc = N::zero();
+#pragma unroll
+    for (int k = 0; k < kItem / (64 * NE); ++k) {
+      const int e = (k * 64 + lane) * NE;
+      if (e >= it.len) continue;
+      const auto v = load<NE, true>(g + it.begin + e);
+#pragma unroll
+      for (int j = 0; j < NE; ++j)
+        if (e + j < it.len) N::take(acc, v[j]);
+    }
+    acc = wave_join<N>(acc);
+    if (lane == 0) part[i] = acc;
+  }
+  __syncthreads();
+  typename N::acc_t acc = lane < n_items ? part[lane] : N::zero();
+  if (lane + 64 < n_items) acc = N::join(acc, part[lane + 64]);
+  return N::norm(wave_join<N>(acc));
+}
+
+// One slice per workgroup: its norm, its tensors' (tensor_norms given), and out = c * g
+// (out given).
+template <typename GT, typename N>
+__global__ __launch_bounds__(kSmallThreads) void cl_small(const ClItem* __restrict__ item_table, int n_items,
+                                                          const ClLayer* __restrict__ item_layers, int n_layers,
+                                                          const GT* grads, GT* out, int64_t stride, double max_norm,
+                                                          float* __restrict__ norms, float* __restrict__ tensor_norms,
+                                                          float* __restrict__ coefs) {
+  constexpr int NE = kUnit<GT>;
+  __shared__ typename N::acc_t part[kMaxItems];
+  __shared__ ClItem items[kMaxItems];
+  const int lane = int(threadIdx.x & 63), wave = int(threadIdx.x >> 6);
+  const int64_t slice = blockIdx.x;
+  if (int(threadIdx.x) < n_items) items[threadIdx.x] = item_table[threadIdx.x];
+  __syncthreads();
+  const GT* g = grads + slice * stride;
+  const double norm = small_norm<GT, N>(items, n_items, g, part);
+  if (tensor_norms != nullptr && int(threadIdx.x) < n_layers) {
+    const ClLayer L = item_layers[threadIdx.x];
+    typename N::acc_t acc = N::zero();
+    for (int i = 0; i < L.ntiles; ++i) acc = N::join(acc, part[L.tile0 + i]);
+    tensor_norms[slice * n_layers + int(threadIdx.x)] = float(N::norm(acc));
+  }
+  const float c = clip_coef(norm, max_norm);
+  if (threadIdx.x == 0) {
+    norms[slice] = float(norm);
+    if (coefs != nullptr) coefs[slice] = c;
+  }
+  if (out == nullptr || (c == 1.0f && grads == out)) return;
+  GT* o = out + slice * stride;
+  for (int i = wave; i < n_items; i += kSmallThreads / 64) {
+    const ClItem it = items[i];
+#pragma unroll
+    for (int k = 0; k < kItem / (64 * NE); ++k) {
+      const int e = (k * 64 + lane) * NE;
+      if (e < it.len) store<NE>(o + it.begin + e, load<NE, true>(g + it.begin + e) * c, it.len - e);
+    }
+  }
+}
+
+// The whole AdamW step in one workgroup.
+template <typename GT, typename N, bool CLIP>
+__global__ __launch_bounds__(kSmallThreads) void cl_small_adamw(const ClItem* __restrict__ item_table, int n_items,
+                                                                const GT* __restrict__ update,
+                                                                float* __restrict__ params,
+                                                                float* __restrict__ exp_avg,
+                                                                float* __restrict__ exp_avg_sq,
+                                                                uint16_t* __restrict__ copy, AwConfig cf, AwArgs aw,
+                                                                double max_norm, float* __restrict__ norm_out,
+                                                                int64_t* step) {
+  __shared__ typename N::acc_t part[kMaxItems];
+  __shared__ ClItem items[kMaxItems];
+  __shared__ AwState scalars;
+  const int lane = int(threadIdx.x & 63), wave = int(threadIdx.x >> 6);
+  if (int(threadIdx.x) < n_items) items[threadIdx.x] = item_table[threadIdx.x];
+  __syncthreads();
+  if (threadIdx.x == kSmallThreads - 1) scalars = step_scalars(aw);
+  float c = 1.0f;
+  if (!CLIP) __syncthreads();
+  if (CLIP) {
+    const double norm = small_norm<GT, N>(items, n_items, update, part);  // a barrier inside
+    c = clip_coef(norm, max_norm);
+    if (threadIdx.x == 0) norm_out[0] = float(norm);
+    if (cf.skip_nonfinite && !isfinite(float(norm))) return;
+  }
+  const AwState s = scalars;
+  if (threadIdx.x == 0) step[0] = s.t;  // read before the barrier
+  for (int i = wave; i < n_items; i += kSmallThreads / 64) {
+    const ClItem it = items[i];
+    const float d = cf.matrices_only && !it.matrix ? 0.0f : cf.decay;
+#pragma unroll
+    for (int k = 0; k < kItem / 256; ++k) {
+      const int e = (k * 64 + lane) * 4, at = it.begin + e, n = it.len - e;
+      if (n <= 0) continue;
+      const v4f g = load<4>(update + at) * c;
+      v4f x = load<4>(params + at), m = load<4>(exp_avg + at), v = load<4>(exp_avg_sq + at);
+      adamw4(g, x, m, v, s, cf, d);
+      store<4>(params + at, x, n);
+      store<4>(exp_avg + at, m, n);
+      store<4>(exp_avg_sq + at, v, n);
+      if (copy != nullptr) store<4>(copy + at, x, n);
+    }
+  }
 }
 
 // ------------------------------------------------------------------ host helpers
@@ -353,15 +542,38 @@ struct DevTables {
   const ClLayer* layers;
   const ClTile* tiles;
   const ClRun* runs;
+  const ClItem* items;
+  const ClLayer* item_layers;
 };
+
+// The plan's tables one after the other, each at a multiple of 256 bytes.
+struct Part {
+  const void* src;
+  uint64_t bytes, at;
+};
+
+constexpr int kParts = 5;
+
+uint64_t lay_out(const psgd_clip_plan* plan, Part (&p)[kParts]) {
+  p[0] = Part{plan->layers.data(), plan->layers.size() * sizeof(ClLayer), 0};
+  p[1] = Part{plan->tiles.data(), plan->tiles.size() * sizeof(ClTile), 0};
+  p[2] = Part{plan->runs.data(), plan->runs.size() * sizeof(ClRun), 0};
+  p[3] = Part{plan->items.data(), plan->items.size() * sizeof(ClItem), 0};
+  p[4] = Part{plan->item_layers.data(), plan->item_layers.size() * sizeof(ClLayer), 0};
+  uint64_t at = 0;
+  for (Part& x : p) {
+    x.at = at;
+    at = a256(at + x.bytes);
+  }
+  return at;
+}
 
 psgd_status device_tables(const char* fn, psgd_clip_plan* plan, hipStream_t st, DevTables* out) {
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return hip_fail("hipGetDevice", e);
-  const uint64_t bl = a256(plan->layers.size() * sizeof(ClLayer));
-  const uint64_t bt = a256(plan->tiles.size() * sizeof(ClTile));
-  const uint64_t br = plan->runs.size() * sizeof(ClRun);
+  Part parts[kParts];
+  const uint64_t total = lay_out(plan, parts);
   auto it = plan->dev.find(dev);
   if (it == plan->dev.end()) {
     hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
@@ -370,18 +582,17 @@ psgd_status device_tables(const char* fn, psgd_clip_plan* plan, hipStream_t st, 
     if (cs != hipStreamCaptureStatusNone)
       return fail(PSGD_ERR_INVALID_ARG, std::string(fn) + ": a plan can be captured into a graph only after an eager "
                                             "call of the plan on this device");
+    std::vector<char> image(total);
+    for (const Part& p : parts)
+      if (p.bytes != 0) std::memcpy(image.data() + p.at, p.src, p.bytes);
     it = plan->dev.emplace(dev, nullptr).first;
     void* base = nullptr;
-    e = hipMalloc(&base, bl + bt + br);
+    e = hipMalloc(&base, total);
     if (e != hipSuccess) {
       plan->dev.erase(it);
       return fail(PSGD_ERR_NO_MEMORY, std::string("hipMalloc of the plan's device tables: ") + hipGetErrorString(e));
     }
-    char* b = static_cast<char*>(base);
-    e = hipMemcpy(b, plan->layers.data(), plan->layers.size() * sizeof(ClLayer), hipMemcpyHostToDevice);
-    if (e == hipSuccess)
-      e = hipMemcpy(b + bl, plan->tiles.data(), plan->tiles.size() * sizeof(ClTile), hipMemcpyHostToDevice);
-    if (e == hipSuccess) e = hipMemcpy(b + bl + bt, plan->runs.data(), br, hipMemcpyHostToDevice);
+    e = hipMemcpy(base, image.data(), total, hipMemcpyHostToDevice);
     if (e != hipSuccess) {
       (void)hipFree(base);
       plan->dev.erase(it);
@@ -389,10 +600,12 @@ psgd_status device_tables(const char* fn, psgd_clip_plan* plan, hipStream_t st, 
     }
     it->second = base;
   }
-  char* b = static_cast<char*>(it->second);
-  out->layers = reinterpret_cast<const ClLayer*>(b);
-  out->tiles = reinterpret_cast<const ClTile*>(b + bl);
-  out->runs = reinterpret_cast<const ClRun*>(b + bl + bt);
+  const char* b = static_cast<const char*>(it->second);
+  out->layers = reinterpret_cast<const ClLayer*>(b + parts[0].at);
+  out->tiles = reinterpret_cast<const ClTile*>(b + parts[1].at);
+  out->runs = reinterpret_cast<const ClRun*>(b + parts[2].at);
+  out->items = reinterpret_cast<const ClItem*>(b + parts[3].at);
+  out->item_layers = reinterpret_cast<const ClLayer*>(b + parts[4].at);
   return PSGD_OK;
 }
 
@@ -475,65 +688,135 @@ psgd_status check_kind(const char* fn, int kind) {
   return fail(PSGD_ERR_UNSUPPORTED, std::string(fn) + ": unknown norm kind");
 }
 
-// What a call's norm is taken for.
-struct NormArgs {
+bool small(const psgd_clip_plan* plan, int64_t most) {
+  return !plan->items.empty() && plan->worker_stride <= most;
+}
+
+bool fold(const psgd_clip_plan* plan) {
+  const int64_t runs = int64_t(plan->runs.size());
+  return runs <= kFoldRuns && runs * plan->n_slices <= kFoldTotal;
+}
+
+// The partials of every slice's norm.  `again`: the same call reads the gradients once more.
+template <typename GT, typename N>
+psgd_status enqueue_partials(psgd_clip_plan* plan, const DevTables& dt, const void* grads, bool tensors, bool again,
+                             const AwArgs& aw, char* ws, hipStream_t st) {
+  typedef typename N::acc_t acc_t;
+  const int64_t total = int64_t(plan->n_slices) * plan->worker_stride;
+  const int64_t keep_from = again ? total - kKeepBytes / int64_t(sizeof(GT)) : total;
+  const dim3 grid(static_cast<unsigned>(plan->runs.size()), static_cast<unsigned>(plan->n_slices));
+  return launch(plan, kNorm, cl_norm<GT, N>, grid, dim3(kThreads), st, dt.tiles, dt.runs, int(plan->tiles.size()),
+                static_cast<const GT*>(grads), plan->worker_stride, keep_from,
+                tensors ? reinterpret_cast<acc_t*>(ws + plan->ws_tile) : nullptr,
+                reinterpret_cast<acc_t*>(ws + plan->ws_run), aw);
+}
+
+// What follows from the partials: see cl_final.
+template <typename N>
+psgd_status enqueue_final(psgd_clip_plan* plan, const DevTables& dt, double max_norm, float* norms,
+                          float* tensor_norms, float* coefs, const AwArgs& aw, char* ws, hipStream_t st) {
+  typedef typename N::acc_t acc_t;
+  const int n_layers = tensor_norms != nullptr ? int(plan->layers.size()) : 0;
+  const unsigned blocks = 1u + unsigned(n_layers) + (aw.state != nullptr ? 1u : 0u);
+  return launch(plan, kFinal, cl_final<N>, dim3(blocks, static_cast<unsigned>(plan->n_slices)), dim3(kThreads), st,
+                dt.layers, n_layers, int(plan->tiles.size()), int(plan->runs.size()),
+                reinterpret_cast<const acc_t*>(ws + plan->ws_tile),
+                norms != nullptr ? reinterpret_cast<const acc_t*>(ws + plan->ws_run) : nullptr, max_norm, norms,
+                tensor_norms, coefs, reinterpret_cast<float*>(ws + plan->ws_coef), aw);
+}
+
+template <typename N>
+CoefArgs<N> coef_args(const psgd_clip_plan* plan, double max_norm, float* norms, float* coefs, const char* ws) {
+  return CoefArgs<N>{reinterpret_cast<const float*>(ws + plan->ws_coef),
+                     reinterpret_cast<const typename N::acc_t*>(ws + plan->ws_run), int32_t(plan->runs.size()),
+                     max_norm, norms, coefs};
+}
+
+template <typename GT, typename N>
+psgd_status enqueue_small(psgd_clip_plan* plan, const DevTables& dt, const void* grads, void* out, double max_norm,
+                          float* norms, float* tensor_norms, float* coefs, hipStream_t st) {
+  return launch(plan, kSmall, cl_small<GT, N>, dim3(static_cast<unsigned>(plan->n_slices)), dim3(kSmallThreads), st,
+                dt.items, int(plan->items.size()), dt.item_layers, int(plan->layers.size()),
+                static_cast<const GT*>(grads), static_cast<GT*>(out), plan->worker_stride, max_norm, norms,
+                tensor_norms, coefs);
+}
+
+struct Norm {
   const void* grads;
-  double max_norm;
-  float *norms, *tensor_norms, *coefs;
-  AwArgs aw;
-  bool again;  // the same call reads the gradients once more
+  float *norms, *tensor_norms;
+
+  template <typename GT, typename N>
+  psgd_status enqueue(psgd_clip_plan* plan, const DevTables& dt, char* ws, hipStream_t st) const {
+    if (small(plan, kSmallNorm))
+      return enqueue_small<GT, N>(plan, dt, grads, nullptr, INFINITY, norms, tensor_norms, nullptr, st);
+    const psgd_status s =
+        enqueue_partials<GT, N>(plan, dt, grads, tensor_norms != nullptr, false, AwArgs{}, ws, st);
+    return s != PSGD_OK ? s
+                        : enqueue_final<N>(plan, dt, INFINITY, norms, tensor_norms, nullptr, AwArgs{}, ws, st);
+  }
 };
 
-// The norm of every slice, and what else cl_final derives.  N = L2 or Max.
-template <typename GT, typename N>
-psgd_status enqueue_norm_of(psgd_clip_plan* plan, const DevTables& dt, const NormArgs& a, char* ws, hipStream_t st) {
-  typedef typename N::acc_t acc_t;
-  const int n_layers = int(plan->layers.size()), n_tiles = int(plan->tiles.size()), n_runs = int(plan->runs.size());
-  const unsigned S = static_cast<unsigned>(plan->n_slices);
-  acc_t* part_tile = a.tensor_norms != nullptr ? reinterpret_cast<acc_t*>(ws + plan->ws_tile) : nullptr;
-  acc_t* part_run = reinterpret_cast<acc_t*>(ws + plan->ws_run);
-  const int64_t total = int64_t(plan->n_slices) * plan->worker_stride;
-  const int64_t keep_from = a.again ? total - kKeepBytes / int64_t(sizeof(GT)) : total;
-  const psgd_status s = launch(plan, kNorm, cl_norm<GT, N>, dim3(static_cast<unsigned>(n_runs), S), dim3(kThreads), st,
-                               dt.tiles, dt.runs, n_tiles, static_cast<const GT*>(a.grads), plan->worker_stride,
-                               keep_from, part_tile, part_run);
-  if (s != PSGD_OK) return s;
-  const unsigned blocks = 1u + (part_tile != nullptr ? unsigned(n_layers) : 0u) + (a.aw.state != nullptr ? 1u : 0u);
-  return launch(plan, kFinal, cl_final<N>, dim3(blocks, S), dim3(kThreads), st, dt.layers, n_layers, n_tiles, n_runs,
-                static_cast<const acc_t*>(part_tile), static_cast<const acc_t*>(part_run), a.max_norm, a.norms,
-                a.tensor_norms, a.coefs, reinterpret_cast<float*>(ws + plan->ws_coef), a.aw);
-}
+struct Clip {
+  const void* grads;
+  void* out;
+  double max_norm;
+  float *norms, *coefs;
 
-psgd_status enqueue_norm(psgd_clip_plan* plan, int kind, const DevTables& dt, const NormArgs& a, char* ws,
-                         hipStream_t st) {
-  const bool bf = plan->dtype == PSGD_BF16;
-  if (kind == PSGD_NORM_MAX)
-    return bf ? enqueue_norm_of<uint16_t, Max>(plan, dt, a, ws, st) : enqueue_norm_of<float, Max>(plan, dt, a, ws, st);
-  return bf ? enqueue_norm_of<uint16_t, L2>(plan, dt, a, ws, st) : enqueue_norm_of<float, L2>(plan, dt, a, ws, st);
-}
+  template <typename GT, typename N>
+  psgd_status enqueue(psgd_clip_plan* plan, const DevTables& dt, char* ws, hipStream_t st) const {
+    if (small(plan, kSmallNorm))
+      return enqueue_small<GT, N>(plan, dt, grads, out, max_norm, norms, nullptr, coefs, st);
+    psgd_status s = enqueue_partials<GT, N>(plan, dt, grads, false, true, AwArgs{}, ws, st);
+    if (s == PSGD_OK && !fold(plan)) s = enqueue_final<N>(plan, dt, max_norm, norms, nullptr, coefs, AwArgs{}, ws, st);
+    if (s != PSGD_OK) return s;
+    const unsigned parts = kTile / (kThreads * kUnit<GT>);
+    const dim3 grid(static_cast<unsigned>(plan->tiles.size()) * parts, static_cast<unsigned>(plan->n_slices));
+    return launch(plan, kScale, fold(plan) ? cl_scale<GT, N, true> : cl_scale<GT, N, false>, grid, dim3(kThreads), st,
+                  dt.tiles, static_cast<const GT*>(grads), static_cast<GT*>(out), plan->worker_stride,
+                  coef_args<N>(plan, max_norm, norms, coefs, ws));
+  }
+};
 
-template <typename GT>
-psgd_status enqueue_scale(psgd_clip_plan* plan, const DevTables& dt, const void* grads, void* out, const char* ws,
-                          hipStream_t st) {
-  const unsigned parts = kTile / (kThreads * kUnit<GT>);
-  const dim3 grid(static_cast<unsigned>(plan->tiles.size()) * parts, static_cast<unsigned>(plan->n_slices));
-  return launch(plan, kScale, cl_scale<GT>, grid, dim3(kThreads), st, dt.tiles, static_cast<const GT*>(grads),
-                static_cast<GT*>(out), plan->worker_stride, reinterpret_cast<const float*>(ws + plan->ws_coef));
-}
-
-struct AwBuffers {
+struct Adamw {
   const void* update;
   float *params, *exp_avg, *exp_avg_sq;
   uint16_t* copy;
   int64_t* step;
+  float* norm;
+  double max_norm;
+  AwConfig cf;
+  AwArgs aw;
+
+  template <typename GT, typename N>
+  psgd_status enqueue(psgd_clip_plan* plan, const DevTables& dt, char* ws, hipStream_t st) const {
+    const GT* u = static_cast<const GT*>(update);
+    const bool clip = max_norm > 0.0;
+    if (small(plan, kSmallAdamw))
+      return launch(plan, kSmallAw, clip ? cl_small_adamw<GT, N, true> : cl_small_adamw<GT, N, false>, dim3(1),
+                    dim3(kSmallThreads), st, dt.items, int(plan->items.size()), u, params, exp_avg, exp_avg_sq, copy,
+                    cf, aw, max_norm, norm, step);
+    psgd_status s = PSGD_OK;
+    const bool folded = clip && fold(plan);
+    if (clip) s = enqueue_partials<GT, N>(plan, dt, update, false, true, folded ? aw : AwArgs{}, ws, st);
+    if (s == PSGD_OK && !folded) s = enqueue_final<N>(plan, dt, max_norm, norm, nullptr, nullptr, aw, ws, st);
+    if (s != PSGD_OK) return s;
+    const dim3 grid(static_cast<unsigned>(plan->tiles.size()) * (kTile / (kThreads * 4)));
+    return launch(plan, kAdamw,
+                  !clip ? cl_adamw<GT, N, 0> : folded ? cl_adamw<GT, N, 2> : cl_adamw<GT, N, 1>, grid, dim3(kThreads),
+                  st, dt.tiles, u, params, exp_avg, exp_avg_sq, copy, static_cast<const AwState*>(aw.state), cf,
+                  coef_args<N>(plan, max_norm, norm, nullptr, ws), step);
+  }
 };
 
-template <typename GT>
-psgd_status enqueue_adamw(psgd_clip_plan* plan, const DevTables& dt, const AwBuffers& b, const AwState* state,
-                          const AwConfig& cf, const float* norm, const float* coef, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(plan->tiles.size()) * (kTile / (kThreads * 4)));
-  return launch(plan, kAdamw, cl_adamw<GT>, grid, dim3(kThreads), st, dt.tiles, static_cast<const GT*>(b.update),
-                b.params, b.exp_avg, b.exp_avg_sq, b.copy, state, cf, norm, coef, b.step);
+template <typename Call>
+psgd_status enqueue(psgd_clip_plan* plan, int kind, const Call& call, const DevTables& dt, void* workspace,
+                    hipStream_t st) {
+  char* ws = static_cast<char*>(workspace);
+  const bool bf = plan->dtype == PSGD_BF16;
+  if (kind == PSGD_NORM_MAX)
+    return bf ? call.template enqueue<uint16_t, Max>(plan, dt, ws, st)
+              : call.template enqueue<float, Max>(plan, dt, ws, st);
+  return bf ? call.template enqueue<uint16_t, L2>(plan, dt, ws, st) : call.template enqueue<float, L2>(plan, dt, ws, st);
 }
 
 }  // namespace
@@ -603,6 +886,17 @@ extern "C" psgd_status psgd_clip_plan_create(const psgd_layer* layers, int32_t n
         run.tile0 = run.tile1;
       }
     }
+    // A small plan's tensors in items.
+    int64_t n_items = 0;
+    for (const psgd_clip_layer_info& li : plan->info) n_items += (li.numel + kItem - 1) / kItem;
+    if (n_items <= kMaxItems)
+      for (const psgd_clip_layer_info& li : plan->info) {
+        const int32_t item0 = int32_t(plan->items.size());
+        for (int64_t b = 0; b < li.numel; b += kItem)
+          plan->items.push_back(ClItem{int32_t(li.offset + b), int32_t(std::min<int64_t>(kItem, li.numel - b)),
+                                       li.rows > 1 && li.cols > 1 ? 1 : 0, 0});
+        plan->item_layers.push_back(ClLayer{item0, int32_t(plan->items.size()) - item0});
+      }
     uint64_t ws = 0;
     plan->ws_tile = ws;  // one partial per tile and slice
     ws = a256(ws + uint64_t(n_slices) * uint64_t(n_tiles) * sizeof(double));
@@ -736,8 +1030,7 @@ extern "C" psgd_status psgd_grad_norm(psgd_clip_plan* plan, const void* grads, p
     const hipStream_t st = static_cast<hipStream_t>(stream);
     DevTables dt{};
     if ((s = device_tables(fn, plan, st, &dt)) != PSGD_OK) return s;
-    const NormArgs a{grads, double(INFINITY), norms, tensor_norms, nullptr, AwArgs{}, false};
-    return enqueue_norm(plan, kind, dt, a, static_cast<char*>(workspace), st);
+    return enqueue(plan, kind, Norm{grads, norms, tensor_norms}, dt, workspace, st);
   } catch (...) {
     return no_memory();
   }
@@ -764,11 +1057,7 @@ extern "C" psgd_status psgd_grad_clip(psgd_clip_plan* plan, const void* grads, v
     const hipStream_t st = static_cast<hipStream_t>(stream);
     DevTables dt{};
     if ((s = device_tables(fn, plan, st, &dt)) != PSGD_OK) return s;
-    char* ws = static_cast<char*>(workspace);
-    const NormArgs a{grads, double(max_norm), norms, nullptr, coefs, AwArgs{}, true};
-    if ((s = enqueue_norm(plan, kind, dt, a, ws, st)) != PSGD_OK) return s;
-    return plan->dtype == PSGD_BF16 ? enqueue_scale<uint16_t>(plan, dt, grads, out, ws, st)
-                                    : enqueue_scale<float>(plan, dt, grads, out, ws, st);
+    return enqueue(plan, kind, Clip{grads, out, double(max_norm), norms, coefs}, dt, workspace, st);
   } catch (...) {
     return no_memory();
   }
@@ -816,28 +1105,15 @@ extern "C" psgd_status psgd_adamw_apply(psgd_clip_plan* plan, const psgd_adamw_c
     const hipStream_t st = static_cast<hipStream_t>(stream);
     DevTables dt{};
     if ((s = device_tables(fn, plan, st, &dt)) != PSGD_OK) return s;
-    char* ws = static_cast<char*>(workspace);
-    const AwArgs aw{cf.lr, cf.beta1, cf.beta2, step, reinterpret_cast<AwState*>(ws + plan->ws_aw)};
+    const AwArgs aw{cf.lr, cf.beta1, cf.beta2, step,
+                    reinterpret_cast<AwState*>(static_cast<char*>(workspace) + plan->ws_aw)};
     const AwConfig ac{float(cf.beta1), float(1.0 - cf.beta1), float(cf.beta2), float(1.0 - cf.beta2),
                       float(cf.eps), float(cf.lr * cf.weight_decay),
                       (cf.flags & PSGD_ADAMW_DECAY_MATRICES_ONLY) ? 1 : 0,
                       (cf.flags & PSGD_ADAMW_SKIP_NONFINITE) ? 1 : 0};
-    const AwBuffers b{update, params, exp_avg, exp_avg_sq, static_cast<uint16_t*>(params_bf16), step};
-    const float* coef = nullptr;
-    if (clipped) {
-      const NormArgs a{update, cf.max_norm, norm, nullptr, nullptr, aw, true};
-      s = enqueue_norm(plan, cf.norm_kind, dt, a, ws, st);
-      coef = reinterpret_cast<const float*>(ws + plan->ws_coef);
-    } else {
-      // only the step's scalars
-      s = launch(plan, kFinal, cl_final<L2>, dim3(2), dim3(kThreads), st, dt.layers, 0, 0, 0,
-                 static_cast<const double*>(nullptr), static_cast<const double*>(nullptr), 0.0,
-                 static_cast<float*>(nullptr), static_cast<float*>(nullptr), static_cast<float*>(nullptr),
-                 static_cast<float*>(nullptr), aw);
-    }
-    if (s != PSGD_OK) return s;
-    return plan->dtype == PSGD_BF16 ? enqueue_adamw<uint16_t>(plan, dt, b, aw.state, ac, norm, coef, st)
-                                    : enqueue_adamw<float>(plan, dt, b, aw.state, ac, norm, coef, st);
+    const Adamw call{update, params, exp_avg, exp_avg_sq, static_cast<uint16_t*>(params_bf16), step, norm,
+                     cf.max_norm, ac, aw};
+    return enqueue(plan, clipped ? cf.norm_kind : int(PSGD_NORM_L2), call, dt, workspace, st);
   } catch (...) {
     return no_memory();
   }

@@ -650,37 +650,45 @@ def psgd_clip_plan_kernel_stats(plan: ClipPlan, reset: bool = False) -> dict:
     return {arr[i].name.decode(): (arr[i].launches, arr[i].total_ms) for i in range(n.value)}
 
 
-def _buffer(name: str, t, dtypes, numel: int, device) -> int:
+def _buffer(name: str, t, dtype, numel: int, device: int) -> int:
     """The device pointer of a tensor the library will read or write `numel` elements of:
     what the C side cannot see (element type, length, strides, device) is checked here."""
-    if t.dtype not in dtypes or t.numel() < numel or not t.is_contiguous() or t.device != device:
-        raise PsgdError(PSGD_ERR_INVALID_ARG, f"{name} must be a contiguous tensor of {dtypes[0]} with at least "
-                                              f"{numel} elements on {device}")
+    if t.dtype is not dtype or t.get_device() != device or t.numel() < numel or not t.is_contiguous():
+        raise PsgdError(PSGD_ERR_INVALID_ARG, f"{name} must be a contiguous tensor of {dtype} with at least {numel} "
+                                              f"elements on the call's device")
     return t.data_ptr()
 
 
-def _clip_common(plan: ClipPlan, ref):
-    """(element types of the gradient buffers, their length, the device) of a call."""
+def _call_device(ref) -> int:
+    device = ref.get_device()
+    if device < 0:
+        raise PsgdError(PSGD_ERR_INVALID_ARG, "the buffers must be on a ROCm device")
+    return device
+
+
+def _grad_dtype(plan: ClipPlan):
     import torch
 
-    if not ref.is_cuda:
-        raise PsgdError(PSGD_ERR_INVALID_ARG, "the buffers must be on a ROCm device")
-    s = plan.sizes
-    return (torch.bfloat16 if s["grad_dtype"] == PSGD_BF16 else torch.float32,), s["n_slices"] * s["worker_stride"], ref.device
+    return torch.bfloat16 if plan.sizes["grad_dtype"] == PSGD_BF16 else torch.float32
 
 
-def _enqueue(fn, device, stream, *args) -> None:
+def _enqueue(fn, device: int, stream, *args) -> None:
     """Call a step function with `device` current; the stream is its last argument."""
     import torch
 
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    st = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, st))
+        # the handle alone: building a Stream object costs 1.8 us, a quarter of a small call
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        st = raw(device) if raw is not None else torch.cuda.current_stream(device).cuda_stream
+    else:
+        st = int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+    if device == torch.cuda.current_device():
+        status = fn(*args, st)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, st))
+            status = fn(*args, st)
+    if status != PSGD_OK:
+        _check(status)
 
 
 def psgd_grad_norm(plan: ClipPlan, grads, kind: int, norms, tensor_norms, workspace, stream=None) -> None:
@@ -688,13 +696,13 @@ def psgd_grad_norm(plan: ClipPlan, grads, kind: int, norms, tensor_norms, worksp
     include/psgd_clip.h)."""
     import torch
 
-    gt, total, dev = _clip_common(plan, grads)
-    s, f32 = plan.sizes, (torch.float32,)
-    _enqueue(load_library().psgd_grad_norm, dev, stream, plan.handle, _buffer("grads", grads, gt, total, dev), int(kind),
-             _buffer("norms", norms, f32, s["n_slices"], dev),
-             None if tensor_norms is None else
-             _buffer("tensor_norms", tensor_norms, f32, s["n_slices"] * s["n_layers"], dev),
-             _buffer("workspace", workspace, (torch.uint8,), s["workspace_bytes"], dev))
+    s, dev, f32 = plan.sizes, _call_device(grads), torch.float32
+    S = s["n_slices"]
+    _enqueue(load_library().psgd_grad_norm, dev, stream, plan.handle,
+             _buffer("grads", grads, _grad_dtype(plan), S * s["worker_stride"], dev), int(kind),
+             _buffer("norms", norms, f32, S, dev),
+             None if tensor_norms is None else _buffer("tensor_norms", tensor_norms, f32, S * s["n_layers"], dev),
+             _buffer("workspace", workspace, torch.uint8, s["workspace_bytes"], dev))
 
 
 def psgd_grad_clip(plan: ClipPlan, grads, out, kind: int, max_norm: float, norms, coefs, workspace,
@@ -703,12 +711,13 @@ def psgd_grad_clip(plan: ClipPlan, grads, out, kind: int, max_norm: float, norms
     include/psgd_clip.h)."""
     import torch
 
-    gt, total, dev = _clip_common(plan, grads)
-    s, f32 = plan.sizes, (torch.float32,)
+    s, dev, f32, gt = plan.sizes, _call_device(grads), torch.float32, _grad_dtype(plan)
+    S = s["n_slices"]
+    total = S * s["worker_stride"]
     _enqueue(load_library().psgd_grad_clip, dev, stream, plan.handle, _buffer("grads", grads, gt, total, dev),
-             _buffer("out", out, gt, total, dev), int(kind), float(max_norm),
-             _buffer("norms", norms, f32, s["n_slices"], dev), _buffer("coefs", coefs, f32, s["n_slices"], dev),
-             _buffer("workspace", workspace, (torch.uint8,), s["workspace_bytes"], dev))
+             _buffer("out", out, gt, total, dev), int(kind), float(max_norm), _buffer("norms", norms, f32, S, dev),
+             _buffer("coefs", coefs, f32, S, dev),
+             _buffer("workspace", workspace, torch.uint8, s["workspace_bytes"], dev))
 
 
 def psgd_adamw_apply(plan: ClipPlan, config: AdamwConfig, update, params, exp_avg, exp_avg_sq, params_bf16, step,
@@ -716,17 +725,17 @@ def psgd_adamw_apply(plan: ClipPlan, config: AdamwConfig, update, params, exp_av
     """Enqueue one AdamW step on (optionally clipped) `update` (see include/psgd_clip.h)."""
     import torch
 
-    gt, _, dev = _clip_common(plan, update)
-    n, f32 = plan.sizes["worker_stride"], (torch.float32,)
+    s, dev, f32 = plan.sizes, _call_device(update), torch.float32
+    n = s["worker_stride"]
     c = _AdamwConfig(config.lr, config.beta1, config.beta2, config.eps, config.weight_decay, config.max_norm,
                      config.norm_kind, config.flags)
     _enqueue(load_library().psgd_adamw_apply, dev, stream, plan.handle, ctypes.byref(c),
-             _buffer("update", update, gt, n, dev), _buffer("params", params, f32, n, dev),
+             _buffer("update", update, _grad_dtype(plan), n, dev), _buffer("params", params, f32, n, dev),
              _buffer("exp_avg", exp_avg, f32, n, dev), _buffer("exp_avg_sq", exp_avg_sq, f32, n, dev),
-             None if params_bf16 is None else _buffer("params_bf16", params_bf16, (torch.bfloat16,), n, dev),
-             _buffer("step", step, (torch.int64,), 1, dev),
+             None if params_bf16 is None else _buffer("params_bf16", params_bf16, torch.bfloat16, n, dev),
+             _buffer("step", step, torch.int64, 1, dev),
              None if norm is None else _buffer("norm", norm, f32, 1, dev),
-             _buffer("workspace", workspace, (torch.uint8,), plan.sizes["workspace_bytes"], dev))
+             _buffer("workspace", workspace, torch.uint8, s["workspace_bytes"], dev))
 
 
 # ------------------------------------------------------------------------ layout helpers

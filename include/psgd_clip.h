@@ -135,7 +135,7 @@ psgd_status psgd_adamw_apply(psgd_clip_plan* plan, const psgd_adamw_config* conf
                              void* workspace, void* stream);
 
 /* Kernel timing as psgd_plan_set_timing / psgd_plan_kernel_stats.  Kernel names:
- * "cl_norm", "cl_final", "cl_scale", "cl_adamw". */
+ * "cl_norm", "cl_final", "cl_scale", "cl_adamw", "cl_small", "cl_small_adamw". */
 psgd_status psgd_clip_plan_set_timing(psgd_clip_plan* plan, int32_t enable);
 psgd_status psgd_clip_plan_kernel_stats(psgd_clip_plan* plan, psgd_kernel_stat* out, int32_t capacity,
                                         int32_t* count, int32_t reset);

@@ -452,7 +452,7 @@ def test_timing_names():
     psgd.psgd_grad_clip(plan, g, g, psgd.PSGD_NORM_L2, 1.0, norms, coefs, ws)
     psgd.psgd_adamw_apply(plan, psgd.AdamwConfig(max_norm=1.0), g[0], x, m, v, None, t, norms, ws)
     stats = psgd.psgd_clip_plan_kernel_stats(plan, reset=True)
-    assert stats and set(stats) <= {"cl_norm", "cl_final", "cl_scale", "cl_adamw"}
+    assert stats and set(stats) <= {"cl_norm", "cl_final", "cl_scale", "cl_adamw", "cl_small", "cl_small_adamw"}
     assert all(n > 0 and ms > 0 for n, ms in stats.values())
     assert psgd.psgd_clip_plan_kernel_stats(plan) == {}
 
