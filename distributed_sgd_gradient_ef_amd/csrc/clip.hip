@@ -52,14 +52,18 @@ constexpr int64_t kKeepBytes = int64_t(224) << 20;
 constexpr int64_t kFoldRuns = 256;   // per slice
 constexpr int64_t kFoldTotal = 512;  // all slices together
 // A single launch with a workgroup per slice, for plans of at most kMaxItems items, up to
-// kSmallNorm (norms, clipping) or kSmallAdamw elements per slice.  Against the two launches
+// kSmallNorm, kSmallClip or kSmallAdamw elements per slice.  Against the two launches
 // above (us a call in a graph): norm of 16384 4.4 against 5.2, of 32768 6.0 against 5.5;
 // clip 5.8 / 5.9 and 8.3 / 5.8; AdamW of 4096 6.3 / 7.2, of 8192 7.6 / 7.2, of 16384
 // 10.5 / 7.6.  Called one by one the smaller number of launches is worth 3.5 us.
 constexpr int kItem = 512;      // elements per item
 constexpr int kMaxItems = 128;
 constexpr int kSmallThreads = 1024;
-constexpr int64_t kSmallNorm = 16384, kSmallAdamw = 8192;
+constexpr int64_t kSmallNorm = 32768, kSmallClip = 16384, kSmallAdamw = 8192;
+// Parts a cl_scale workgroup takes when out is grads: 1, 2, 3, 4 of them let a call that has
+// nothing to scale return after 39, 20, 13, 10 us (16 x 45 MB: 175 thousand workgroups
+// for 1), and scale in 221, 216, 220, 233 us when it has.
+constexpr int kInPlaceParts = 2;
 constexpr int64_t kMaxTiles = 0x1fffff;  // tiles * (kTile / 4) threads fit a launch's 32 bits
 
 struct ClTile {
@@ -263,7 +267,11 @@ __device__ __forceinline__ typename N::acc_t tile_sum(const GT* __restrict__ g, 
 }
 
 // A workgroup reads one run of one slice (grid.y).  Its partial goes to `part_run`, each
-// tile's to `part_tile` if tensor norms are wanted.
+// tile's to `part_tile` if tensor norms are wanted.  Bound by HBM reads: 715 MB of float32
+// in 102 us (7.0 TB/s; a bare reading loop reaches 7.2), 508 MB of bfloat16 in 73 us.  A
+// workgroup to a tile keeps 32 KB of loads per 256 threads short enough that the last ones
+// end together; float64 costs nothing next to the loads, if whole steps go without bounds
+// checks (with them bfloat16 took 83 us).
 template <typename GT, typename N>
 __global__ __launch_bounds__(kThreads) void cl_norm(const ClTile* __restrict__ tiles, const ClRun* __restrict__ runs,
                                                     int n_tiles, const GT* __restrict__ grads, int64_t stride,
@@ -303,6 +311,9 @@ __device__ __forceinline__ typename N::acc_t join_all(const typename N::acc_t* _
   return block_join<N>(acc, lds);
 }
 
+// Bound by its launch (4 us).  Letting cl_norm's last workgroup to arrive do this instead
+// costs as much (a store, two device-wide counts and a load one after the other) and needs
+// counters that outlive the call.
 // grid.x: workgroup 0 of a slice (grid.y) takes its norm and coefficient; the next n_layers
 // ones a tensor's norm each (tensor_norms given); the last one the AdamW step's scalars
 // (aw.state given).
@@ -357,22 +368,28 @@ __device__ __forceinline__ float coefficient(const CoefArgs<N>& a, int64_t slice
   return c;
 }
 
+// One 16-byte unit per thread and 4 KB per workgroup: reads and writes then sweep the
+// buffers in dispatch order, which HBM serves at the speed of a plain copy (16 x 45 MB in
+// 214 us, 6.7 TB/s; 64 KB per workgroup took 262 us).
 template <typename GT, typename N, bool FOLD>
-__global__ __launch_bounds__(kThreads) void cl_scale(const ClTile* __restrict__ tiles, const GT* grads, GT* out,
-                                                     int64_t stride, CoefArgs<N> ca) {
+__global__ __launch_bounds__(kThreads) void cl_scale(const ClTile* __restrict__ tiles, int n_parts,
+                                                     const GT* grads, GT* out, int64_t stride, CoefArgs<N> ca) {
   constexpr int NE = kUnit<GT>, parts = kTile / (kThreads * NE);
   const int64_t slice = gridDim.y - 1 - blockIdx.y;  // last read, first rescaled
-  const unsigned at_part = gridDim.x - 1 - blockIdx.x;
   float norm;
   const float c = coefficient<N, FOLD>(ca, slice, &norm);
   if (c == 1.0f && grads == out) return;
-  const ClTile t = tiles[at_part / parts];
-  const int e = (int(at_part % parts) * kThreads + int(threadIdx.x)) * NE;
-  if (e >= t.len) return;
-  const int64_t at = slice * stride + t.begin + e;
-  store<NE>(out + at, load<NE>(grads + at) * c, t.len - e);
+  for (int p = n_parts - 1 - int(blockIdx.x); p >= 0; p -= int(gridDim.x)) {
+    const ClTile t = tiles[p / parts];
+    const int e = (p % parts * kThreads + int(threadIdx.x)) * NE;
+    if (e >= t.len) continue;
+    const int64_t at = slice * stride + t.begin + e;
+    store<NE>(out + at, load<NE>(grads + at) * c, t.len - e);
+  }
 }
 
+// Four elements per thread, as in cl_scale: four (five) streams at 6.3 to 6.6 TB/s.  45 MB of
+// update in 50 us, 1.6 GB in 1.80 ms (64 KB per workgroup: 67 us, 2.11 ms).
 // CLIP: 0 no clipping (c = 1), 1 cl_final's coefficient, 2 from the partials.
 template <typename GT, typename N, int CLIP>
 __global__ __launch_bounds__(kThreads) void cl_adamw(const ClTile* __restrict__ tiles, const GT* __restrict__ update,
@@ -390,10 +407,10 @@ __global__ __launch_bounds__(kThreads) void cl_adamw(const ClTile* __restrict__ 
     if (cf.skip_nonfinite && !isfinite(norm)) return;
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) step[0] = s.t;
-  const unsigned at_part = gridDim.x - 1 - blockIdx.x;  // last read, first used
-  const ClTile t = tiles[at_part / parts];
+  const unsigned p = gridDim.x - 1 - blockIdx.x;  // last read, first used
+  const ClTile t = tiles[p / parts];
   const float d = cf.matrices_only && !t.matrix ? 0.0f : cf.decay;
-  const int e = (int(at_part % parts) * kThreads + int(threadIdx.x)) * 4;
+  const int e = (int(p % parts) * kThreads + int(threadIdx.x)) * 4;
   if (e >= t.len) return;
   const int64_t at = t.begin + e;
   const v4f g = load<4>(update + at) * c;
@@ -434,6 +451,7 @@ __device__ __forceinline__ double small_norm(const ClItem* items, int n_items, c
   return N::norm(wave_join<N>(acc));
 }
 
+// Bound by latency: launch, table, loads, join, loads, stores (4 us for 7 thousand elements).
 // One slice per workgroup: its norm, its tensors' (tensor_norms given), and out = c * g
 // (out given).
 template <typename GT, typename N>
@@ -474,7 +492,8 @@ __global__ __launch_bounds__(kSmallThreads) void cl_small(const ClItem* __restri
   }
 }
 
-// The whole AdamW step in one workgroup.
+// The whole AdamW step in one workgroup; one wave forms the step's scalars (two float64
+// powers) while the others take the norm.  6 us for 7 thousand elements.
 template <typename GT, typename N, bool CLIP>
 __global__ __launch_bounds__(kSmallThreads) void cl_small_adamw(const ClItem* __restrict__ item_table, int n_items,
                                                                 const GT* __restrict__ update,
@@ -575,13 +594,15 @@ psgd_status device_tables(const char* fn, psgd_clip_plan* plan, hipStream_t st, 
   Part parts[kParts];
   const uint64_t total = lay_out(plan, parts);
   auto it = plan->dev.find(dev);
-  if (it == plan->dev.end()) {
+  if (it == plan->dev.end() || plan->timing) {
     hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
     e = hipStreamIsCapturing(st, &cs);
     if (e != hipSuccess) return hip_fail("hipStreamIsCapturing", e);
     if (cs != hipStreamCaptureStatusNone)
       return fail(PSGD_ERR_INVALID_ARG, std::string(fn) + ": a plan can be captured into a graph only after an eager "
-                                            "call of the plan on this device");
+                                            "call of the plan on this device, and with kernel timing off");
+  }
+  if (it == plan->dev.end()) {
     std::vector<char> image(total);
     for (const Part& p : parts)
       if (p.bytes != 0) std::memcpy(image.data() + p.at, p.src, p.bytes);
@@ -626,8 +647,9 @@ psgd_status launch(psgd_clip_plan* plan, int kid, void (*kernel)(KArgs...), dim3
                    Args... args) {
   hipEvent_t a = nullptr, b = nullptr;
   if (plan->timing) {
-    plan->pending.reserve(plan->pending.size() + 1);
-    plan->event_pool.reserve(plan->event_pool.size() + 2);
+    // room first: nothing below may throw once events are taken
+    if (plan->pending.size() == plan->pending.capacity()) plan->pending.reserve(2 * plan->pending.size() + 64);
+    if (plan->event_pool.capacity() - plan->event_pool.size() < 2) plan->event_pool.reserve(2 * plan->event_pool.size() + 64);
     psgd_status s = take_event(plan, &a);
     if (s == PSGD_OK) s = take_event(plan, &b);
     if (s != PSGD_OK) {
@@ -764,15 +786,16 @@ struct Clip {
 
   template <typename GT, typename N>
   psgd_status enqueue(psgd_clip_plan* plan, const DevTables& dt, char* ws, hipStream_t st) const {
-    if (small(plan, kSmallNorm))
+    if (small(plan, kSmallClip))
       return enqueue_small<GT, N>(plan, dt, grads, out, max_norm, norms, nullptr, coefs, st);
     psgd_status s = enqueue_partials<GT, N>(plan, dt, grads, false, true, AwArgs{}, ws, st);
     if (s == PSGD_OK && !fold(plan)) s = enqueue_final<N>(plan, dt, max_norm, norms, nullptr, coefs, AwArgs{}, ws, st);
     if (s != PSGD_OK) return s;
-    const unsigned parts = kTile / (kThreads * kUnit<GT>);
-    const dim3 grid(static_cast<unsigned>(plan->tiles.size()) * parts, static_cast<unsigned>(plan->n_slices));
+    const int n_parts = int(plan->tiles.size()) * (kTile / (kThreads * kUnit<GT>));
+    const int per = grads == out ? kInPlaceParts : 1;
+    const dim3 grid(static_cast<unsigned>((n_parts + per - 1) / per), static_cast<unsigned>(plan->n_slices));
     return launch(plan, kScale, fold(plan) ? cl_scale<GT, N, true> : cl_scale<GT, N, false>, grid, dim3(kThreads), st,
-                  dt.tiles, static_cast<const GT*>(grads), static_cast<GT*>(out), plan->worker_stride,
+                  dt.tiles, n_parts, static_cast<const GT*>(grads), static_cast<GT*>(out), plan->worker_stride,
                   coef_args<N>(plan, max_norm, norms, coefs, ws));
   }
 };
@@ -789,21 +812,30 @@ struct Adamw {
 
   template <typename GT, typename N>
   psgd_status enqueue(psgd_clip_plan* plan, const DevTables& dt, char* ws, hipStream_t st) const {
-    const GT* u = static_cast<const GT*>(update);
-    const bool clip = max_norm > 0.0;
+    const bool clip = max_norm > 0.0, folded = clip && fold(plan);
     if (small(plan, kSmallAdamw))
-      return launch(plan, kSmallAw, clip ? cl_small_adamw<GT, N, true> : cl_small_adamw<GT, N, false>, dim3(1),
-                    dim3(kSmallThreads), st, dt.items, int(plan->items.size()), u, params, exp_avg, exp_avg_sq, copy,
-                    cf, aw, max_norm, norm, step);
+      return clip ? launch_small<GT>(cl_small_adamw<GT, N, true>, plan, dt, st)
+                  : launch_small<GT>(cl_small_adamw<GT, L2, false>, plan, dt, st);
     psgd_status s = PSGD_OK;
-    const bool folded = clip && fold(plan);
     if (clip) s = enqueue_partials<GT, N>(plan, dt, update, false, true, folded ? aw : AwArgs{}, ws, st);
     if (s == PSGD_OK && !folded) s = enqueue_final<N>(plan, dt, max_norm, norm, nullptr, nullptr, aw, ws, st);
     if (s != PSGD_OK) return s;
+    if (!clip) return launch_parts<GT, L2>(cl_adamw<GT, L2, 0>, plan, dt, ws, st);
+    return folded ? launch_parts<GT, N>(cl_adamw<GT, N, 2>, plan, dt, ws, st)
+                  : launch_parts<GT, N>(cl_adamw<GT, N, 1>, plan, dt, ws, st);
+  }
+
+  template <typename GT, typename K>
+  psgd_status launch_small(K kernel, psgd_clip_plan* plan, const DevTables& dt, hipStream_t st) const {
+    return launch(plan, kSmallAw, kernel, dim3(1), dim3(kSmallThreads), st, dt.items, int(plan->items.size()),
+                  static_cast<const GT*>(update), params, exp_avg, exp_avg_sq, copy, cf, aw, max_norm, norm, step);
+  }
+
+  template <typename GT, typename N, typename K>
+  psgd_status launch_parts(K kernel, psgd_clip_plan* plan, const DevTables& dt, char* ws, hipStream_t st) const {
     const dim3 grid(static_cast<unsigned>(plan->tiles.size()) * (kTile / (kThreads * 4)));
-    return launch(plan, kAdamw,
-                  !clip ? cl_adamw<GT, N, 0> : folded ? cl_adamw<GT, N, 2> : cl_adamw<GT, N, 1>, grid, dim3(kThreads),
-                  st, dt.tiles, u, params, exp_avg, exp_avg_sq, copy, static_cast<const AwState*>(aw.state), cf,
+    return launch(plan, kAdamw, kernel, grid, dim3(kThreads), st, dt.tiles, static_cast<const GT*>(update), params,
+                  exp_avg, exp_avg_sq, copy, static_cast<const AwState*>(aw.state), cf,
                   coef_args<N>(plan, max_norm, norm, nullptr, ws), step);
   }
 };

@@ -554,3 +554,127 @@ def test_clip_compress_and_adamw_together():
             assert np.linalg.norm(got - ref) <= 1e-4 * np.linalg.norm(ref)
         assert int(t) == step + 1
         _check_adamw(one, cfg, u, before, (x, m, v), step + 1, "l2")
+
+
+# ------------------------------------------------------------------ more calls the header allows
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("name", ["ends", "large"])
+def test_clip_into_subnormal_numbers(name, dtype):
+    """Products below the smallest normal number keep their subnormal bits."""
+    code, td = DTYPES[dtype]
+    plan = psgd.psgd_clip_plan_create(SHAPE_SETS[name], 2, code)
+    g = _grads(plan, td, seed=40, scales=[1.0, 1e-35])
+    given, out = g.clone(), torch.full_like(g, 7.0)
+    norms, coefs = torch.zeros(2, device=DEV), torch.zeros(2, device=DEV)
+    psgd.psgd_grad_clip(plan, g, out, psgd.PSGD_NORM_MAX, 1e-39, norms, coefs, _workspace(plan))
+    bound = float(np.float32(1e-39))  # a subnormal itself: half a step of it is 2^-150
+    want = [O.norm_of_tensors(_tensors(plan, r), "max") for r in _values(given)]
+    assert np.all(np.abs(_values(coefs) - [bound / n for n in want]) <= 2.0 ** -150 + 1.001 * U * bound / np.array(want))
+    inside = torch.from_numpy(~_padding(plan))
+    prod = torch.from_numpy(given.float().cpu().numpy() * coefs.cpu().numpy()[:, None]).to(td)
+    assert torch.equal(_bits(out.cpu()[:, inside]), _bits(prod[:, inside]))
+    assert bool((out.float().abs().nan_to_num(0.0)[:, inside.to(DEV)] > 0).any())
+
+
+@pytest.mark.parametrize("total", [8191, 8192, 8193, 16384, 16385, 32768, 32769, 65536, 2097152, 2097153])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_sizes_around_the_variants_borders(total, dtype):
+    """Element counts at which another kernel takes over; one call of each operator."""
+    code, td = DTYPES[dtype]
+    shapes = [(1, total - 640), (16, 40)]
+    plan, one = psgd.psgd_clip_plan_create(shapes, 2, code), psgd.psgd_clip_plan_create(shapes, 1, code)
+    g = _grads(plan, td, seed=41)
+    ws = _workspace(plan)
+    norms, coefs, per = torch.zeros(2, device=DEV), torch.zeros(2, device=DEV), torch.zeros((2, 2), device=DEV)
+    psgd.psgd_grad_norm(plan, g, psgd.PSGD_NORM_L2, norms, per, ws)
+    first = norms.clone()
+    out = torch.full_like(g, 7.0)
+    psgd.psgd_grad_clip(plan, g, out, psgd.PSGD_NORM_L2, 0.5, norms, coefs, ws)
+    rows = _values(g)
+    _near(first.cpu(), [O.norm_of_tensors(_tensors(plan, r), "l2") for r in rows], 1.001 * U)
+    _near(per.cpu(), [[O.norm(t, "l2") for t in _tensors(plan, r)] for r in rows], 1.001 * U)
+    _check_clip(plan, g, out, norms, coefs, "l2", 0.5)
+    for max_norm in (0.0, 0.25):
+        cfg = psgd.AdamwConfig(lr=1e-2, max_norm=max_norm, flags=psgd.PSGD_ADAMW_DECAY_MATRICES_ONLY)
+        x, m, v, t = _adamw_state(one, seed=42, step=9)
+        before = [a.clone() for a in (x, m, v)]
+        norm = torch.zeros(1, device=DEV) if max_norm else None
+        psgd.psgd_adamw_apply(one, cfg, g[0], x, m, v, None, t, norm, _workspace(one))
+        assert int(t) == 10
+        _check_adamw(one, cfg, g[0], before, (x, m, v), 10, "l2")
+
+
+def test_many_slices():
+    """The most slices a plan takes, on a small plan and through the two-launch path."""
+    plan = psgd.psgd_clip_plan_create([(1, 3), (2, 2)], 65535)
+    ld = plan.sizes["worker_stride"]
+    g = torch.arange(65535, dtype=torch.float32, device=DEV)[:, None].expand(65535, ld).contiguous()
+    norms, coefs = torch.zeros(65535, device=DEV), torch.zeros(65535, device=DEV)
+    psgd.psgd_grad_clip(plan, g, g, psgd.PSGD_NORM_L2, 100.0, norms, coefs, _workspace(plan))
+    want = np.sqrt(7.0) * np.arange(65535, dtype=np.float64)
+    _near(norms.cpu(), want, 1.001 * U)
+    scaled = np.float32(np.arange(65535)) * coefs.cpu().numpy()
+    assert np.array_equal(g[:, 0].cpu().numpy(), scaled) and np.array_equal(g[:, ld - 61].cpu().numpy(), scaled)
+    plan = psgd.psgd_clip_plan_create([(1, 1)] * 200, 700)  # 200 tensors: not a small plan
+    g = torch.ones((700, plan.sizes["worker_stride"]), device=DEV)
+    norms, per = torch.zeros(700, device=DEV), torch.zeros((700, 200), device=DEV)
+    psgd.psgd_grad_norm(plan, g, psgd.PSGD_NORM_L2, norms, per, _workspace(plan))
+    _near(norms.cpu(), np.full(700, math.sqrt(200.0)), 1.001 * U)
+    assert bool((per == 1).all())
+
+
+def test_capture_is_refused_with_timing_on():
+    plan = psgd.psgd_clip_plan_create(SHAPE_SETS["ends"], 3)
+    g = torch.nan_to_num(_grads(plan, torch.float32, seed=43))
+    call, _ = _one_of_each(plan, g, _workspace(plan))
+    call()
+    psgd.psgd_clip_plan_set_timing(plan, True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(psgd.PsgdError) as e:
+            call()
+        g.add_(0.0)
+    assert e.value.status == psgd.PSGD_ERR_INVALID_ARG
+
+
+def test_two_graphs_of_one_plan_one_after_the_other():
+    """Graphs that share a plan and a workspace, replayed in turn on one stream."""
+    plan = psgd.psgd_clip_plan_create(SHAPE_SETS["mixed"], 3)
+    ws = _workspace(plan)
+    sets = []
+    for seed in (44, 45):
+        g = torch.nan_to_num(_grads(plan, torch.float32, seed=seed))
+        call, outs = _one_of_each(plan, g, ws)
+        call()
+        torch.cuda.synchronize()
+        want = [o.clone() for o in outs]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        sets.append((graph, outs, want, g))  # a graph reads g as long as it is replayed
+    for _ in range(3):
+        for graph, outs, _, _ in sets:
+            for o in outs:
+                o.zero_()
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, outs, want, _ in sets:
+            assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_scaled_update_changes_nothing_but_the_norm():
+    """Clipping makes AdamW blind to the size of a large update: U and 2^20 U (both clipped)
+    give the same c U up to its roundings, and a power of two changes none of them."""
+    plan = psgd.psgd_clip_plan_create(SHAPE_SETS["large"], 1)
+    g = torch.nan_to_num(_grads(plan, torch.float32, seed=46))[0]
+    cfg = psgd.AdamwConfig(max_norm=0.125)
+    results = []
+    for scale in (1.0, 2.0 ** 20):
+        x, m, v, t = _adamw_state(plan, seed=47, step=5)
+        norm = torch.zeros(1, device=DEV)
+        psgd.psgd_adamw_apply(plan, cfg, g * scale, x, m, v, None, t, norm, _workspace(plan))
+        results.append((x, m, v, norm / scale))
+    inside = torch.from_numpy(~_padding(plan)).to(DEV)
+    for a, b in zip(*results):
+        a, b = (a[inside], b[inside]) if a.numel() > 1 else (a, b)
+        assert torch.equal(a, b)
