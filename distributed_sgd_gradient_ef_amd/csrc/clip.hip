@@ -555,6 +555,16 @@ psgd_status no_memory() {
   return PSGD_ERR_NO_MEMORY;
 }
 
+// A refusal outside a try block: no exception leaves it.
+psgd_status refuse(psgd_status s, const char* msg) noexcept {
+  try {
+    set_error(msg);
+  } catch (...) {
+    return no_memory();
+  }
+  return s;
+}
+
 uint64_t a256(uint64_t x) { return (x + 255) / 256 * 256; }
 
 struct DevTables {
@@ -860,15 +870,15 @@ using namespace psgd::clip;
 
 extern "C" psgd_status psgd_clip_plan_create(const psgd_layer* layers, int32_t n_layers, int32_t n_slices,
                                              psgd_dtype grad_dtype, uint32_t flags, psgd_clip_plan** out) {
-  if (out == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_create: out is NULL");
+  if (out == nullptr) return refuse(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_create: out is NULL");
   *out = nullptr;
-  if (layers == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_create: layers is NULL");
-  if (n_layers < 1) return fail(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_create: n_layers must be >= 1");
+  if (layers == nullptr) return refuse(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_create: layers is NULL");
+  if (n_layers < 1) return refuse(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_create: n_layers must be >= 1");
   if (n_slices < 1 || n_slices > 65535)
-    return fail(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_create: n_slices must be in 1..65535");
+    return refuse(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_create: n_slices must be in 1..65535");
   if (grad_dtype != PSGD_F32 && grad_dtype != PSGD_BF16)
-    return fail(PSGD_ERR_UNSUPPORTED, "psgd_clip_plan_create: unknown grad_dtype");
-  if (flags != 0) return fail(PSGD_ERR_UNSUPPORTED, "psgd_clip_plan_create: unknown flag bits");
+    return refuse(PSGD_ERR_UNSUPPORTED, "psgd_clip_plan_create: unknown grad_dtype");
+  if (flags != 0) return refuse(PSGD_ERR_UNSUPPORTED, "psgd_clip_plan_create: unknown flag bits");
   psgd_clip_plan* plan = nullptr;
   try {
     plan = new psgd_clip_plan();
@@ -879,6 +889,7 @@ extern "C" psgd_status psgd_clip_plan_create(const psgd_layer* layers, int32_t n
       const int64_t rows = layers[i].rows, cols = layers[i].cols;
       if (rows < 1 || cols < 1 || rows > int64_t(0x7fffffff) / cols) {
         delete plan;
+        plan = nullptr;
         return fail(PSGD_ERR_INVALID_ARG,
                     "psgd_clip_plan_create: layer " + std::to_string(i) + " needs 1 <= rows*cols < 2^31");
       }
@@ -896,6 +907,7 @@ extern "C" psgd_status psgd_clip_plan_create(const psgd_layer* layers, int32_t n
       }
       if (int64_t(plan->tiles.size()) > kMaxTiles) {
         delete plan;
+        plan = nullptr;
         return fail(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_create: too many tiles");
       }
       plan->layers.push_back(L);
@@ -948,7 +960,7 @@ extern "C" psgd_status psgd_clip_plan_create(const psgd_layer* layers, int32_t n
 }
 
 extern "C" psgd_status psgd_clip_plan_sizes(const psgd_clip_plan* plan, psgd_clip_sizes* out) {
-  if (plan == nullptr || out == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_sizes: NULL argument");
+  if (plan == nullptr || out == nullptr) return refuse(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_sizes: NULL argument");
   psgd_clip_sizes s{};
   s.n_layers = int32_t(plan->info.size());
   s.n_slices = plan->n_slices;
@@ -967,9 +979,9 @@ extern "C" psgd_status psgd_clip_plan_sizes(const psgd_clip_plan* plan, psgd_cli
 
 extern "C" psgd_status psgd_clip_plan_layer_info(const psgd_clip_plan* plan, int32_t layer,
                                                  psgd_clip_layer_info* out) {
-  if (plan == nullptr || out == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_layer_info: NULL argument");
+  if (plan == nullptr || out == nullptr) return refuse(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_layer_info: NULL argument");
   if (layer < 0 || size_t(layer) >= plan->info.size())
-    return fail(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_layer_info: layer index out of range");
+    return refuse(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_layer_info: layer index out of range");
   *out = plan->info[size_t(layer)];
   return PSGD_OK;
 }
@@ -987,8 +999,7 @@ extern "C" psgd_status psgd_clip_plan_destroy(psgd_clip_plan* plan) {
     const bool have = hipGetDevice(&cur) == hipSuccess;
     if (have && cur != kv.first) (void)hipSetDevice(kv.first);
     if (hipFree(kv.second) != hipSuccess) {
-      set_error("psgd_clip_plan_destroy: hipFree of the device tables failed");
-      st = PSGD_ERR_HIP;
+      st = refuse(PSGD_ERR_HIP, "psgd_clip_plan_destroy: hipFree of the device tables failed");
     }
     if (have && cur != kv.first) (void)hipSetDevice(cur);
   }
@@ -997,15 +1008,15 @@ extern "C" psgd_status psgd_clip_plan_destroy(psgd_clip_plan* plan) {
 }
 
 extern "C" psgd_status psgd_clip_plan_set_timing(psgd_clip_plan* plan, int32_t enable) {
-  if (plan == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_set_timing: plan is NULL");
+  if (plan == nullptr) return refuse(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_set_timing: plan is NULL");
   plan->timing = enable != 0;
   return PSGD_OK;
 }
 
 extern "C" psgd_status psgd_clip_plan_kernel_stats(psgd_clip_plan* plan, psgd_kernel_stat* out, int32_t capacity,
                                                    int32_t* count, int32_t reset) {
-  if (plan == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_kernel_stats: plan is NULL");
-  if (capacity > 0 && out == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_kernel_stats: out is NULL");
+  if (plan == nullptr) return refuse(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_kernel_stats: plan is NULL");
+  if (capacity > 0 && out == nullptr) return refuse(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_kernel_stats: out is NULL");
   psgd_status st = PSGD_OK;
   try {
     plan->event_pool.reserve(plan->event_pool.size() + 2 * plan->pending.size());

@@ -132,10 +132,16 @@ class _ClipSizes(ctypes.Structure):
                 ("clip_bytes", ctypes.c_uint64), ("adamw_bytes", ctypes.c_uint64)]
 
 
-class _AdamwConfig(ctypes.Structure):
+class AdamwConfig(ctypes.Structure):
+    """psgd_adamw_config (see include/psgd_clip.h for ranges)."""
+
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("max_norm", ctypes.c_double),
                 ("norm_kind", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+    def __init__(self, lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                 weight_decay: float = 0.01, max_norm: float = 0.0, norm_kind: int = PSGD_NORM_L2, flags: int = 0):
+        super().__init__(lr, beta1, beta2, eps, weight_decay, max_norm, norm_kind, flags)
 
 
 _lib = None
@@ -195,7 +201,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.psgd_clip_plan_destroy.argtypes = [vp]
     lib.psgd_grad_norm.argtypes = [vp, vp, i32, vp, vp, vp, vp]
     lib.psgd_grad_clip.argtypes = [vp, vp, vp, i32, f32, vp, vp, vp, vp]
-    lib.psgd_adamw_apply.argtypes = [vp, ctypes.POINTER(_AdamwConfig), vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.psgd_adamw_apply.argtypes = [vp, ctypes.POINTER(AdamwConfig), vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.psgd_clip_plan_set_timing.argtypes = [vp, i32]
     lib.psgd_clip_plan_kernel_stats.argtypes = [vp, ctypes.POINTER(_KernelStat), i32, ctypes.POINTER(i32), i32]
     for name in EXPORTED:
@@ -596,20 +602,6 @@ class ClipPlan:
                 pass
 
 
-@dataclass
-class AdamwConfig:
-    """psgd_adamw_config (see include/psgd_clip.h for ranges)."""
-
-    lr: float = 1e-3
-    beta1: float = 0.9
-    beta2: float = 0.999
-    eps: float = 1e-8
-    weight_decay: float = 0.01
-    max_norm: float = 0.0
-    norm_kind: int = PSGD_NORM_L2
-    flags: int = 0
-
-
 def psgd_clip_plan_create(shapes: Sequence[Tuple[int, int]], n_slices: int, grad_dtype: int = PSGD_F32,
                           flags: int = 0) -> ClipPlan:
     lib = load_library()
@@ -727,9 +719,7 @@ def psgd_adamw_apply(plan: ClipPlan, config: AdamwConfig, update, params, exp_av
 
     s, dev, f32 = plan.sizes, _call_device(update), torch.float32
     n = s["worker_stride"]
-    c = _AdamwConfig(config.lr, config.beta1, config.beta2, config.eps, config.weight_decay, config.max_norm,
-                     config.norm_kind, config.flags)
-    _enqueue(load_library().psgd_adamw_apply, dev, stream, plan.handle, ctypes.byref(c),
+    _enqueue(load_library().psgd_adamw_apply, dev, stream, plan.handle, ctypes.byref(config),
              _buffer("update", update, _grad_dtype(plan), n, dev), _buffer("params", params, f32, n, dev),
              _buffer("exp_avg", exp_avg, f32, n, dev), _buffer("exp_avg_sq", exp_avg_sq, f32, n, dev),
              None if params_bf16 is None else _buffer("params_bf16", params_bf16, torch.bfloat16, n, dev),
@@ -747,7 +737,7 @@ def pack(plan, per_layer: Sequence[np.ndarray], dtype=np.float32, workers: Optio
     update/momentum/params).  Returns (W, worker_stride) or (worker_stride,); padding is 0.
     """
     ld = plan.sizes["worker_stride"]
-    W = plan.sizes["n_workers"] if workers is None else workers
+    W = plan.sizes["n_slices" if isinstance(plan, ClipPlan) else "n_workers"] if workers is None else workers
     out = np.zeros((W, ld) if W else (ld,), dtype=dtype)
     idx = range(len(plan.layers)) if layers is None else layers
     for a, li in zip(per_layer, idx):

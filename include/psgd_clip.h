@@ -40,8 +40,10 @@
  * contents of a workspace need not be preserved between calls.
  *
  * Graphs.  Every call can be captured once the plan has run one call eagerly on that
- * device (the first call uploads the plan's tables; a capture before that is refused with
- * PSGD_ERR_INVALID_ARG).  The AdamW step count lives in device memory, so replays count.
+ * device (the first call uploads the plan's tables) and with kernel timing off; other
+ * captures are refused with PSGD_ERR_INVALID_ARG.  The AdamW step count lives in device
+ * memory, so replays count.  A graph reads the plan's tables and the buffers of the call
+ * it captured: all of them must outlive it.
  */
 #ifndef PSGD_CLIP_H_
 #define PSGD_CLIP_H_
@@ -83,7 +85,7 @@ psgd_status psgd_clip_plan_create(const psgd_layer* layers, int32_t n_layers, in
 psgd_status psgd_clip_plan_sizes(const psgd_clip_plan* plan, psgd_clip_sizes* out);
 psgd_status psgd_clip_plan_layer_info(const psgd_clip_plan* plan, int32_t layer, psgd_clip_layer_info* out);
 /* Free the plan and its device tables.  NULL is accepted.  No call using the plan may
- * still be running. */
+ * still be running, and no graph that captured one may be replayed afterwards. */
 psgd_status psgd_clip_plan_destroy(psgd_clip_plan* plan);
 
 /* Norm of every slice, and of every tensor of every slice:

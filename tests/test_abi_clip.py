@@ -5,6 +5,7 @@ fake addresses below are never dereferenced)."""
 import ctypes
 import math
 
+import numpy as np
 import pytest
 
 from distributed_sgd_gradient_ef_amd import psgd
@@ -122,8 +123,7 @@ def test_clip_rejects_bad_bounds(max_norm):
 
 def _adamw(plan, cfg, **bad):
     a = {**A, **bad}
-    c = psgd._AdamwConfig(cfg.lr, cfg.beta1, cfg.beta2, cfg.eps, cfg.weight_decay, cfg.max_norm, cfg.norm_kind, cfg.flags)
-    return psgd.load_library().psgd_adamw_apply(plan.handle, ctypes.byref(c), a["grads"], a["params"], a["exp_avg"],
+    return psgd.load_library().psgd_adamw_apply(plan.handle, ctypes.byref(cfg), a["grads"], a["params"], a["exp_avg"],
                                                 a["exp_avg_sq"], a["copy"], a["step"], a["norms"], a["workspace"], None)
 
 
@@ -156,6 +156,18 @@ def test_adamw_rejects_contradictions():
     assert _adamw(plan, psgd.AdamwConfig(max_norm=0.0, flags=psgd.PSGD_ADAMW_SKIP_NONFINITE), norms=None) == INVALID
     lib = psgd.load_library()
     assert lib.psgd_adamw_apply(plan.handle, None, *[0x1000] * 9) == INVALID
+
+
+def test_pack_roundtrip():
+    plan = psgd.psgd_clip_plan_create(SHAPES, 3)
+    rng = np.random.default_rng(1)
+    per = [rng.standard_normal((3,) + s).astype(np.float32) for s in SHAPES]
+    flat = psgd.pack(plan, per)
+    assert flat.shape == (3, plan.sizes["worker_stride"])
+    for li, a in enumerate(per):
+        assert np.array_equal(psgd.unpack(plan, flat, li), a)
+    one = psgd.pack(plan, [a[0] for a in per], workers=0)
+    assert np.array_equal(one, flat[0])
 
 
 def test_timing_calls_without_gpu():
