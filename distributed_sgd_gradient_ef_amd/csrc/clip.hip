@@ -2,8 +2,8 @@
 // side of psgd_clip.h.
 //
 // A tile is at most kTile consecutive elements of one tensor, a run is a number of
-// consecutive tiles.  Sums of squares are held in float64; every reduction has a fixed
-// order, and a norm is joined the same way wherever it is needed.
+// consecutive tiles.  Sums of squares are held in float64, and every reduction has a fixed
+// order (another one in each variant: their float64 sums may differ in the last bits).
 //
 //   cl_norm    per (run, slice): the sum of squares, or the largest magnitude
 //   cl_final   from these partials: the slices' norms and coefficients, the tensors' norms
@@ -35,13 +35,19 @@
 namespace psgd {
 namespace clip {
 
-constexpr int kTile = 8192;  // elements per tile
+// Elements per tile.  16384 ran alike on large plans; 8192 gives moderate ones more
+// workgroups.
+constexpr int kTile = 8192;
 constexpr int kThreads = 256;
-constexpr int64_t kMaxRuns = 4096;       // cl_norm workgroups per slice
-constexpr int64_t kTileCost = kTile;     // what a tile costs besides its elements, in elements
+// cl_norm workgroups per slice: cl_final's 256 threads then take at most 16 partials each.
+constexpr int64_t kMaxRuns = 4096;
+// What a tile costs cl_norm besides its elements, in elements: its loads start anew, so a
+// run of tiny tensors takes their latencies one after the other (119 tensors of 1 to 2
+// million elements: 17.8 us counted at 1024, 11.3 at 8192).
+constexpr int64_t kTileCost = kTile;
 // The norm pass leaves the last kKeepBytes it reads in the 256 MB memory-side cache
-// (ordinary loads; the rest is read with non-temporal ones, which run at 6.9 instead of
-// 6.1 TB/s), and the second pass goes backwards and finds them there.  Against no such
+// (ordinary loads; the rest is read with non-temporal ones, which run at 7.2 instead of
+// 6.4 TB/s), and the second pass goes backwards and finds them there.  Against no such
 // part: AdamW on a 45 MB update 65.3 instead of 70.2 us, clipping 715 MB 327 instead of
 // 332 us, 1.6 GB 732 instead of 740 us.  0, 64, 128, 160, 192, 224, 256 MB tried.
 constexpr int64_t kKeepBytes = int64_t(224) << 20;
@@ -143,7 +149,7 @@ typedef __bf16 v8b __attribute__((ext_vector_type(8)));
 // Vectors of NE elements in memory and in registers (always float32 there).  bfloat16
 // widens exactly and is rounded to nearest even by the hardware conversion, which keeps
 // NaN.  cl_norm and cl_scale move 16 bytes per lane: 4 float32 or 8 bfloat16 (with 4,
-// 8 bytes, scaling bfloat16 ran at 5.2 instead of 6.1 TB/s).
+// 8 bytes, scaling bfloat16 ran at 5.2 instead of 6.4 TB/s).
 template <typename T, int NE> struct Vec;
 template <> struct Vec<float, 4> { typedef v4f mem; typedef v4f reg; };
 template <> struct Vec<uint16_t, 4> { typedef v4b mem; typedef v4f reg; };

@@ -19,13 +19,14 @@
  * Precision.  Sums of squares are held in float64, so no float32 gradient overflows or
  * underflows them, and are added in a fixed order: equal calls give equal bits.  Norms
  * and coefficients are rounded once to float32 (a norm past its largest number becomes
- * infinite); a coefficient is taken from the float64 norm.  out is c * g in float32, rounded once to the gradient type.  The AdamW state is
- * float32 and its step size and bias corrections are formed in float64.
+ * infinite); a coefficient is taken from the float64 norm.  out is c * g in float32,
+ * rounded once to the gradient type.  The AdamW state is float32 and its step size and
+ * bias corrections are formed in float64.
  *
  * Non-finite gradients are not errors: an infinite entry gives an infinite norm, hence
- * c = 0 (finite entries become 0, infinite ones NaN); a NaN entry gives a NaN norm of
- * either kind, and NaN everywhere in what is scaled by it.  With
- * PSGD_ADAMW_SKIP_NONFINITE such an update changes nothing instead.
+ * c = 0 for every finite max_norm (finite entries become 0, infinite ones NaN); a NaN
+ * entry gives a NaN norm of either kind, and NaN everywhere in what is scaled by it.
+ * With PSGD_ADAMW_SKIP_NONFINITE such an update changes nothing instead.
  *
  * Memory layout, pointers, errors and ownership are those of psgd.h: a clip plan made
  * from a layer list has the layout (offsets, worker_stride) of every other plan made from

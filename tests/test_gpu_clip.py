@@ -678,3 +678,51 @@ def test_scaled_update_changes_nothing_but_the_norm():
     for a, b in zip(*results):
         a, b = (a[inside], b[inside]) if a.numel() > 1 else (a, b)
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("compressor", ["rtopk", "atomo"])
+def test_clip_and_adamw_around_the_other_compressors(compressor):
+    """Two steps: worker gradients clipped in place, compressed, AdamW from the update."""
+    shapes, W = [(20, 33), (33, 20), (1, 9)], 3
+    workers, one = psgd.psgd_clip_plan_create(shapes, W), psgd.psgd_clip_plan_create(shapes, 1)
+    n = one.sizes["worker_stride"]
+    rng = np.random.default_rng(50)
+    u, errors = torch.zeros(n, device=DEV), torch.zeros((W, n), device=DEV)
+    if compressor == "rtopk":
+        plan = psgd.psgd_rtopk_plan_create(shapes, [60, 70, 5], [30, 20, 5], W)
+        s = plan.sizes
+        index = torch.zeros((W, s["keep_total"]), dtype=torch.int32, device=DEV)
+        value = torch.zeros((W, s["keep_total"]), device=DEV)
+    else:
+        plan = psgd.psgd_atomo_plan_create(shapes, 1.5, W)
+        s = plan.sizes
+        sv = [torch.zeros((W, s["sv_total"]), device=DEV) for _ in range(2)]
+        index = torch.zeros((W, s["sv_total"]), dtype=torch.int32, device=DEV)
+        count = torch.zeros((W, s["n_matrices"]), dtype=torch.int32, device=DEV)
+        atoms = torch.zeros((W, s["atom_total"]), device=DEV)
+    ws = torch.zeros(s["workspace_bytes"], dtype=torch.uint8, device=DEV)
+
+    def compress(g):
+        if compressor == "rtopk":
+            ranks = psgd.pack_rows(plan, [np.stack([rng.permutation(t) for _ in range(W)]) for t in (60, 70, 5)], "top",
+                                   np.uint32).view(np.int32)
+            psgd.psgd_rtopk_step(plan, g, errors, torch.from_numpy(ranks).to(DEV), index, value, u, ws)
+        else:
+            x = torch.from_numpy(rng.random((W, s["sv_total"])).astype(np.float32)).to(DEV)
+            psgd.psgd_atomo_step(plan, g, x, sv[0], sv[1], index, count, atoms, u, ws)
+        torch.cuda.synchronize()  # the inputs above end with this call
+
+    x, m, v, t = _adamw_state(one, seed=51, step=0)
+    norms, coefs, norm = torch.zeros(W, device=DEV), torch.zeros(W, device=DEV), torch.zeros(1, device=DEV)
+    cfg = psgd.AdamwConfig(lr=1e-2, max_norm=0.1)
+    for step in range(2):
+        g = torch.nan_to_num(_grads(workers, torch.float32, seed=52 + step))
+        given = g.clone()
+        psgd.psgd_grad_clip(workers, g, g, psgd.PSGD_NORM_L2, 0.5, norms, coefs, _workspace(workers))
+        compress(g)
+        before = [a.clone() for a in (x, m, v)]
+        psgd.psgd_adamw_apply(one, cfg, u, x, m, v, None, t, norm, _workspace(one))
+        torch.cuda.synchronize()
+        _check_clip(workers, given, g, norms, coefs, "l2", 0.5)
+        assert bool((u != 0).any()) and int(t) == step + 1
+        _check_adamw(one, cfg, u, before, (x, m, v), step + 1, "l2")
