@@ -293,16 +293,19 @@ def test_adamw(name, dtype, max_norm, kind):
             _near(norm.cpu(), [O.norm_of_tensors(_tensors(plan, _values(g)), kind)], 1.001 * U)
 
 
-def test_adamw_skips_a_non_finite_update():
-    plan = psgd.psgd_clip_plan_create(SHAPE_SETS["mixed"], 1)
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("name", ["ends", "mixed", "large"])
+def test_adamw_skips_a_non_finite_update(name, kind):
+    plan = psgd.psgd_clip_plan_create(SHAPE_SETS[name], 1)
     ws = _workspace(plan)
-    cfg = psgd.AdamwConfig(max_norm=1.0, flags=psgd.PSGD_ADAMW_SKIP_NONFINITE)
+    cfg = psgd.AdamwConfig(max_norm=1.0, norm_kind=KINDS[kind], flags=psgd.PSGD_ADAMW_SKIP_NONFINITE)
     x, m, v, t = _adamw_state(plan, seed=10, step=3)
     norm = torch.zeros(1, device=DEV)
     copy = torch.full_like(x, 5.0, dtype=torch.bfloat16)
+    at = max(plan.layers, key=lambda L: L.numel)
     for bad in (math.nan, math.inf, -math.inf):
         g = _grads(plan, torch.float32, seed=11)[0]
-        g[plan.layers[5].offset + 1234] = bad
+        g[at.offset + at.numel - 1] = bad
         before = [a.clone() for a in (x, m, v, copy)]
         psgd.psgd_adamw_apply(plan, cfg, g, x, m, v, copy, t, norm, ws)
         assert int(t) == 3 and not torch.isfinite(norm).any()
@@ -311,7 +314,48 @@ def test_adamw_skips_a_non_finite_update():
     before = [a.clone() for a in (x, m, v)]
     psgd.psgd_adamw_apply(plan, cfg, g, x, m, v, copy, t, norm, ws)
     assert int(t) == 4
-    _check_adamw(plan, cfg, g, before, (x, m, v), 4, "l2", copy)
+    _check_adamw(plan, cfg, g, before, (x, m, v), 4, kind, copy)
+
+
+@pytest.mark.parametrize("name", ["ends", "mixed", "large"])
+@pytest.mark.parametrize("beta1,beta2,weight_decay", [(0.0, 0.0, 0.0), (0.0, 0.99, 0.1), (0.95, 0.0, 0.1)])
+def test_adamw_at_the_ends_of_its_ranges(name, beta1, beta2, weight_decay):
+    plan = psgd.psgd_clip_plan_create(SHAPE_SETS[name], 1)
+    g = _grads(plan, torch.float32, seed=60)[0]
+    cfg = psgd.AdamwConfig(lr=1e-2, beta1=beta1, beta2=beta2, weight_decay=weight_decay, max_norm=0.5)
+    x, m, v, t = _adamw_state(plan, seed=61, step=1)
+    before = [a.clone() for a in (x, m, v)]
+    psgd.psgd_adamw_apply(plan, cfg, g, x, m, v, None, t, torch.zeros(1, device=DEV), _workspace(plan))
+    assert int(t) == 2
+    _check_adamw(plan, cfg, g, before, (x, m, v), 2, "l2")
+    # a rate of zero moves the moments and the count, not the weights
+    cfg = psgd.AdamwConfig(lr=0.0, beta1=beta1, beta2=beta2, weight_decay=weight_decay)
+    before = x.clone()
+    psgd.psgd_adamw_apply(plan, cfg, g, x, m, v, None, t, None, _workspace(plan))
+    assert int(t) == 3 and torch.equal(_bits(x), _bits(before))
+
+
+@pytest.mark.parametrize("name", ["ends", "mixed", "large"])
+def test_outputs_need_only_their_types_alignment(name):
+    W = 3
+    plan, one = psgd.psgd_clip_plan_create(SHAPE_SETS[name], W), psgd.psgd_clip_plan_create(SHAPE_SETS[name], 1)
+    n = len(plan.layers)
+    g = _grads(plan, torch.float32, seed=62)
+    norms, coefs = torch.full((W + 2,), 9.0, device=DEV), torch.full((W + 2,), 9.0, device=DEV)
+    per = torch.full((W * n + 2,), 9.0, device=DEV)
+    psgd.psgd_grad_norm(plan, g, psgd.PSGD_NORM_L2, norms[1:W + 1], per[1:W * n + 1], _workspace(plan))
+    rows = _values(g)
+    _near(norms[1:-1].cpu(), [O.norm_of_tensors(_tensors(plan, r), "l2") for r in rows], 1.001 * U)
+    _near(per[1:-1].cpu(), [O.norm(t, "l2") for r in rows for t in _tensors(plan, r)], 1.001 * U)
+    out = torch.zeros_like(g)
+    psgd.psgd_grad_clip(plan, g, out, psgd.PSGD_NORM_L2, 0.5, norms[1:W + 1], coefs[1:W + 1], _workspace(plan))
+    _check_clip(plan, g, out, norms[1:-1], coefs[1:-1], "l2", 0.5)
+    x, m, v, _ = _adamw_state(one, seed=63, step=0)
+    steps = torch.tensor([7, 7, 7], dtype=torch.int64, device=DEV)
+    psgd.psgd_adamw_apply(one, psgd.AdamwConfig(max_norm=1.0), g[0], x, m, v, None, steps[1:2], norms[W + 1:],
+                          _workspace(one))
+    assert steps.tolist() == [7, 8, 7]
+    assert all(float(a[0]) == 9.0 for a in (norms, coefs, per)) and float(coefs[-1]) == float(per[-1]) == 9.0
 
 
 def test_adamw_of_a_non_finite_update_spreads_it_without_the_flag():
