@@ -394,7 +394,7 @@ __global__ __launch_bounds__(kThreads) void cl_scale(const ClTile* __restrict__ 
   }
 }
 
-// Four elements per thread, as in cl_scale: four (five) streams at 6.3 to 6.6 TB/s.  45 MB of
+// Four elements per thread, as in cl_scale: seven (eight) streams at 6.1 to 6.6 TB/s.  45 MB of
 // update in 50 us, 1.6 GB in 1.80 ms (64 KB per workgroup: 67 us, 2.11 ms).
 // CLIP: 0 no clipping (c = 1), 1 cl_final's coefficient, 2 from the partials.
 template <typename GT, typename N, int CLIP>
