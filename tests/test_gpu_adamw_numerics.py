@@ -1,0 +1,58 @@
+"""AdamW where its numbers get long: averages over many steps.  Against
+float64, with u = 2^-24 (half a float32 step); tolerances are derived beside each test.  The
+element counts take the single launch, the joined partials and cl_final."""
+
+import math
+
+import pytest
+
+from distributed_sgd_gradient_ef_amd import psgd
+from tests.test_gpu_clip import DEV, U, _workspace
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+SIZES = {"single": 8000, "joined": 65536, "final": 2_200_000}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def library():
+    if not torch.cuda.is_available():
+        pytest.skip("no ROCm GPU visible")
+    return psgd.load_library()
+
+
+@pytest.mark.parametrize("beta", [0.9999, 0.99999])
+@pytest.mark.parametrize("max_norm", [0.0, math.inf])
+@pytest.mark.parametrize("size", SIZES)
+def test_moments_stay_the_average_of_the_gradients(size, max_norm, beta):
+    """2000 steps on random gradients, from moments at their steady state.
+
+    Each step rounds a moment once by at most u of it; on random gradients these roundings
+    are independent and have mean zero.  So the mean over n elements is off by at most
+    1.5 u sqrt(2 T ln(2e9) / n) but for one case in 1e9 (Hoeffding; 1.5 bounds an element's
+    moment against the mean).  One-sided are only the new gradient's weight and products:
+    3 u.  A pair of weights that does not add up to 1, or not to the step's beta, drifts by
+    up to u / 2 every step: hundreds of u."""
+    n, steps = SIZES[size], 2000
+    plan = psgd.psgd_clip_plan_create([(1, n)], 1)
+    ld = plan.sizes["worker_stride"]
+    gen = torch.Generator(device=DEV).manual_seed(71)
+    cfg = psgd.AdamwConfig(lr=1e-3, beta1=beta, beta2=beta, max_norm=max_norm)
+    x, m, v = torch.zeros(ld, device=DEV), torch.full((ld,), 1.5, device=DEV), torch.full((ld,), 2.5, device=DEV)
+    m64, v64 = m[:n].double(), v[:n].double()
+    t = torch.full((1,), 10 ** 6, dtype=torch.int64, device=DEV)
+    norm, ws = torch.zeros(1, device=DEV) if max_norm else None, _workspace(plan)
+    for _ in range(steps):
+        g = torch.randn(ld, generator=gen, device=DEV) * 0.5 + 1.5
+        psgd.psgd_adamw_apply(plan, cfg, g, x, m, v, None, t, norm, ws)
+        d = g[:n].double()
+        m64.mul_(beta).add_(d, alpha=1.0 - beta)
+        v64.mul_(beta).addcmul_(d, d, value=1.0 - beta)
+    tol = (3.0 + 1.5 * math.sqrt(2 * steps * math.log(2e9) / n)) * U
+    for got, want in ((m, m64), (v, v64)):
+        mean = float(want.mean())
+        assert float(want.max()) <= 1.5 * mean
+        off = float((got[:n].double() - want).mean()) / mean
+        assert abs(off) <= tol, (off / U, tol / U)
