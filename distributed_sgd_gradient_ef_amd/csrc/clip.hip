@@ -234,12 +234,13 @@ __device__ __forceinline__ AwState step_scalars(const AwArgs& aw) {
 }
 
 // Four elements' AdamW update: the new x, m and v in place of the old.  The moments are
-// averaged in float64 and rounded once; that costs nothing next to the loads.
+// averaged in float64 and rounded once; that costs nothing next to the loads.  In float32
+// g^2 would be infinite from 1.8e19 on, where (1 - beta2) g^2 is not.
 __device__ __forceinline__ void adamw4(v4f g, v4f& x, v4f& m, v4f& v, const AwState& s, const AwConfig& cf, float decay) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     m[j] = float(cf.beta1 * double(m[j]) + cf.om_beta1 * double(g[j]));
-    v[j] = float(cf.beta2 * double(v[j]) + cf.om_beta2 * double(g[j] * g[j]));
+    v[j] = float(cf.beta2 * double(v[j]) + cf.om_beta2 * (double(g[j]) * double(g[j])));
     const float den = sqrtf(v[j]) * s.inv_sqrt + cf.eps;
     x[j] = fmaf(-decay, x[j], x[j]) - s.step_size * (m[j] / den);
   }

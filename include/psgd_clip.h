@@ -28,7 +28,10 @@
  * Non-finite gradients are not errors: an infinite entry gives an infinite norm, hence
  * c = 0 for every finite max_norm (finite entries become 0, infinite ones NaN); a NaN
  * entry gives a NaN norm of either kind, and NaN everywhere in what is scaled by it.
- * With PSGD_ADAMW_SKIP_NONFINITE such an update changes nothing instead.
+ * With PSGD_ADAMW_SKIP_NONFINITE such an update changes nothing instead.  A finite update is
+ * never skipped by the flag unless its norm is past float32's largest number; where it makes
+ * v infinite (|c U| above about sqrt(3.4e38 / (1 - beta2)), 5.8e20 at beta2 = 0.999), v stays
+ * so and the weight takes no further step but its decay.
  *
  * Memory layout, pointers, errors and ownership are those of psgd.h: a clip plan made
  * from a layer list has the layout (offsets, worker_stride) of every other plan made from

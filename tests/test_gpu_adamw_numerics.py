@@ -1,13 +1,14 @@
-"""AdamW where its numbers get long: averages over many steps.  Against
-float64, with u = 2^-24 (half a float32 step); tolerances are derived beside each test.  The
-element counts take the single launch, the joined partials and cl_final."""
+"""AdamW where its numbers get long: averages over many steps, large gradients.
+Against float64, with u = 2^-24 (half a float32 step); tolerances are derived beside
+each test.  The element counts take the single launch, the joined partials and cl_final."""
 
 import math
 
+import numpy as np
 import pytest
 
 from distributed_sgd_gradient_ef_amd import psgd
-from tests.test_gpu_clip import DEV, U, _workspace
+from tests.test_gpu_clip import DEV, DTYPES, U, _adamw_state, _check_adamw, _padding, _workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +57,49 @@ def test_moments_stay_the_average_of_the_gradients(size, max_norm, beta):
         assert float(want.max()) <= 1.5 * mean
         off = float((got[:n].double() - want).mean()) / mean
         assert abs(off) <= tol, (off / U, tol / U)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("max_norm,flags", [(0.0, 0), (math.inf, psgd.PSGD_ADAMW_SKIP_NONFINITE)])
+@pytest.mark.parametrize("size", SIZES)
+def test_second_moment_of_large_gradients(size, max_norm, flags, dtype):
+    """g^2 is past float32's range, (1 - beta2) g^2 is not (to _check_adamw's tolerances)."""
+    code, td = DTYPES[dtype]
+    n = SIZES[size]
+    plan = psgd.psgd_clip_plan_create([(1, n)], 1, code)
+    rng = np.random.default_rng(72)
+    a = 1e20 * (1.0 + rng.random(plan.sizes["worker_stride"])) * rng.choice([-1.0, 1.0], plan.sizes["worker_stride"])
+    g = torch.from_numpy(a.astype(np.float32)).to(td).to(DEV)
+    cfg = psgd.AdamwConfig(lr=1e-2, max_norm=max_norm, flags=flags)
+    for step in (0, 3):
+        x, m, v, t = _adamw_state(plan, seed=73, step=step)
+        before = [b.clone() for b in (x, m, v)]
+        norm = torch.zeros(1, device=DEV) if max_norm else None
+        psgd.psgd_adamw_apply(plan, cfg, g, x, m, v, None, t, norm, _workspace(plan))
+        assert int(t) == step + 1
+        inside = torch.from_numpy(~_padding(plan)).to(DEV)
+        assert bool(torch.isfinite(v[inside]).all())
+        _check_adamw(plan, cfg, g, before, (x, m, v), step + 1, "l2")
+
+
+@pytest.mark.parametrize("beta2", [0.5, 0.999])
+@pytest.mark.parametrize("size", SIZES)
+def test_an_infinite_second_moment_stays_infinite(size, beta2):
+    """beta2 * inf is inf for every beta2, also one that float32 holds exactly: the weight
+    only decays (1 - 2^-4, exact), and its neighbours take their step."""
+    n = SIZES[size]
+    plan = psgd.psgd_clip_plan_create([(1, n)], 1)
+    ld = plan.sizes["worker_stride"]
+    g, x = torch.ones(ld, device=DEV), torch.ones(ld, device=DEV)
+    m, v = torch.zeros(ld, device=DEV), torch.zeros(ld, device=DEV)
+    bad = torch.zeros(ld, dtype=torch.bool, device=DEV)
+    bad[[0, 70, n - 1]] = True
+    v[bad] = math.inf
+    t = torch.zeros(1, dtype=torch.int64, device=DEV)
+    cfg = psgd.AdamwConfig(lr=0.125, beta1=0.5, beta2=beta2, weight_decay=0.5)
+    psgd.psgd_adamw_apply(plan, cfg, g, x, m, v, None, t, None, _workspace(plan))
+    assert bool((v[bad] == math.inf).all()) and bool((x[bad] == 0.9375).all()) and bool((m[:n] == 0.5).all())
+    rest = ~bad
+    rest[n:] = False
+    # 1 - 2^-4 - lr / (1 + 1e-8): a step within 17 u of itself and three roundings below 1
+    assert bool(((x[rest] - 0.8125).abs() <= 5 * U + 17 * U * 0.125 + 2e-9).all())
