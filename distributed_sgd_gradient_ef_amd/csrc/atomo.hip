@@ -47,7 +47,7 @@
 #include <cmath>
 #include <cstdio>
 #include <map>
-#include <new>
+#include <memory>
 #include <string>
 #include <vector>
 
@@ -2029,10 +2029,13 @@ psgd_status device_tables(psgd_atomo_plan* plan, DevTables* out) {
   const uint64_t be = a256(plan->eig_items.size() * sizeof(int32_t) + 1);
   auto it = plan->dev.find(dev);
   if (it == plan->dev.end()) {
+    it = plan->dev.emplace(dev, nullptr).first;
     void* base = nullptr;
     e = hipMalloc(&base, bm + bg + bf + bu + bl + be);
-    if (e != hipSuccess)
+    if (e != hipSuccess) {
+      plan->dev.erase(it);
       return fail(PSGD_ERR_NO_MEMORY, std::string("hipMalloc of the plan's device tables: ") + hipGetErrorString(e));
+    }
     char* b = static_cast<char*>(base);
     e = hipMemcpy(b, plan->mats.data(), plan->mats.size() * sizeof(AtMat), hipMemcpyHostToDevice);
     if (e == hipSuccess)
@@ -2051,9 +2054,10 @@ psgd_status device_tables(psgd_atomo_plan* plan, DevTables* out) {
                     hipMemcpyHostToDevice);
     if (e != hipSuccess) {
       (void)hipFree(base);
+      plan->dev.erase(it);
       return hip_fail("hipMemcpy of the plan's device tables", e);
     }
-    it = plan->dev.emplace(dev, base).first;
+    it->second = base;
   }
   char* b = static_cast<char*>(it->second);
   out->mats = reinterpret_cast<AtMat*>(b);
@@ -2083,6 +2087,7 @@ psgd_status launch(psgd_atomo_plan* plan, int kid, void (*kernel)(KArgs...), dim
   if (grid.x == 0 || grid.y == 0) return PSGD_OK;
   hipEvent_t a = nullptr, b = nullptr;
   if (plan->timing) {
+    room_for_timing(plan);
     psgd_status s = take_event(plan, &a);
     if (s == PSGD_OK) s = take_event(plan, &b);
     if (s != PSGD_OK) {
@@ -2118,7 +2123,7 @@ using namespace psgd;
 using namespace psgd::atm;
 
 extern "C" psgd_status psgd_atomo_plan_create(const psgd_layer* layers, int32_t n_layers, double budget,
-                                              int32_t n_workers, uint32_t flags, psgd_atomo_plan** out) {
+                                              int32_t n_workers, uint32_t flags, psgd_atomo_plan** out) try {
   static const char* fn = "psgd_atomo_plan_create";
   if (out == nullptr) return fail(PSGD_ERR_INVALID_ARG, std::string(fn) + ": out is NULL");
   *out = nullptr;
@@ -2129,151 +2134,142 @@ extern "C" psgd_status psgd_atomo_plan_create(const psgd_layer* layers, int32_t 
   if (!(budget > 0.0) || !std::isfinite(budget) || budget > 1e30)
     return fail(PSGD_ERR_INVALID_ARG, std::string(fn) + ": budget must be positive and finite");
   if (flags != 0u) return fail(PSGD_ERR_UNSUPPORTED, std::string(fn) + ": flags must be 0");
-  psgd_atomo_plan* plan = nullptr;
-  try {
-    plan = new psgd_atomo_plan();
-    plan->n_workers = n_workers;
-    plan->budget = budget;
-    int64_t off = 0, sv = 0, atom = 0, gram = 0, refl = 0;
-    for (int32_t i = 0; i < n_layers; ++i) {
-      const int64_t rows = layers[i].rows, cols = layers[i].cols;
-      if (rows < 1 || cols < 1 || rows > (int64_t(1) << 31) || cols > (int64_t(1) << 31) ||
-          rows * cols > int64_t(0x7fffffff)) {
-        delete plan;
-        return fail(PSGD_ERR_INVALID_ARG, std::string(fn) + ": layer " + std::to_string(i) +
-                                              " must have 1 <= rows, cols and rows * cols < 2^31");
+  std::unique_ptr<psgd_atomo_plan> plan(new psgd_atomo_plan());
+  plan->n_workers = n_workers;
+  plan->budget = budget;
+  int64_t off = 0, sv = 0, atom = 0, gram = 0, refl = 0;
+  for (int32_t i = 0; i < n_layers; ++i) {
+    const int64_t rows = layers[i].rows, cols = layers[i].cols;
+    if (rows < 1 || cols < 1 || rows > (int64_t(1) << 31) || cols > (int64_t(1) << 31) ||
+        rows * cols > int64_t(0x7fffffff)) {
+      return fail(PSGD_ERR_INVALID_ARG, std::string(fn) + ": layer " + std::to_string(i) +
+                                            " must have 1 <= rows, cols and rows * cols < 2^31");
+    }
+    psgd_atomo_layer_info li{};
+    li.rows = rows;
+    li.cols = cols;
+    li.numel = rows * cols;
+    li.offset = off;
+    li.matrix_index = -1;
+    const int64_t k = std::min(rows, cols);
+    if (k >= 2) {
+      if (k > kMaxK) {
+        return fail(PSGD_ERR_UNSUPPORTED, std::string(fn) + ": layer " + std::to_string(i) +
+                                              " has min(rows, cols) above PSGD_ATOMO_MAX_K");
       }
-      psgd_atomo_layer_info li{};
-      li.rows = rows;
-      li.cols = cols;
-      li.numel = rows * cols;
-      li.offset = off;
-      li.matrix_index = -1;
-      const int64_t k = std::min(rows, cols);
-      if (k >= 2) {
-        if (k > kMaxK) {
-          delete plan;
-          return fail(PSGD_ERR_UNSUPPORTED, std::string(fn) + ": layer " + std::to_string(i) +
-                                                " has min(rows, cols) above PSGD_ATOMO_MAX_K");
-        }
-        li.compressed = 1;
-        li.matrix_index = int32_t(plan->mats.size());
-        li.k = k;
-        li.sv_offset = sv;
-        li.atom_offset = atom;
-        AtMat m{};
-        m.offset = off;
-        m.sv_off = sv;
-        m.atom_off = atom;
-        m.b_off = gram;
-        m.r_off = refl;
-        m.rows = int32_t(rows);
-        m.cols = int32_t(cols);
-        m.k = int32_t(k);
-        m.left = rows <= cols ? 1 : 0;
-        m.mat_index = li.matrix_index;
-        plan->mats.push_back(m);
-        sv += k;
-        atom += k * (rows + cols);
-        gram += (k * k + 63) / 64 * 64;
-        refl += (chase_block(int(k)) + 63) / 64 * 64;
-        plan->max_k = std::max(plan->max_k, int32_t(k));
-      }
-      plan->info.push_back(li);
-      off += (li.numel + 63) / 64 * 64;
+      li.compressed = 1;
+      li.matrix_index = int32_t(plan->mats.size());
+      li.k = k;
+      li.sv_offset = sv;
+      li.atom_offset = atom;
+      AtMat m{};
+      m.offset = off;
+      m.sv_off = sv;
+      m.atom_off = atom;
+      m.b_off = gram;
+      m.r_off = refl;
+      m.rows = int32_t(rows);
+      m.cols = int32_t(cols);
+      m.k = int32_t(k);
+      m.left = rows <= cols ? 1 : 0;
+      m.mat_index = li.matrix_index;
+      plan->mats.push_back(m);
+      sv += k;
+      atom += k * (rows + cols);
+      gram += (k * k + 63) / 64 * 64;
+      refl += (chase_block(int(k)) + 63) / 64 * 64;
+      plan->max_k = std::max(plan->max_k, int32_t(k));
     }
-    plan->worker_stride = off;
-    plan->sv_total = sv;
-    plan->atom_total = atom;
-    plan->gram_total = gram;
-    plan->refl_total = refl;
-    plan->numel = 0;
-    const uint64_t W = uint64_t(n_workers);
-    uint64_t model = 0;
-    for (const auto& li : plan->info) {
-      plan->numel += li.numel;
-      model += (li.compressed ? 8 * W + 4 : 4 * W + 4) * uint64_t(li.numel);
-    }
-    plan->model_bytes = model;
-    // tiles
-    for (size_t mi = 0; mi < plan->mats.size(); ++mi) {
-      const AtMat& m = plan->mats[mi];
-      const int nt = (m.k + kGramTile - 1) / kGramTile;
-      for (int ti = 0; ti < nt; ++ti)
-        for (int tj = 0; tj <= ti; ++tj) plan->gtiles.push_back(GramTile{int32_t(mi), ti, tj, 0});
-      if (m.left) {
-        for (int c = 0; c < m.cols; c += kFactorThreads)
-          plan->ftiles.push_back(FactorTile{int32_t(mi), c, std::min(m.cols, c + kFactorThreads), 0});
-      } else {
-        const int rows_per = 4 * (kFactorThreads / 64);
-        for (int r = 0; r < m.rows; r += rows_per)
-          plan->ftiles.push_back(FactorTile{int32_t(mi), r, std::min(m.rows, r + rows_per), 0});
-      }
-      for (int r = 0; r < m.rows; r += kAtUpdRows)
-        for (int c = 0; c < m.cols; c += kAtUpdThreads)
-          plan->utiles.push_back(AtUpdTile{0, 0, int32_t(mi), r, std::min(m.rows, r + kAtUpdRows), c});
-    }
-    // the longest contractions first, so that they do not form the launch's tail (each
-    // tile writes its own block of the Gram matrix; the order changes no result)
-    std::stable_sort(plan->gtiles.begin(), plan->gtiles.end(), [&](const GramTile& a, const GramTile& b) {
-      const AtMat& ma = plan->mats[size_t(a.mat)];
-      const AtMat& mb = plan->mats[size_t(b.mat)];
-      return (ma.left ? ma.cols : ma.rows) > (mb.left ? mb.cols : mb.rows);
-    });
-    if (plan->gtiles.size() > 65535) {  // the Gram launch's second grid dimension
-      delete plan;
-      return fail(PSGD_ERR_UNSUPPORTED, std::string(fn) + ": more than 65535 Gram tiles (128 x 128) in one plan");
-    }
-    // the largest factor tiles first (rows x columns each covers), for the same reason
-    std::stable_sort(plan->ftiles.begin(), plan->ftiles.end(), [&](const FactorTile& a, const FactorTile& b) {
-      const AtMat& ma = plan->mats[size_t(a.mat)];
-      const AtMat& mb = plan->mats[size_t(b.mat)];
-      const int64_t wa = int64_t(a.end - a.begin) * (ma.left ? ma.rows : ma.cols);
-      const int64_t wb = int64_t(b.end - b.begin) * (mb.left ? mb.rows : mb.cols);
-      return wa > wb;
-    });
-    if (plan->ftiles.size() > 65535) {  // the factor launch's second grid dimension
-      delete plan;
-      return fail(PSGD_ERR_UNSUPPORTED, std::string(fn) + ": more than 65535 factor tiles in one plan");
-    }
-    for (size_t mi = 0; mi < plan->mats.size(); ++mi) plan->tri_list.push_back(int32_t(mi));
-    std::stable_sort(plan->tri_list.begin(), plan->tri_list.end(),
-                     [&](int32_t x, int32_t y) { return plan->mats[size_t(x)].k > plan->mats[size_t(y)].k; });
-    static_assert(kMaxK / kEigSlots <= 16, "a slice index fits four bits");
-    for (const int32_t mi : plan->tri_list)
-      for (int sl = 0; sl * kEigSlots < plan->mats[size_t(mi)].k; ++sl) plan->eig_items.push_back(mi * 16 + sl);
-    if (plan->eig_items.size() > 65535) {  // the eigenvalue launch's second grid dimension
-      delete plan;
-      return fail(PSGD_ERR_UNSUPPORTED, std::string(fn) + ": more than 65535 eigenvalue slices in one plan");
-    }
-    for (const auto& li : plan->info)
-      if (!li.compressed)
-        for (int64_t b = 0; b < li.numel; b += 4096)
-          plan->utiles.push_back(AtUpdTile{li.offset + b, li.offset + std::min(li.numel, b + 4096), -1, 0, 0, 0});
-    // workspace
-    uint64_t ws = 0;
-    plan->ws_gram = ws;
-    ws = a256(ws + W * uint64_t(gram) * 4);
-    plan->ws_y = ws;
-    ws = a256(ws + W * uint64_t(gram) * 4);
-    plan->ws_refl = ws;
-    ws = a256(ws + W * uint64_t(refl) * 4);
-    plan->ws_d = ws;
-    ws = a256(ws + W * uint64_t(sv) * 4);
-    plan->ws_e = ws;
-    ws = a256(ws + W * uint64_t(sv) * 4);
-    plan->ws_lam = ws;
-    ws = a256(ws + W * uint64_t(sv) * 4);
-    plan->workspace_bytes = std::max<uint64_t>(ws, 256);
-  } catch (const std::bad_alloc&) {
-    delete plan;
-    return fail(PSGD_ERR_NO_MEMORY, std::string(fn) + ": out of host memory");
+    plan->info.push_back(li);
+    off += (li.numel + 63) / 64 * 64;
   }
-  *out = plan;
+  plan->worker_stride = off;
+  plan->sv_total = sv;
+  plan->atom_total = atom;
+  plan->gram_total = gram;
+  plan->refl_total = refl;
+  plan->numel = 0;
+  const uint64_t W = uint64_t(n_workers);
+  uint64_t model = 0;
+  for (const auto& li : plan->info) {
+    plan->numel += li.numel;
+    model += (li.compressed ? 8 * W + 4 : 4 * W + 4) * uint64_t(li.numel);
+  }
+  plan->model_bytes = model;
+  // tiles
+  for (size_t mi = 0; mi < plan->mats.size(); ++mi) {
+    const AtMat& m = plan->mats[mi];
+    const int nt = (m.k + kGramTile - 1) / kGramTile;
+    for (int ti = 0; ti < nt; ++ti)
+      for (int tj = 0; tj <= ti; ++tj) plan->gtiles.push_back(GramTile{int32_t(mi), ti, tj, 0});
+    if (m.left) {
+      for (int c = 0; c < m.cols; c += kFactorThreads)
+        plan->ftiles.push_back(FactorTile{int32_t(mi), c, std::min(m.cols, c + kFactorThreads), 0});
+    } else {
+      const int rows_per = 4 * (kFactorThreads / 64);
+      for (int r = 0; r < m.rows; r += rows_per)
+        plan->ftiles.push_back(FactorTile{int32_t(mi), r, std::min(m.rows, r + rows_per), 0});
+    }
+    for (int r = 0; r < m.rows; r += kAtUpdRows)
+      for (int c = 0; c < m.cols; c += kAtUpdThreads)
+        plan->utiles.push_back(AtUpdTile{0, 0, int32_t(mi), r, std::min(m.rows, r + kAtUpdRows), c});
+  }
+  // the longest contractions first, so that they do not form the launch's tail (each
+  // tile writes its own block of the Gram matrix; the order changes no result)
+  std::stable_sort(plan->gtiles.begin(), plan->gtiles.end(), [&](const GramTile& a, const GramTile& b) {
+    const AtMat& ma = plan->mats[size_t(a.mat)];
+    const AtMat& mb = plan->mats[size_t(b.mat)];
+    return (ma.left ? ma.cols : ma.rows) > (mb.left ? mb.cols : mb.rows);
+  });
+  if (plan->gtiles.size() > 65535) {  // the Gram launch's second grid dimension
+    return fail(PSGD_ERR_UNSUPPORTED, std::string(fn) + ": more than 65535 Gram tiles (128 x 128) in one plan");
+  }
+  // the largest factor tiles first (rows x columns each covers), for the same reason
+  std::stable_sort(plan->ftiles.begin(), plan->ftiles.end(), [&](const FactorTile& a, const FactorTile& b) {
+    const AtMat& ma = plan->mats[size_t(a.mat)];
+    const AtMat& mb = plan->mats[size_t(b.mat)];
+    const int64_t wa = int64_t(a.end - a.begin) * (ma.left ? ma.rows : ma.cols);
+    const int64_t wb = int64_t(b.end - b.begin) * (mb.left ? mb.rows : mb.cols);
+    return wa > wb;
+  });
+  if (plan->ftiles.size() > 65535) {  // the factor launch's second grid dimension
+    return fail(PSGD_ERR_UNSUPPORTED, std::string(fn) + ": more than 65535 factor tiles in one plan");
+  }
+  for (size_t mi = 0; mi < plan->mats.size(); ++mi) plan->tri_list.push_back(int32_t(mi));
+  std::stable_sort(plan->tri_list.begin(), plan->tri_list.end(),
+                   [&](int32_t x, int32_t y) { return plan->mats[size_t(x)].k > plan->mats[size_t(y)].k; });
+  static_assert(kMaxK / kEigSlots <= 16, "a slice index fits four bits");
+  for (const int32_t mi : plan->tri_list)
+    for (int sl = 0; sl * kEigSlots < plan->mats[size_t(mi)].k; ++sl) plan->eig_items.push_back(mi * 16 + sl);
+  if (plan->eig_items.size() > 65535) {  // the eigenvalue launch's second grid dimension
+    return fail(PSGD_ERR_UNSUPPORTED, std::string(fn) + ": more than 65535 eigenvalue slices in one plan");
+  }
+  for (const auto& li : plan->info)
+    if (!li.compressed)
+      for (int64_t b = 0; b < li.numel; b += 4096)
+        plan->utiles.push_back(AtUpdTile{li.offset + b, li.offset + std::min(li.numel, b + 4096), -1, 0, 0, 0});
+  // workspace
+  uint64_t ws = 0;
+  plan->ws_gram = ws;
+  ws = a256(ws + W * uint64_t(gram) * 4);
+  plan->ws_y = ws;
+  ws = a256(ws + W * uint64_t(gram) * 4);
+  plan->ws_refl = ws;
+  ws = a256(ws + W * uint64_t(refl) * 4);
+  plan->ws_d = ws;
+  ws = a256(ws + W * uint64_t(sv) * 4);
+  plan->ws_e = ws;
+  ws = a256(ws + W * uint64_t(sv) * 4);
+  plan->ws_lam = ws;
+  ws = a256(ws + W * uint64_t(sv) * 4);
+  plan->workspace_bytes = std::max<uint64_t>(ws, 256);
+  *out = plan.release();
   return PSGD_OK;
+} catch (...) {
+  return no_memory();
 }
 
-extern "C" psgd_status psgd_atomo_plan_sizes(const psgd_atomo_plan* plan, psgd_atomo_sizes* out) {
+extern "C" psgd_status psgd_atomo_plan_sizes(const psgd_atomo_plan* plan, psgd_atomo_sizes* out) try {
   if (plan == nullptr || out == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_atomo_plan_sizes: NULL argument");
   psgd_atomo_sizes s{};
   s.n_layers = int32_t(plan->info.size());
@@ -2288,16 +2284,20 @@ extern "C" psgd_status psgd_atomo_plan_sizes(const psgd_atomo_plan* plan, psgd_a
   s.budget = plan->budget;
   *out = s;
   return PSGD_OK;
+} catch (...) {
+  return no_memory();
 }
 
 extern "C" psgd_status psgd_atomo_plan_layer_info(const psgd_atomo_plan* plan, int32_t layer,
-                                                  psgd_atomo_layer_info* out) {
+                                                  psgd_atomo_layer_info* out) try {
   if (plan == nullptr || out == nullptr)
     return fail(PSGD_ERR_INVALID_ARG, "psgd_atomo_plan_layer_info: NULL argument");
   if (layer < 0 || size_t(layer) >= plan->info.size())
     return fail(PSGD_ERR_INVALID_ARG, "psgd_atomo_plan_layer_info: layer index out of range");
   *out = plan->info[size_t(layer)];
   return PSGD_OK;
+} catch (...) {
+  return no_memory();
 }
 
 extern "C" psgd_status psgd_atomo_plan_destroy(psgd_atomo_plan* plan) {
@@ -2313,8 +2313,7 @@ extern "C" psgd_status psgd_atomo_plan_destroy(psgd_atomo_plan* plan) {
     const bool have = hipGetDevice(&cur) == hipSuccess;
     if (have && cur != kv.first) (void)hipSetDevice(kv.first);
     if (hipFree(kv.second) != hipSuccess) {
-      set_error("psgd_atomo_plan_destroy: hipFree of the device tables failed");
-      st = PSGD_ERR_HIP;
+      st = refuse(PSGD_ERR_HIP, "psgd_atomo_plan_destroy: hipFree of the device tables failed");
     }
     if (have && cur != kv.first) (void)hipSetDevice(cur);
   }
@@ -2322,32 +2321,19 @@ extern "C" psgd_status psgd_atomo_plan_destroy(psgd_atomo_plan* plan) {
   return st;
 }
 
-extern "C" psgd_status psgd_atomo_plan_set_timing(psgd_atomo_plan* plan, int32_t enable) {
+extern "C" psgd_status psgd_atomo_plan_set_timing(psgd_atomo_plan* plan, int32_t enable) try {
   if (plan == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_atomo_plan_set_timing: plan is NULL");
   plan->timing = enable != 0;
   return PSGD_OK;
+} catch (...) {
+  return no_memory();
 }
 
 extern "C" psgd_status psgd_atomo_plan_kernel_stats(psgd_atomo_plan* plan, psgd_kernel_stat* out, int32_t capacity,
-                                                    int32_t* count, int32_t reset) {
+                                                    int32_t* count, int32_t reset) try {
   if (plan == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_atomo_plan_kernel_stats: plan is NULL");
   if (capacity > 0 && out == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_atomo_plan_kernel_stats: out is NULL");
-  psgd_status st = PSGD_OK;
-  for (const PendingTiming& t : plan->pending) {
-    float ms = 0.f;
-    hipError_t e = hipEventSynchronize(t.stop);
-    if (e == hipSuccess) e = hipEventElapsedTime(&ms, t.start, t.stop);
-    if (e != hipSuccess) {
-      set_error(std::string("psgd_atomo_plan_kernel_stats: ") + hipGetErrorString(e));
-      st = PSGD_ERR_HIP;
-    } else {
-      plan->stats[t.kernel].launches += 1;
-      plan->stats[t.kernel].total_ms += double(ms);
-    }
-    plan->event_pool.push_back(t.start);
-    plan->event_pool.push_back(t.stop);
-  }
-  plan->pending.clear();
+  const psgd_status st = collect_timings("psgd_atomo_plan_kernel_stats", plan->pending, plan->event_pool, plan->stats);
   int32_t n = 0;
   for (int k = 0; k < kNumK; ++k) {
     if (plan->stats[k].launches == 0) continue;
@@ -2364,11 +2350,13 @@ extern "C" psgd_status psgd_atomo_plan_kernel_stats(psgd_atomo_plan* plan, psgd_
   if (reset)
     for (auto& k : plan->stats) k = KernelStat{};
   return st;
+} catch (...) {
+  return no_memory();
 }
 
 extern "C" psgd_status psgd_atomo_step(psgd_atomo_plan* plan, const float* grads, const float* uniforms,
                                        float* sigma, float* prob, int32_t* index, int32_t* count, float* atoms,
-                                       float* update, void* workspace, void* stream) {
+                                       float* update, void* workspace, void* stream) try {
   static const char* fn = "psgd_atomo_step";
   if (plan == nullptr) return fail(PSGD_ERR_INVALID_ARG, std::string(fn) + ": plan is NULL");
   const uint64_t W = uint64_t(plan->n_workers);
@@ -2478,4 +2466,6 @@ extern "C" psgd_status psgd_atomo_step(psgd_atomo_plan* plan, const float* grads
                static_cast<const AtUpdTile*>(dt.utiles), M, grads, ld, static_cast<const int32_t*>(count),
                static_cast<const float*>(atoms), update, int(W), att, nmats, 1.0f / float(W));
   return s;
+} catch (...) {
+  return no_memory();
 }

@@ -560,23 +560,6 @@ psgd_status hip_fail(const char* what, hipError_t e) {
   return fail(PSGD_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
 }
 
-// What an exception thrown inside an entry point becomes (the message fits without an
-// allocation).
-psgd_status no_memory() {
-  set_error("out of memory");
-  return PSGD_ERR_NO_MEMORY;
-}
-
-// A refusal outside a try block: no exception leaves it.
-psgd_status refuse(psgd_status s, const char* msg) noexcept {
-  try {
-    set_error(msg);
-  } catch (...) {
-    return no_memory();
-  }
-  return s;
-}
-
 uint64_t a256(uint64_t x) { return (x + 255) / 256 * 256; }
 
 struct DevTables {
@@ -669,9 +652,7 @@ psgd_status launch(psgd_clip_plan* plan, int kid, void (*kernel)(KArgs...), dim3
                    Args... args) {
   hipEvent_t a = nullptr, b = nullptr;
   if (plan->timing) {
-    // room first: nothing below may throw once events are taken
-    if (plan->pending.size() == plan->pending.capacity()) plan->pending.reserve(2 * plan->pending.size() + 64);
-    if (plan->event_pool.capacity() - plan->event_pool.size() < 2) plan->event_pool.reserve(2 * plan->event_pool.size() + 64);
+    room_for_timing(plan);
     psgd_status s = take_event(plan, &a);
     if (s == PSGD_OK) s = take_event(plan, &b);
     if (s != PSGD_OK) {
@@ -1031,24 +1012,10 @@ extern "C" psgd_status psgd_clip_plan_kernel_stats(psgd_clip_plan* plan, psgd_ke
   if (capacity > 0 && out == nullptr) return refuse(PSGD_ERR_INVALID_ARG, "psgd_clip_plan_kernel_stats: out is NULL");
   psgd_status st = PSGD_OK;
   try {
-    plan->event_pool.reserve(plan->event_pool.size() + 2 * plan->pending.size());
-    for (const PendingTiming& t : plan->pending) {
-      float ms = 0.f;
-      hipError_t e = hipEventSynchronize(t.stop);
-      if (e == hipSuccess) e = hipEventElapsedTime(&ms, t.start, t.stop);
-      if (e != hipSuccess) {
-        st = hip_fail("psgd_clip_plan_kernel_stats", e);
-      } else {
-        plan->stats[t.kernel].launches += 1;
-        plan->stats[t.kernel].total_ms += double(ms);
-      }
-      plan->event_pool.push_back(t.start);
-      plan->event_pool.push_back(t.stop);
-    }
+    st = collect_timings("psgd_clip_plan_kernel_stats", plan->pending, plan->event_pool, plan->stats);
   } catch (...) {
     return no_memory();
   }
-  plan->pending.clear();
   int32_t n = 0;
   for (int k = 0; k < kNumK; ++k) {
     if (plan->stats[k].launches == 0) continue;

@@ -1723,9 +1723,11 @@ psgd_status ensure_tables(psgd_plan* plan, DeviceTables** out) {
     *out = &it->second;
     return PSGD_OK;
   }
+  it = plan->dev.emplace(dev, DeviceTables{}).first;  // a place first: nothing below may throw with memory taken
   void* base = nullptr;
   e = hipMalloc(&base, layout_tables(plan, nullptr, nullptr));
   if (e != hipSuccess) {
+    plan->dev.erase(it);
     set_error(std::string("hipMalloc of the plan's device tables: ") + hipGetErrorString(e));
     return PSGD_ERR_NO_MEMORY;
   }
@@ -1734,10 +1736,11 @@ psgd_status ensure_tables(psgd_plan* plan, DeviceTables** out) {
   const psgd_status s = copy_tables(plan, t, false, nullptr);
   if (s != PSGD_OK) {
     (void)hipFree(base);
+    plan->dev.erase(it);
     return s;
   }
-  auto ins = plan->dev.emplace(dev, t);
-  *out = &ins.first->second;
+  it->second = t;
+  *out = &it->second;
   return PSGD_OK;
 }
 
@@ -1777,6 +1780,7 @@ psgd_status launch_k(psgd_plan* plan, int kid, void (*kernel)(KArgs...), dim3 gr
                      Args... args) {
   hipEvent_t a = nullptr, b = nullptr;
   if (plan->timing) {
+    room_for_timing(plan);
     psgd_status s = take_event(plan, &a);
     if (s == PSGD_OK) s = take_event(plan, &b);
     if (s != PSGD_OK) {
@@ -2123,12 +2127,14 @@ psgd_status run_step(const char* fn, psgd_plan* plan, const void* grads, float* 
 using namespace psgd;
 
 extern "C" psgd_status psgd_compress_step(psgd_plan* plan, const void* grads, float* errors, float* q,
-                                          float* p, float* update, void* workspace, void* stream) {
+                                          float* p, float* update, void* workspace, void* stream) try {
   return run_step("psgd_compress_step", plan, grads, errors, q, p, update, nullptr, nullptr, 0.f, 0.f,
                   workspace, stream, kCompress);
+} catch (...) {
+  return no_memory();
 }
 
-extern "C" psgd_status psgd_stream_copy(const void* src, void* dst, uint64_t bytes, void* stream) {
+extern "C" psgd_status psgd_stream_copy(const void* src, void* dst, uint64_t bytes, void* stream) try {
   psgd_status s;
   if ((s = check_ptr("psgd_stream_copy", "src", src, false)) != PSGD_OK) return s;
   if ((s = check_ptr("psgd_stream_copy", "dst", dst, false)) != PSGD_OK) return s;
@@ -2148,19 +2154,23 @@ extern "C" psgd_status psgd_stream_copy(const void* src, void* dst, uint64_t byt
                      static_cast<const float*>(src), static_cast<float*>(dst), int64_t(bytes / 16));
   hipError_t e = hipGetLastError();
   return e == hipSuccess ? PSGD_OK : hip_fail("launch k_stream_copy", e);
+} catch (...) {
+  return no_memory();
 }
 
-extern "C" psgd_status psgd_plan_reset_carry(psgd_plan* plan) {
+extern "C" psgd_status psgd_plan_reset_carry(psgd_plan* plan) try {
   if (plan == nullptr) {
     set_error("psgd_plan_reset_carry: plan is NULL");
     return PSGD_ERR_INVALID_ARG;
   }
   plan->state_valid = false;
   return PSGD_OK;
+} catch (...) {
+  return no_memory();
 }
 
 extern "C" psgd_status psgd_errors_materialize(psgd_plan* plan, const float* errors, float* out,
-                                               void* workspace, void* stream) {
+                                               void* workspace, void* stream) try {
   const char* fn = "psgd_errors_materialize";
   if (plan == nullptr) {
     set_error(std::string(fn) + ": plan is NULL");
@@ -2206,9 +2216,11 @@ extern "C" psgd_status psgd_errors_materialize(psgd_plan* plan, const float* err
     if (e != hipSuccess) return hip_fail("launch k_state_store", e);
   }
   return PSGD_OK;
+} catch (...) {
+  return no_memory();
 }
 
-extern "C" psgd_status psgd_plan_reset_carry_stream(psgd_plan* plan, void* workspace, void* stream) {
+extern "C" psgd_status psgd_plan_reset_carry_stream(psgd_plan* plan, void* workspace, void* stream) try {
   const char* fn = "psgd_plan_reset_carry_stream";
   if (plan == nullptr) {
     set_error(std::string(fn) + ": plan is NULL");
@@ -2223,15 +2235,19 @@ extern "C" psgd_status psgd_plan_reset_carry_stream(psgd_plan* plan, void* works
                      reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) + plan->ws_state), uint64_t(0));
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? PSGD_OK : hip_fail("launch k_state_store", e);
+} catch (...) {
+  return no_memory();
 }
 
 extern "C" psgd_status psgd_ef_momentum_apply(psgd_plan* plan, const void* grads, float* errors,
                                               float* q, float* p, float* momentum, float* params,
                                               float lr, float mu, float* update, void* workspace,
-                                              void* stream) {
+                                              void* stream) try {
   const int mode = (plan != nullptr && (plan->flags & PSGD_FLAG_NESTEROV)) ? kNesterov : kMomentum;
   return run_step("psgd_ef_momentum_apply", plan, grads, errors, q, p, update, momentum, params, lr, mu,
                   workspace, stream, mode);
+} catch (...) {
+  return no_memory();
 }
 
 // ------------------------------------------------------------------ no-allocation entry point
@@ -2255,7 +2271,7 @@ std::map<int, NoAllocDevice> g_noalloc;  // per HIP device id
 }  // namespace
 
 extern "C" psgd_status psgd_compress_step_noalloc(psgd_plan* plan, const void* grads, float* errors, float* q,
-                                                  float* p, float* update, void* stream) {
+                                                  float* p, float* update, void* stream) try {
   const char* fn = "psgd_compress_step_noalloc";
   if (plan == nullptr) {
     set_error(std::string(fn) + ": plan is NULL");
@@ -2290,4 +2306,6 @@ extern "C" psgd_status psgd_compress_step_noalloc(psgd_plan* plan, const void* g
   slot.owner = &nd.tables_of;
   return run_step(fn, plan, grads, errors, q, p, update, nullptr, nullptr, 0.f, 0.f, nd.base + tables, stream,
                   kCompress, &slot);
+} catch (...) {
+  return no_memory();
 }

@@ -113,6 +113,14 @@ struct DeviceTables {
 
 void set_error(const std::string& msg);
 
+// What an exception inside an entry point becomes: PSGD_ERR_NO_MEMORY, the only one that
+// the library's own code can meet.  Every entry point that may allocate (an error message
+// does) ends in it, as a function try block.
+psgd_status no_memory() noexcept;
+
+// An error set outside a try block: no exception leaves it.
+psgd_status refuse(psgd_status s, const char* msg) noexcept;
+
 enum KernelId {
   kKFirst = 0, kKMgs, kKQPartial, kKQReduce, kKApply, kKUpdate, kKPMbar, kKQwPartial, kKQwReduce,
   kKTallRows, kKTallApply, kNumKernels
@@ -128,6 +136,19 @@ struct KernelStat {
   int64_t launches = 0;
   double total_ms = 0.0;
 };
+
+// Room for one more timed launch, made before its events are taken: nothing may throw
+// between that and their place in `pending`.
+template <typename Plan>
+void room_for_timing(Plan* plan) {
+  if (plan->pending.size() == plan->pending.capacity()) plan->pending.reserve(2 * plan->pending.size() + 64);
+  if (plan->event_pool.capacity() - plan->event_pool.size() < 2) plan->event_pool.reserve(2 * plan->event_pool.size() + 64);
+}
+
+// Waits for the launches in `pending`, adds their times to `stats` and returns their events
+// to `pool`.
+psgd_status collect_timings(const char* fn, std::vector<PendingTiming>& pending, std::vector<hipEvent_t>& pool,
+                            KernelStat* stats);
 
 }  // namespace psgd
 

@@ -52,7 +52,7 @@
 #include <cmath>
 #include <cstdio>
 #include <map>
-#include <new>
+#include <memory>
 #include <random>
 #include <string>
 #include <vector>
@@ -1137,10 +1137,13 @@ psgd_status device_tables(psgd_rtopk_plan* plan, DevTables* out) {
   const uint64_t bc = a256(plan->chunks.size() * sizeof(RkChunk) + 1);
   auto it = plan->dev.find(dev);
   if (it == plan->dev.end()) {
+    it = plan->dev.emplace(dev, nullptr).first;
     void* base = nullptr;
     e = hipMalloc(&base, bl + bt + bc);
-    if (e != hipSuccess) return fail(PSGD_ERR_NO_MEMORY, std::string("hipMalloc of the plan's device tables: ") +
-                                                             hipGetErrorString(e));
+    if (e != hipSuccess) {
+      plan->dev.erase(it);
+      return fail(PSGD_ERR_NO_MEMORY, std::string("hipMalloc of the plan's device tables: ") + hipGetErrorString(e));
+    }
     char* b = static_cast<char*>(base);
     e = hipMemcpy(b, plan->layers.data(), plan->layers.size() * sizeof(RkLayer), hipMemcpyHostToDevice);
     if (e == hipSuccess)
@@ -1149,9 +1152,10 @@ psgd_status device_tables(psgd_rtopk_plan* plan, DevTables* out) {
       e = hipMemcpy(b + bl + bt, plan->chunks.data(), plan->chunks.size() * sizeof(RkChunk), hipMemcpyHostToDevice);
     if (e != hipSuccess) {
       (void)hipFree(base);
+      plan->dev.erase(it);
       return hip_fail("hipMemcpy of the plan's device tables", e);
     }
-    it = plan->dev.emplace(dev, base).first;
+    it->second = base;
   }
   char* b = static_cast<char*>(it->second);
   out->layers = reinterpret_cast<RkLayer*>(b);
@@ -1177,6 +1181,7 @@ psgd_status launch(psgd_rtopk_plan* plan, int kid, void (*kernel)(KArgs...), dim
                    Args... args) {
   hipEvent_t a = nullptr, b = nullptr;
   if (plan->timing) {
+    room_for_timing(plan);
     psgd_status s = take_event(plan, &a);
     if (s == PSGD_OK) s = take_event(plan, &b);
     if (s != PSGD_OK) {
@@ -1239,7 +1244,7 @@ using namespace psgd::rtk;
 
 extern "C" psgd_status psgd_rtopk_plan_create(const psgd_layer* layers, int32_t n_layers, const int64_t* top,
                                               const int64_t* keep, int32_t n_workers, psgd_dtype grad_dtype,
-                                              uint32_t flags, psgd_rtopk_plan** out) {
+                                              uint32_t flags, psgd_rtopk_plan** out) try {
   if (out == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_rtopk_plan_create: out is NULL");
   *out = nullptr;
   if (n_layers < 1) return fail(PSGD_ERR_INVALID_ARG, "psgd_rtopk_plan_create: n_layers must be >= 1");
@@ -1251,128 +1256,121 @@ extern "C" psgd_status psgd_rtopk_plan_create(const psgd_layer* layers, int32_t 
     return fail(PSGD_ERR_UNSUPPORTED, "psgd_rtopk_plan_create: unknown grad_dtype");
   if (flags & ~uint32_t(PSGD_RTOPK_FLAG_DEFERRED_ZERO))
     return fail(PSGD_ERR_UNSUPPORTED, "psgd_rtopk_plan_create: unknown flag bits");
-  psgd_rtopk_plan* plan = nullptr;
-  try {
-    plan = new psgd_rtopk_plan();
-    plan->n_workers = n_workers;
-    plan->dtype = grad_dtype;
-    plan->flags = flags;
-    {  // a key no other plan's state word is likely to hold: random bits, the clock, a counter
-      static std::atomic<uint64_t> counter{0};
-      uint64_t nonce = (++counter) * 0xD1B54A32D192ED03ull ^
-                       uint64_t(std::chrono::steady_clock::now().time_since_epoch().count());
-      try {
-        std::random_device rd;
-        nonce ^= uint64_t(rd()) << 32 | rd();
-      } catch (...) {
-      }
-      plan->nonce = nonce;
+  std::unique_ptr<psgd_rtopk_plan> plan(new psgd_rtopk_plan());
+  plan->n_workers = n_workers;
+  plan->dtype = grad_dtype;
+  plan->flags = flags;
+  {  // a key no other plan's state word is likely to hold: random bits, the clock, a counter
+    static std::atomic<uint64_t> counter{0};
+    uint64_t nonce = (++counter) * 0xD1B54A32D192ED03ull ^
+                     uint64_t(std::chrono::steady_clock::now().time_since_epoch().count());
+    try {
+      std::random_device rd;
+      nonce ^= uint64_t(rd()) << 32 | rd();
+    } catch (...) {
     }
-    int64_t off = 0, tile_count = 0;
-    for (int32_t i = 0; i < n_layers; ++i) {
-      const int64_t rows = layers[i].rows, cols = layers[i].cols;
-      if (rows < 1 || cols < 1 || rows > (int64_t(1) << 31) || cols > (int64_t(1) << 31) ||
-          rows * cols > int64_t(0x7fffffff)) {
-        delete plan;
-        return fail(PSGD_ERR_INVALID_ARG, "psgd_rtopk_plan_create: layer " + std::to_string(i) +
-                                              " needs 1 <= rows*cols < 2^31");
-      }
-      const int64_t numel = rows * cols;
-      if (keep[i] < 1 || keep[i] > top[i] || top[i] > numel) {
-        delete plan;
-        return fail(PSGD_ERR_INVALID_ARG, "psgd_rtopk_plan_create: layer " + std::to_string(i) +
-                                              " needs 1 <= keep <= top <= rows*cols");
-      }
-      psgd_rtopk_layer_info li{};
-      li.rows = rows;
-      li.cols = cols;
-      li.numel = numel;
-      li.offset = off;
-      li.top = top[i];
-      li.keep = keep[i];
-      li.top_offset = plan->top_total;
-      li.keep_offset = plan->keep_total;
-      RkLayer L{};
-      L.offset = off;
-      L.numel = numel;
-      L.top = top[i];
-      L.keep = keep[i];
-      L.top_off = plan->top_total;
-      L.keep_off = plan->keep_total;
-      L.ntiles = int32_t((numel + kTile - 1) / kTile);
-      L.tile_off = int32_t(tile_count);
-      for (int32_t c = 0; c < L.ntiles; ++c) {
-        RkTile t{};
-        t.begin = off + int64_t(c) * kTile;
-        t.layer = i;
-        t.len = int32_t(std::min<int64_t>(kTile, numel - int64_t(c) * kTile));
-        t.chunk = c;
-        plan->tiles.push_back(t);
-      }
-      for (int32_t c = 0; c < L.ntiles; c += kChunkTiles)
-        plan->chunks.push_back(RkChunk{i, c, std::min(L.ntiles, c + kChunkTiles), c == 0 ? 1 : 0});
-      tile_count += L.ntiles;
-      if (tile_count > int64_t(0x7fffffff)) {
-        delete plan;
-        return fail(PSGD_ERR_INVALID_ARG, "psgd_rtopk_plan_create: too many tiles");
-      }
-      plan->top_total += top[i];
-      plan->keep_total += keep[i];
-      plan->numel += numel;
-      plan->info.push_back(li);
-      plan->layers.push_back(L);
-      off = (off + numel + kAlignElems - 1) / kAlignElems * kAlignElems;
-    }
-    plan->worker_stride = off;
-    plan->n_seg = int64_t(n_workers) * n_layers;
-    const uint64_t W = uint64_t(n_workers);
-    const uint64_t ntiles = plan->tiles.size();
-    const uint64_t words = uint64_t(plan->worker_stride / 32);
-    uint64_t ws = 0;
-    // the three digit histograms are contiguous: one fill clears them
-    plan->ws_hist1 = ws;
-    ws += uint64_t(plan->n_seg) * kBins1 * 4;
-    plan->ws_hist2 = ws;
-    ws += uint64_t(plan->n_seg) * kBins2 * 4;
-    plan->ws_hist3 = ws;
-    ws = a256(ws + uint64_t(plan->n_seg) * kBins3 * 4);
-    plan->ws_seg = ws;
-    ws = a256(ws + uint64_t(plan->n_seg) * sizeof(RkSeg));
-    plan->ws_pred = ws;  // predicted digit-1 bin per segment (a hint only)
-    ws = a256(ws + uint64_t(plan->n_seg) * 4);
-    plan->ws_cand = ws;  // same layout as the error buffer, one uint32 per element
-    ws = a256(ws + W * uint64_t(plan->worker_stride) * 4);
-    uint64_t* word_arrays[] = {&plan->ws_mask, &plan->ws_tmask, &plan->ws_kmask, &plan->ws_kpos};
-    for (uint64_t* a : word_arrays) {
-      *a = ws;
-      ws = a256(ws + W * words * 4);
-    }
-    uint64_t* wave_arrays[] = {&plan->ws_ccnt4, &plan->ws_tcnt4};  // one count per wave of a tile
-    for (uint64_t* a : wave_arrays) {
-      *a = ws;
-      ws = a256(ws + W * ntiles * 16);
-    }
-    uint64_t* tile_arrays[] = {&plan->ws_tfin, &plan->ws_ttie, &plan->ws_tiebase, &plan->ws_tbase, &plan->ws_kcnt,
-                               &plan->ws_kbase};
-    for (uint64_t* a : tile_arrays) {
-      *a = ws;
-      ws = a256(ws + W * ntiles * 4);
-    }
-    plan->ws_state = ws;  // one 64-bit state word (deferred-zero plans)
-    ws += 256;
-    plan->workspace_bytes = ws;
-    const uint64_t gb = grad_dtype == PSGD_BF16 ? 2 : 4;
-    plan->message_bytes = uint64_t(plan->keep_total) * 8;
-    plan->model_bytes = (W * (gb + 8) + 4) * uint64_t(plan->numel);
-  } catch (const std::bad_alloc&) {
-    delete plan;
-    return fail(PSGD_ERR_NO_MEMORY, "psgd_rtopk_plan_create: out of host memory");
+    plan->nonce = nonce;
   }
-  *out = plan;
+  int64_t off = 0, tile_count = 0;
+  for (int32_t i = 0; i < n_layers; ++i) {
+    const int64_t rows = layers[i].rows, cols = layers[i].cols;
+    if (rows < 1 || cols < 1 || rows > (int64_t(1) << 31) || cols > (int64_t(1) << 31) ||
+        rows * cols > int64_t(0x7fffffff)) {
+      return fail(PSGD_ERR_INVALID_ARG, "psgd_rtopk_plan_create: layer " + std::to_string(i) +
+                                            " needs 1 <= rows*cols < 2^31");
+    }
+    const int64_t numel = rows * cols;
+    if (keep[i] < 1 || keep[i] > top[i] || top[i] > numel) {
+      return fail(PSGD_ERR_INVALID_ARG, "psgd_rtopk_plan_create: layer " + std::to_string(i) +
+                                            " needs 1 <= keep <= top <= rows*cols");
+    }
+    psgd_rtopk_layer_info li{};
+    li.rows = rows;
+    li.cols = cols;
+    li.numel = numel;
+    li.offset = off;
+    li.top = top[i];
+    li.keep = keep[i];
+    li.top_offset = plan->top_total;
+    li.keep_offset = plan->keep_total;
+    RkLayer L{};
+    L.offset = off;
+    L.numel = numel;
+    L.top = top[i];
+    L.keep = keep[i];
+    L.top_off = plan->top_total;
+    L.keep_off = plan->keep_total;
+    L.ntiles = int32_t((numel + kTile - 1) / kTile);
+    L.tile_off = int32_t(tile_count);
+    for (int32_t c = 0; c < L.ntiles; ++c) {
+      RkTile t{};
+      t.begin = off + int64_t(c) * kTile;
+      t.layer = i;
+      t.len = int32_t(std::min<int64_t>(kTile, numel - int64_t(c) * kTile));
+      t.chunk = c;
+      plan->tiles.push_back(t);
+    }
+    for (int32_t c = 0; c < L.ntiles; c += kChunkTiles)
+      plan->chunks.push_back(RkChunk{i, c, std::min(L.ntiles, c + kChunkTiles), c == 0 ? 1 : 0});
+    tile_count += L.ntiles;
+    if (tile_count > int64_t(0x7fffffff)) {
+      return fail(PSGD_ERR_INVALID_ARG, "psgd_rtopk_plan_create: too many tiles");
+    }
+    plan->top_total += top[i];
+    plan->keep_total += keep[i];
+    plan->numel += numel;
+    plan->info.push_back(li);
+    plan->layers.push_back(L);
+    off = (off + numel + kAlignElems - 1) / kAlignElems * kAlignElems;
+  }
+  plan->worker_stride = off;
+  plan->n_seg = int64_t(n_workers) * n_layers;
+  const uint64_t W = uint64_t(n_workers);
+  const uint64_t ntiles = plan->tiles.size();
+  const uint64_t words = uint64_t(plan->worker_stride / 32);
+  uint64_t ws = 0;
+  // the three digit histograms are contiguous: one fill clears them
+  plan->ws_hist1 = ws;
+  ws += uint64_t(plan->n_seg) * kBins1 * 4;
+  plan->ws_hist2 = ws;
+  ws += uint64_t(plan->n_seg) * kBins2 * 4;
+  plan->ws_hist3 = ws;
+  ws = a256(ws + uint64_t(plan->n_seg) * kBins3 * 4);
+  plan->ws_seg = ws;
+  ws = a256(ws + uint64_t(plan->n_seg) * sizeof(RkSeg));
+  plan->ws_pred = ws;  // predicted digit-1 bin per segment (a hint only)
+  ws = a256(ws + uint64_t(plan->n_seg) * 4);
+  plan->ws_cand = ws;  // same layout as the error buffer, one uint32 per element
+  ws = a256(ws + W * uint64_t(plan->worker_stride) * 4);
+  uint64_t* word_arrays[] = {&plan->ws_mask, &plan->ws_tmask, &plan->ws_kmask, &plan->ws_kpos};
+  for (uint64_t* a : word_arrays) {
+    *a = ws;
+    ws = a256(ws + W * words * 4);
+  }
+  uint64_t* wave_arrays[] = {&plan->ws_ccnt4, &plan->ws_tcnt4};  // one count per wave of a tile
+  for (uint64_t* a : wave_arrays) {
+    *a = ws;
+    ws = a256(ws + W * ntiles * 16);
+  }
+  uint64_t* tile_arrays[] = {&plan->ws_tfin, &plan->ws_ttie, &plan->ws_tiebase, &plan->ws_tbase, &plan->ws_kcnt,
+                             &plan->ws_kbase};
+  for (uint64_t* a : tile_arrays) {
+    *a = ws;
+    ws = a256(ws + W * ntiles * 4);
+  }
+  plan->ws_state = ws;  // one 64-bit state word (deferred-zero plans)
+  ws += 256;
+  plan->workspace_bytes = ws;
+  const uint64_t gb = grad_dtype == PSGD_BF16 ? 2 : 4;
+  plan->message_bytes = uint64_t(plan->keep_total) * 8;
+  plan->model_bytes = (W * (gb + 8) + 4) * uint64_t(plan->numel);
+  *out = plan.release();
   return PSGD_OK;
+} catch (...) {
+  return no_memory();
 }
 
-extern "C" psgd_status psgd_rtopk_plan_sizes(const psgd_rtopk_plan* plan, psgd_rtopk_sizes* out) {
+extern "C" psgd_status psgd_rtopk_plan_sizes(const psgd_rtopk_plan* plan, psgd_rtopk_sizes* out) try {
   if (plan == nullptr || out == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_rtopk_plan_sizes: NULL argument");
   psgd_rtopk_sizes s{};
   s.n_layers = int32_t(plan->info.size());
@@ -1387,15 +1385,19 @@ extern "C" psgd_status psgd_rtopk_plan_sizes(const psgd_rtopk_plan* plan, psgd_r
   s.model_bytes = plan->model_bytes;
   *out = s;
   return PSGD_OK;
+} catch (...) {
+  return no_memory();
 }
 
 extern "C" psgd_status psgd_rtopk_plan_layer_info(const psgd_rtopk_plan* plan, int32_t layer,
-                                             psgd_rtopk_layer_info* out) {
+                                             psgd_rtopk_layer_info* out) try {
   if (plan == nullptr || out == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_rtopk_plan_layer_info: NULL argument");
   if (layer < 0 || size_t(layer) >= plan->info.size())
     return fail(PSGD_ERR_INVALID_ARG, "psgd_rtopk_plan_layer_info: layer index out of range");
   *out = plan->info[size_t(layer)];
   return PSGD_OK;
+} catch (...) {
+  return no_memory();
 }
 
 extern "C" psgd_status psgd_rtopk_plan_destroy(psgd_rtopk_plan* plan) {
@@ -1411,8 +1413,7 @@ extern "C" psgd_status psgd_rtopk_plan_destroy(psgd_rtopk_plan* plan) {
     const bool have = hipGetDevice(&cur) == hipSuccess;
     if (have && cur != kv.first) (void)hipSetDevice(kv.first);
     if (hipFree(kv.second) != hipSuccess) {
-      set_error("psgd_rtopk_plan_destroy: hipFree of the device tables failed");
-      st = PSGD_ERR_HIP;
+      st = refuse(PSGD_ERR_HIP, "psgd_rtopk_plan_destroy: hipFree of the device tables failed");
     }
     if (have && cur != kv.first) (void)hipSetDevice(cur);
   }
@@ -1420,32 +1421,19 @@ extern "C" psgd_status psgd_rtopk_plan_destroy(psgd_rtopk_plan* plan) {
   return st;
 }
 
-extern "C" psgd_status psgd_rtopk_plan_set_timing(psgd_rtopk_plan* plan, int32_t enable) {
+extern "C" psgd_status psgd_rtopk_plan_set_timing(psgd_rtopk_plan* plan, int32_t enable) try {
   if (plan == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_rtopk_plan_set_timing: plan is NULL");
   plan->timing = enable != 0;
   return PSGD_OK;
+} catch (...) {
+  return no_memory();
 }
 
 extern "C" psgd_status psgd_rtopk_plan_kernel_stats(psgd_rtopk_plan* plan, psgd_kernel_stat* out, int32_t capacity,
-                                                    int32_t* count, int32_t reset) {
+                                                    int32_t* count, int32_t reset) try {
   if (plan == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_rtopk_plan_kernel_stats: plan is NULL");
   if (capacity > 0 && out == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_rtopk_plan_kernel_stats: out is NULL");
-  psgd_status st = PSGD_OK;
-  for (const PendingTiming& t : plan->pending) {
-    float ms = 0.f;
-    hipError_t e = hipEventSynchronize(t.stop);
-    if (e == hipSuccess) e = hipEventElapsedTime(&ms, t.start, t.stop);
-    if (e != hipSuccess) {
-      set_error(std::string("psgd_rtopk_plan_kernel_stats: ") + hipGetErrorString(e));
-      st = PSGD_ERR_HIP;
-    } else {
-      plan->stats[t.kernel].launches += 1;
-      plan->stats[t.kernel].total_ms += double(ms);
-    }
-    plan->event_pool.push_back(t.start);
-    plan->event_pool.push_back(t.stop);
-  }
-  plan->pending.clear();
+  const psgd_status st = collect_timings("psgd_rtopk_plan_kernel_stats", plan->pending, plan->event_pool, plan->stats);
   int32_t n = 0;
   for (int k = 0; k < kNumK; ++k) {
     if (plan->stats[k].launches == 0) continue;
@@ -1462,11 +1450,13 @@ extern "C" psgd_status psgd_rtopk_plan_kernel_stats(psgd_rtopk_plan* plan, psgd_
   if (reset)
     for (auto& k : plan->stats) k = KernelStat{};
   return st;
+} catch (...) {
+  return no_memory();
 }
 
 extern "C" psgd_status psgd_rtopk_step(psgd_rtopk_plan* plan, const void* grads, float* errors,
                                        const uint32_t* ranks, int32_t* index, float* value, float* update,
-                                       void* workspace, void* stream) {
+                                       void* workspace, void* stream) try {
   static const char* fn = "psgd_rtopk_step";
   if (plan == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_rtopk_step: plan is NULL");
   const uint64_t W = uint64_t(plan->n_workers);
@@ -1600,10 +1590,12 @@ extern "C" psgd_status psgd_rtopk_step(psgd_rtopk_plan* plan, const void* grads,
     plan->state_device = dev;
   }
   return s;
+} catch (...) {
+  return no_memory();
 }
 
 extern "C" psgd_status psgd_rtopk_errors_materialize(psgd_rtopk_plan* plan, const float* errors, float* out,
-                                                     void* workspace, void* stream) {
+                                                     void* workspace, void* stream) try {
   static const char* fn = "psgd_rtopk_errors_materialize";
   if (plan == nullptr) return fail(PSGD_ERR_INVALID_ARG, std::string(fn) + ": plan is NULL");
   const uintptr_t ptrs[] = {uintptr_t(errors), uintptr_t(out), uintptr_t(workspace)};
@@ -1640,9 +1632,11 @@ extern "C" psgd_status psgd_rtopk_errors_materialize(psgd_rtopk_plan* plan, cons
     if (e != hipSuccess) return hip_fail("launch rk_state_store", e);
   }
   return PSGD_OK;
+} catch (...) {
+  return no_memory();
 }
 
-extern "C" psgd_status psgd_rtopk_plan_reset_state(psgd_rtopk_plan* plan, void* workspace, void* stream) {
+extern "C" psgd_status psgd_rtopk_plan_reset_state(psgd_rtopk_plan* plan, void* workspace, void* stream) try {
   static const char* fn = "psgd_rtopk_plan_reset_state";
   if (plan == nullptr) return fail(PSGD_ERR_INVALID_ARG, std::string(fn) + ": plan is NULL");
   if (workspace == nullptr || uintptr_t(workspace) % 16 != 0)
@@ -1653,4 +1647,6 @@ extern "C" psgd_status psgd_rtopk_plan_reset_state(psgd_rtopk_plan* plan, void* 
                      reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) + plan->ws_state), uint64_t(0));
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? PSGD_OK : hip_fail("launch rk_state_store", e);
+} catch (...) {
+  return no_memory();
 }
