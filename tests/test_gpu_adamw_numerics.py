@@ -1,8 +1,9 @@
-"""AdamW where its numbers get long: averages over many steps, large gradients.
-Against float64, with u = 2^-24 (half a float32 step); tolerances are derived beside
+"""AdamW where its numbers get long: averages over many steps, large gradients, betas next
+to 1.  Against float64, with u = 2^-24 (half a float32 step); tolerances are derived beside
 each test.  The element counts take the single launch, the joined partials and cl_final."""
 
 import math
+from decimal import Decimal, localcontext
 
 import numpy as np
 import pytest
@@ -103,3 +104,34 @@ def test_an_infinite_second_moment_stays_infinite(size, beta2):
     rest[n:] = False
     # 1 - 2^-4 - lr / (1 + 1e-8): a step within 17 u of itself and three roundings below 1
     assert bool(((x[rest] - 0.8125).abs() <= 5 * U + 17 * U * 0.125 + 2e-9).all())
+
+
+@pytest.mark.parametrize("gap", [1e-9, 1e-12])
+@pytest.mark.parametrize("max_norm", [0.0, math.inf])
+@pytest.mark.parametrize("size", SIZES)
+def test_bias_corrections_of_betas_next_to_one(size, max_norm, gap):
+    """1 - beta^t without cancellation: the weights' step is right to _check_adamw's 17 u and
+    the first moment's 5 u, also where 1 - beta^t is as small as 2e-12."""
+    n = SIZES[size]
+    beta = 1.0 - gap
+    w = 1.0 - beta  # exact
+    plan = psgd.psgd_clip_plan_create([(1, n)], 1)
+    ld = plan.sizes["worker_stride"]
+    g = torch.linspace(0.5, 1.5, ld, device=DEV)
+    cfg = psgd.AdamwConfig(lr=0.5, beta1=beta, beta2=beta, eps=1e-8, weight_decay=0.0, max_norm=max_norm)
+    for step in (0, 1, 2, 6, 99, 12344):
+        x = torch.zeros(ld, device=DEV)
+        m, v = (torch.full((ld,), float(np.float32(w * step)), device=DEV) for _ in range(2))
+        m0 = float(m[0])
+        t = torch.full((1,), step, dtype=torch.int64, device=DEV)
+        norm = torch.zeros(1, device=DEV) if max_norm else None
+        psgd.psgd_adamw_apply(plan, cfg, g, x, m, v, None, t, norm, _workspace(plan))
+        with localcontext() as ctx:
+            ctx.prec = 60
+            bc = float(1 - Decimal(beta) ** (step + 1))
+        d = g[:n].double().cpu().numpy()
+        m1 = beta * m0 + w * d
+        want = -0.5 * (m1 / bc) / (np.sqrt((beta * m0 + w * d * d) / bc) + 1e-8)
+        got = x[:n].double().cpu().numpy()
+        off = np.max(np.abs(got - want) / np.abs(want))
+        assert off <= 23 * 1.01 * U, (step, off / U)
