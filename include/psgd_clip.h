@@ -20,10 +20,11 @@
  * underflows them, and are added in a fixed order: equal calls give equal bits.  Norms
  * and coefficients are rounded once to float32 (a norm past its largest number becomes
  * infinite); a coefficient is taken from the float64 norm.  out is c * g in float32,
- * rounded once to the gradient type.  The AdamW state is float32; its step size, bias
- * corrections and new moments are formed in float64 and rounded once.  A moment at its
- * steady value takes no change below half a float32 step: for 1 - beta below about 2^-24
- * (6e-8) it stands still there.
+ * rounded once to the gradient type.  The AdamW state is float32 and its step size and
+ * bias corrections are formed in float64.  A moment's weights beta and 1 - beta are not
+ * rounded against each other: they add up to 1 far below a rounding of the moment.  A
+ * moment at its steady value takes no change below half a float32 step, so for 1 - beta
+ * below about 2^-24 (6e-8) it stands still there.
  *
  * Non-finite gradients are not errors: an infinite entry gives an infinite norm, hence
  * c = 0 for every finite max_norm (finite entries become 0, infinite ones NaN); a NaN
