@@ -40,7 +40,10 @@ namespace clip {
 // workgroups.
 constexpr int kTile = 8192;
 constexpr int kThreads = 256;
-// cl_norm workgroups per slice: cl_final's 256 threads then take at most 16 partials each.
+// cl_norm workgroups per slice: for a slice's norm cl_final's 256 threads then take at most
+// 16 partials each (for a tensor's, one per tile).  Up to here there are about as many runs
+// as tiles; the cut by cost lets short neighbours share one (119 odd tensors: 1155 tiles in
+// 1114 runs).
 constexpr int64_t kMaxRuns = 4096;
 // What a tile costs cl_norm besides its elements, in elements: its loads start anew, so a
 // run of tiny tensors takes their latencies one after the other (119 tensors of 1 to 2
@@ -61,15 +64,16 @@ constexpr int64_t kFoldTotal = 512;  // all slices together
 // A single launch with a workgroup per slice, for plans of at most kMaxItems items, up to
 // kSmallNorm, kSmallClip or kSmallAdamw elements per slice.  Against the two launches
 // above (us a call in a graph): norm of 16384 4.4 against 5.2, of 32768 6.0 against 5.5;
-// clip 5.8 / 5.9 and 8.3 / 5.8; AdamW of 4096 6.3 / 7.2, of 8192 7.6 / 7.2, of 16384
-// 10.5 / 7.6.  Called one by one the smaller number of launches is worth 3.5 us.
+// clip 5.8 / 5.9 and 8.3 / 5.8; AdamW of 4096 5.9 / 7.1, of 8192 7.7 / 7.1, of 16384
+// 11.1 / 7.4.  Called one by one the smaller number of launches is worth 3.5 us.
 constexpr int kItem = 512;      // elements per item
 constexpr int kMaxItems = 128;
 constexpr int kSmallThreads = 1024;
 constexpr int64_t kSmallNorm = 32768, kSmallClip = 16384, kSmallAdamw = 8192;
 // Parts a cl_scale workgroup takes when out is grads: 1, 2, 3, 4 of them let a call that has
 // nothing to scale return after 39, 20, 13, 10 us (16 x 45 MB: 175 thousand workgroups
-// for 1), and scale in 221, 216, 220, 233 us when it has.
+// for 1), and scale in 221, 216, 220, 233 us when it has.  With 2 the whole call takes 134
+// us with nothing to scale (the norm alone 112) and 334 with every slice scaled.
 constexpr int kInPlaceParts = 2;
 constexpr int64_t kMaxTiles = 0x1fffff;  // tiles * (kTile / 4) threads fit a launch's 32 bits
 
@@ -286,10 +290,11 @@ __device__ __forceinline__ typename N::acc_t tile_sum(const GT* __restrict__ g, 
 
 // A workgroup reads one run of one slice (grid.y).  Its partial goes to `part_run`, each
 // tile's to `part_tile` if tensor norms are wanted.  Bound by HBM reads: 715 MB of float32
-// in 102 us (7.0 TB/s; a bare reading loop reaches 7.2), 508 MB of bfloat16 in 73 us.  A
-// workgroup to a tile keeps 32 KB of loads per 256 threads short enough that the last ones
-// end together; float64 costs nothing next to the loads, if whole steps go without bounds
-// checks (with them bfloat16 took 83 us).
+// in 106 us on average, 101 at best (6.7 and 7.1 TB/s; a bare reading loop reaches 7.2); 508
+// MB of bfloat16 in 84 us, 76 at best (MAX: 74 and 70).  A workgroup to a tile keeps its
+// loads (32 KB per 256 threads, 16 KB of bfloat16) short enough that the last ones end
+// together; float64 costs nothing next to the loads, if whole steps go without bounds
+// checks (with them bfloat16 took 83 us at best).
 template <typename GT, typename N>
 __global__ __launch_bounds__(kThreads) void cl_norm(const ClTile* __restrict__ tiles, const ClRun* __restrict__ runs,
                                                     int n_tiles, const GT* __restrict__ grads, int64_t stride,
@@ -388,7 +393,7 @@ __device__ __forceinline__ float coefficient(const CoefArgs<N>& a, int64_t slice
 
 // One 16-byte unit per thread and 4 KB per workgroup: reads and writes then sweep the
 // buffers in dispatch order, which HBM serves at the speed of a plain copy (16 x 45 MB in
-// 214 us, 6.7 TB/s; 64 KB per workgroup took 262 us).
+// 222 us on average, 216 at best, 6.4 and 6.6 TB/s; 64 KB per workgroup took 262 us).
 template <typename GT, typename N, bool FOLD>
 __global__ __launch_bounds__(kThreads) void cl_scale(const ClTile* __restrict__ tiles, int n_parts,
                                                      const GT* grads, GT* out, int64_t stride, CoefArgs<N> ca) {
@@ -406,8 +411,9 @@ __global__ __launch_bounds__(kThreads) void cl_scale(const ClTile* __restrict__ 
   }
 }
 
-// Four elements per thread, as in cl_scale: seven (eight) streams at 6.1 to 6.6 TB/s.  45 MB of
-// update in 50 us, 1.6 GB in 1.80 ms (64 KB per workgroup: 67 us, 2.11 ms).
+// Four elements per thread, as in cl_scale: seven (eight) streams at 5.8 to 6.5 TB/s.  45 MB of
+// update in 52 us, 1.6 GB in 1.72 to 1.95 ms from card to card (64 KB per workgroup: 67 us,
+// 2.11 ms).
 // CLIP: 0 no clipping (c = 1), 1 cl_final's coefficient, 2 from the partials.
 template <typename GT, typename N, int CLIP>
 __global__ __launch_bounds__(kThreads) void cl_adamw(const ClTile* __restrict__ tiles, const GT* __restrict__ update,
@@ -511,7 +517,7 @@ __global__ __launch_bounds__(kSmallThreads) void cl_small(const ClItem* __restri
 }
 
 // The whole AdamW step in one workgroup; one wave forms the step's scalars (two float64
-// powers) while the others take the norm.  6 us for 7 thousand elements.
+// powers) while the others take the norm.  6.9 us for 7 thousand elements.
 template <typename GT, typename N, bool CLIP>
 __global__ __launch_bounds__(kSmallThreads) void cl_small_adamw(const ClItem* __restrict__ item_table, int n_items,
                                                                 const GT* __restrict__ update,

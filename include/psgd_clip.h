@@ -17,7 +17,9 @@
  *                             - lr * (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
  *
  * Precision.  Sums of squares are held in float64, so no float32 gradient overflows or
- * underflows them, and are added in a fixed order: equal calls give equal bits.  Norms
+ * underflows them, and are added in a fixed order: equal calls give equal bits.  That order
+ * depends on the call and the plan's sizes, so norms of one buffer from two different calls
+ * (psgd_grad_norm and psgd_grad_clip, say) may differ in their last bit.  Norms
  * and coefficients are rounded once to float32 (a norm past its largest number becomes
  * infinite); a coefficient is taken from the float64 norm.  out is c * g in float32,
  * rounded once to the gradient type.  The AdamW state is float32 and its step size and
