@@ -687,39 +687,6 @@ psgd_status launch(psgd_clip_plan* plan, int kid, void (*kernel)(KArgs...), dim3
   return PSGD_OK;
 }
 
-struct Span {
-  const char* name;
-  const void* ptr;
-  uint64_t bytes;
-  unsigned align;
-  bool nullable;
-};
-
-// Every pointer given, aligned, and no two ranges overlapping; `same` names the one pair
-// (by index) that may be the same buffer.
-psgd_status check_spans(const char* fn, const Span* spans, int n, int same_a = -1, int same_b = -1) {
-  for (int i = 0; i < n; ++i) {
-    const Span& a = spans[i];
-    if (a.ptr == nullptr) {
-      if (a.nullable) continue;
-      return fail(PSGD_ERR_INVALID_ARG, std::string(fn) + ": " + a.name + " is NULL");
-    }
-    if (uintptr_t(a.ptr) % a.align != 0)
-      return fail(PSGD_ERR_INVALID_ARG, std::string(fn) + ": " + a.name + " is not " + std::to_string(a.align) +
-                                            "-byte aligned");
-  }
-  for (int i = 0; i < n; ++i)
-    for (int j = i + 1; j < n; ++j) {
-      const Span &a = spans[i], &b = spans[j];
-      if (a.ptr == nullptr || b.ptr == nullptr) continue;
-      if (i == same_a && j == same_b && a.ptr == b.ptr) continue;
-      const uintptr_t al = uintptr_t(a.ptr), bl = uintptr_t(b.ptr);
-      if (al < bl + b.bytes && bl < al + a.bytes)
-        return fail(PSGD_ERR_INVALID_ARG, std::string(fn) + ": " + a.name + " and " + b.name + " overlap");
-    }
-  return PSGD_OK;
-}
-
 psgd_status check_kind(const char* fn, int kind) {
   if (kind == PSGD_NORM_L2 || kind == PSGD_NORM_MAX) return PSGD_OK;
   return fail(PSGD_ERR_UNSUPPORTED, std::string(fn) + ": unknown norm kind");
@@ -1054,7 +1021,7 @@ extern "C" psgd_status psgd_grad_norm(psgd_clip_plan* plan, const void* grads, p
     psgd_status s = check_kind(fn, kind);
     if (s != PSGD_OK) return s;
     const uint64_t S = uint64_t(plan->n_slices), gb = plan->dtype == PSGD_BF16 ? 2 : 4;
-    const Span spans[] = {
+    const ArgSpan spans[] = {
         {"grads", grads, S * uint64_t(plan->worker_stride) * gb, 16, false},
         {"norms", norms, S * 4, 4, false},
         {"tensor_norms", tensor_norms, S * plan->layers.size() * 4, 4, true},
@@ -1080,7 +1047,7 @@ extern "C" psgd_status psgd_grad_clip(psgd_clip_plan* plan, const void* grads, v
     if (!(max_norm > 0.0f)) return fail(PSGD_ERR_INVALID_ARG, "psgd_grad_clip: max_norm must be > 0");
     const uint64_t S = uint64_t(plan->n_slices), gb = plan->dtype == PSGD_BF16 ? 2 : 4;
     const uint64_t bytes = S * uint64_t(plan->worker_stride) * gb;
-    const Span spans[] = {
+    const ArgSpan spans[] = {
         {"grads", grads, bytes, 16, false},
         {"out", out, bytes, 16, false},
         {"norms", norms, S * 4, 4, false},
@@ -1125,7 +1092,7 @@ extern "C" psgd_status psgd_adamw_apply(psgd_clip_plan* plan, const psgd_adamw_c
     if (!clipped && norm != nullptr)
       return fail(PSGD_ERR_INVALID_ARG, "psgd_adamw_apply: norm must be NULL when max_norm is 0");
     const uint64_t n = uint64_t(plan->worker_stride), gb = plan->dtype == PSGD_BF16 ? 2 : 4;
-    const Span spans[] = {
+    const ArgSpan spans[] = {
         {"update", update, n * gb, 16, false},
         {"params", params, n * 4, 16, false},
         {"exp_avg", exp_avg, n * 4, 16, false},

@@ -1,0 +1,1467 @@
+// Embedding, softmax cross entropy and dropout around a language model's table: the gfx950
+// kernels and the host side of psgd_lm.h.
+//
+// Products run on bf16 matrix cores from packed operands: 64 x 64 blocks of bf16, 8 KB each
+// and one after the other, so that a tile is a few contiguous runs of 16-byte loads, zero
+// past a matrix's edges, so that no product loop has an edge of its own.  A float32 operand
+// is held as three such bf16 parts, x = h + m + l, and a product of two of them is the sum
+// of the six part products above 2^-24: the loop over the contraction simply gets longer.
+//
+//   lm_count   counted rows of every worker
+//   lm_pack    x (through dropout, zero where a row does not count) and the table, packed
+//   lm_scores  a 256 x 256 tile of T drop(x)^T: its columns' running maximum and sum
+//              (loss), or g of its entries, packed (gradient)
+//   lm_rows    lse and loss of every row from the tiles' maxima and sums
+//   lm_mean    the workers' means
+//   lm_dx      g T, added up over the pieces of the vocabulary in float32
+//   lm_dx_out  the sum of its splits, through dropout
+//   lm_dw      g^T drop(x) into the gradient slices
+//   lm_embed   rows of the table
+//   lm_sort, lm_merge  every worker's (token, row) pairs in order
+//   lm_zero, lm_sum, lm_join  the table gradient from runs of these pairs
+//   lm_dropout
+//
+// No kernel waits for another workgroup, no atomics, no state is kept between calls.
+
+#include <hip/hip_runtime.h>
+#include <hip/hip_ext.h>
+
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+#include <cstdio>
+#include <string>
+#include <vector>
+
+#include "plan.hpp"
+#include "psgd_lm.h"
+
+namespace psgd {
+namespace lm {
+
+constexpr int kBlk = 64;           // rows and columns of a packed block
+constexpr int kBlkElems = kBlk * kBlk;
+constexpr int64_t kMaxBlocks = int64_t(1) << 23;  // of x or the table: launches of 256 threads each stay below 2^32
+constexpr int kTile = 4;           // blocks per side of a workgroup's tile
+constexpr int kThreads = 256;      // of the kernels around the products
+constexpr int kGroup = 4;          // row tiles that take turns on one vocabulary tile (lm_scores)
+constexpr int64_t kPieceBytes = int64_t(256) << 20;  // g of one piece of the vocabulary
+constexpr int64_t kStatBytes = int64_t(64) << 20;    // maxima and sums of one chunk of rows
+constexpr int kSortMax = 4096;     // pairs sorted by one workgroup
+constexpr int kSortThreads = 512;
+constexpr int kRun = 32;           // sorted pairs summed by one wave
+
+enum KernelId {
+  kCount = 0, kPack, kScores, kRows, kMean, kDx, kDxOut, kDw, kEmbed, kSort, kMerge, kZero, kSum, kJoin, kDrop, kNumK
+};
+const char* const kNames[kNumK] = {"lm_count", "lm_pack", "lm_scores", "lm_rows", "lm_mean", "lm_dx", "lm_dx_out", "lm_dw",
+                                   "lm_embed", "lm_sort", "lm_merge", "lm_zero", "lm_sum", "lm_join", "lm_dropout"};
+
+}  // namespace lm
+}  // namespace psgd
+
+struct psgd_lm_plan {
+  int32_t n_layers = 0, n_workers = 0, table = 0;
+  psgd_dtype act = PSGD_F32, grad = PSGD_F32;
+  int64_t vocab = 0, dim = 0, rows = 0, worker_stride = 0, offset = 0;
+  int32_t vb = 0, db = 0;        // blocks of the table
+  int32_t tb = 0, tw = 0;        // blocks of all rows together, and of one worker's rows
+  int32_t piece = 0, splits = 1;  // blocks of the vocabulary per piece, splits of its sum in lm_dx
+  int32_t chunk = 0;             // row blocks per chunk in psgd_lm_loss
+  uint64_t ws_x = 0, ws_w = 0, ws_info = 0, ws_count = 0, ws_stat = 0, ws_hit = 0, ws_g = 0, ws_dx = 0;
+  uint64_t ws_key = 0, ws_key2 = 0, ws_part = 0, workspace_bytes = 0;
+  bool timing = false;
+  std::vector<psgd::PendingTiming> pending;
+  std::vector<hipEvent_t> event_pool;
+  psgd::KernelStat stats[psgd::lm::kNumK];
+};
+
+namespace psgd {
+namespace lm {
+namespace {
+
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef short s4v __attribute__((ext_vector_type(4)));
+typedef short s8v __attribute__((ext_vector_type(8)));
+typedef float f16v __attribute__((ext_vector_type(16)));
+typedef uint32_t u4v __attribute__((ext_vector_type(4)));
+
+// ------------------------------------------------------------------ numbers
+__device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float(uint32_t(b) << 16); }
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ uint16_t narrow_bits(float x) { return __builtin_bit_cast(uint16_t, __bf16(x)); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(uint16_t* p, float x) { *p = narrow_bits(x); }
+
+// N elements from or to an address that is aligned to its type only.
+template <int N, typename T>
+__device__ __forceinline__ void load(const T* p, float (&x)[N]) {
+  T v[N];
+  __builtin_memcpy(v, p, sizeof(v));
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = widen(v[i]);
+}
+template <int N>
+__device__ __forceinline__ void store(float* p, const float (&x)[N]) {
+  __builtin_memcpy(p, x, sizeof(x));
+}
+template <int N>
+__device__ __forceinline__ void store(uint16_t* p, const float (&x)[N]) {
+  uint16_t v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = narrow_bits(x[i]);
+  __builtin_memcpy(p, v, sizeof(v));
+}
+
+// x = sum of P bf16 parts, each the nearest to what is left.  A number past the largest
+// bf16 takes that as its first part; infinities and NaN have one part.
+template <int P>
+__device__ __forceinline__ void split(float x, uint16_t (&h)[P]) {
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    uint16_t b = narrow_bits(x);
+    if (P > 1 && (b & 0x7fff) == 0x7f80 && (__float_as_uint(x) & 0x7fffffffu) < 0x7f800000u) b -= 1;
+    h[p] = b;
+    x = (b & 0x7f80) == 0x7f80 ? 0.f : x - widen(b);
+  }
+}
+
+struct Drop {
+  uint64_t keep_from;  // an entry is kept if its word is at least this; 0 with scale 1: no dropout
+  uint32_t key0, key1;
+  const int64_t* step;
+  float scale;
+  int32_t on;
+};
+
+// Philox4x32-10 with counter (i, step): the words of entries 4i to 4i + 3.
+__device__ __forceinline__ void philox(uint64_t i, uint64_t step, uint32_t k0, uint32_t k1, uint32_t (&w)[4]) {
+  uint32_t c0 = uint32_t(i), c1 = uint32_t(i >> 32), c2 = uint32_t(step), c3 = uint32_t(step >> 32);
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t a = uint64_t(0xD2511F53u) * c0, b = uint64_t(0xCD9E8D57u) * c2;
+    c0 = uint32_t(b >> 32) ^ c1 ^ k0;
+    c1 = uint32_t(b);
+    c2 = uint32_t(a >> 32) ^ c3 ^ k1;
+    c3 = uint32_t(a);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  w[0] = c0, w[1] = c1, w[2] = c2, w[3] = c3;
+}
+
+__device__ __forceinline__ uint64_t step_of(const Drop& d) { return d.step != nullptr ? uint64_t(*d.step) : 0u; }
+
+// Entries i to i + N - 1 through dropout.
+template <int N>
+__device__ __forceinline__ void drop(const Drop& d, uint64_t step, uint64_t i, float (&x)[N]) {
+  const int lead = int(i & 3);
+#pragma unroll
+  for (int g = 0; g < (N + 6) / 4; ++g) {
+    if (4 * g >= N + lead) break;
+    uint32_t w[4];
+    philox(i / 4 + g, step, d.key0, d.key1, w);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const int at = e + lead - 4 * g;  // its word, if in 0..3
+      if (at >= 0 && at < 4) {
+        const uint32_t v = at == 0 ? w[0] : at == 1 ? w[1] : at == 2 ? w[2] : w[3];
+        x[e] = uint64_t(v) >= d.keep_from ? x[e] * d.scale : 0.f;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ packed operands
+// A packed matrix: block (r, c) is 4096 elements at (r * cb + c) * 4096 of every part.
+// Inside a block element (r, c) is at 64 r + 8 (c / 8 ^ turn(r)) + c % 8: the 16-byte pieces
+// of a row are turned so that neither the reads along rows (16 rows, one piece each) nor the
+// transposing ones (4 rows, two pieces each) meet on a bank.
+struct Mat {
+  const uint16_t* p;
+  int64_t part;  // elements between parts
+  int32_t rb, cb;
+};
+
+__device__ __forceinline__ int turn(int r) { return ((r >> 1) & 1) << 2 | ((r >> 2) & 1) << 1 | ((r >> 3) & 1); }
+
+// The part products of one contraction, one after the other.
+struct Parts {
+  int32_t n;
+  uint8_t a[6], b[6];
+};
+
+// C += A B over K blocks for a tile of WM FM x WN FN pieces of 32 x 32, each wave FM x FN of
+// them.  TA, TB: the operand's contraction runs along its blocks' rows instead of along
+// their columns; it is then read from LDS with the transposing load.  Two LDS stages; the
+// next blocks are on their way in registers while the matrix cores work on a stage.
+template <int WM, int WN, int FM, int FN, bool TA, bool TB>
+struct Gemm {
+  static constexpr int kT = WM * WN * 64;
+  static constexpr int kA = WM * FM / 2, kB = WN * FN / 2;  // blocks of the tile's sides
+  static constexpr int kPer = kBlkElems / 8 / kT;           // 16-byte pieces of a block per thread
+  static constexpr int kStage = (kA + kB) * kBlkElems;
+  static_assert(kPer * kT * 8 == kBlkElems, "a block is a whole number of pieces per thread");
+
+  template <bool T>
+  static __device__ __forceinline__ const uint16_t* block(const Mat& m, int part, int side, int k) {
+    const int r = T ? k : min(side, m.rb - 1), c = T ? min(side, m.cb - 1) : k;
+    return m.p + part * m.part + (int64_t(r) * m.cb + c) * kBlkElems;
+  }
+
+  // 32 x 16 operand piece f of step kk: row (column) lane % 32, contraction 8 (lane / 32) on.
+  template <bool T>
+  static __device__ __forceinline__ bf8 piece(const uint16_t* s, int f, int kk, int lane) {
+    if constexpr (!T) {
+      const int r = (f & 1) * 32 + (lane & 31);
+      return *reinterpret_cast<const bf8*>(s + (f >> 1) * kBlkElems + r * kBlk + (((kk * 2 + (lane >> 5)) ^ turn(lane)) << 3));
+    } else {
+      typedef __attribute__((address_space(3))) s4v lds4;
+      s8v v;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int k = (lane >> 5) * 8 + j * 4 + ((lane & 15) >> 2);
+        const int c = (f & 1) * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+        const uint16_t* at = s + (f >> 1) * kBlkElems + (kk * 16 + k) * kBlk + ((c ^ turn(k)) << 3) + (lane & 1) * 4;
+        const s4v q = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)at);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * j + e] = q[e];
+      }
+      return __builtin_bit_cast(bf8, v);
+    }
+  }
+
+  static __device__ __forceinline__ void run(const Mat& a, int a0, const Mat& b, int b0, int k0, int k1, const Parts& parts,
+                                             uint16_t* sm, f16v (&acc)[FM][FN]) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wa = (wave / WN) * FM, wb = (wave % WN) * FN;
+    u4v ra[kA][kPer], rb[kB][kPer];
+    auto fetch = [&](int q, int k) {
+#pragma unroll
+      for (int i = 0; i < kA; ++i)
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          ra[i][j] = *reinterpret_cast<const u4v*>(block<TA>(a, parts.a[q], a0 + i, k) + (j * kT + int(threadIdx.x)) * 8);
+#pragma unroll
+      for (int i = 0; i < kB; ++i)
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          rb[i][j] = *reinterpret_cast<const u4v*>(block<TB>(b, parts.b[q], b0 + i, k) + (j * kT + int(threadIdx.x)) * 8);
+    };
+    auto stage = [&](uint16_t* s) {
+#pragma unroll
+      for (int i = 0; i < kA; ++i)
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          *reinterpret_cast<u4v*>(s + i * kBlkElems + (j * kT + int(threadIdx.x)) * 8) = ra[i][j];
+#pragma unroll
+      for (int i = 0; i < kB; ++i)
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          *reinterpret_cast<u4v*>(s + (kA + i) * kBlkElems + (j * kT + int(threadIdx.x)) * 8) = rb[i][j];
+    };
+    int q = 0, k = k0;
+    const int steps = parts.n * (k1 - k0);
+    if (steps <= 0) return;
+    fetch(q, k);
+    stage(sm);
+    __syncthreads();
+    for (int s = 0; s < steps; ++s) {
+      const bool more = s + 1 < steps;
+      if (more) {
+        if (++k == k1) k = k0, ++q;
+        fetch(q, k);
+      }
+      const uint16_t* cur = sm + (s & 1) * kStage;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        bf8 x[FM], y[FN];
+#pragma unroll
+        for (int i = 0; i < FM; ++i) x[i] = piece<TA>(cur, wa + i, kk, lane);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) y[j] = piece<TB>(cur + kA * kBlkElems, wb + j, kk, lane);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
+      }
+      if (more) stage(sm + ((s + 1) & 1) * kStage);
+      __syncthreads();
+    }
+  }
+};
+
+// Accumulator i of a 32 x 32 piece: its row for this lane; its column is lane % 32.
+__device__ __forceinline__ int acc_row(int i, int lane) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
+
+// ------------------------------------------------------------------ rows and packing
+// What lm_scores needs of a packed row.
+struct RowInfo {
+  int32_t target;  // -1: the row does not count
+  float coef;      // scale / counted
+  float lse;
+  int32_t pad;
+};
+
+template <typename F>
+__device__ __forceinline__ F block_sum(F x, F* sm) {
+  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);
+  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = x;
+  __syncthreads();
+  F t = 0;
+  for (int i = 0; i < int(blockDim.x) / 64; ++i) t += sm[i];
+  __syncthreads();
+  return t;
+}
+
+__global__ __launch_bounds__(kThreads) void lm_count(const int64_t* targets, int64_t rows, int64_t vocab, int32_t* count) {
+  __shared__ int32_t sm[kThreads / 64];
+  const int64_t* t = targets + blockIdx.x * rows;
+  int32_t n = 0;
+  for (int64_t i = threadIdx.x; i < rows; i += kThreads) n += uint64_t(t[i]) < uint64_t(vocab) ? 1 : 0;
+  n = block_sum(n, sm);
+  if (threadIdx.x == 0) count[blockIdx.x] = n;
+}
+
+struct PackRows {
+  const int64_t* targets;  // NULL: no rows are left out and no RowInfo is written
+  const float* lse;        // NULL for the loss
+  const float* scale;
+  const int32_t* count;
+  RowInfo* info;
+  int64_t vocab;
+};
+
+// One block per workgroup.  Groups of `rows` source rows start at a block of their own
+// (`blocks` of them each).
+template <typename T, int P>
+__global__ __launch_bounds__(kThreads) void lm_pack(const T* src, int64_t rows, int32_t dim, int32_t blocks, int32_t cb,
+                                                    uint16_t* dst, int64_t part, PackRows pr, Drop d) {
+  const int64_t rb = blockIdx.x / cb;
+  const int32_t c0 = int32_t(blockIdx.x % cb) * kBlk;
+  const int64_t w = rb / blocks, t0 = (rb % blocks) * kBlk;
+  const uint64_t step = d.on ? step_of(d) : 0;
+#pragma unroll
+  for (int it = 0; it < 2; ++it) {
+    const int r = it * 32 + int(threadIdx.x) / 8, c = c0 + int(threadIdx.x % 8) * 8;
+    const int64_t t = t0 + r, row = w * rows + t;
+    int64_t target = 0;
+    bool on = t < rows;
+    if (pr.targets != nullptr) {
+      target = on ? pr.targets[row] : -1;
+      on = uint64_t(target) < uint64_t(pr.vocab);
+      if (c == 0) {
+        RowInfo ri{};
+        ri.target = on ? int32_t(target) : -1;
+        if (on && pr.count != nullptr) {
+          ri.coef = float((pr.scale != nullptr ? double(pr.scale[w]) : 1.0) / double(pr.count[w]));
+          ri.lse = pr.lse[row];
+        }
+        pr.info[rb * kBlk + r] = ri;
+      }
+    }
+    float x[8] = {};
+    if (on && c < dim) {
+      const T* p = src + row * dim + c;
+      if (c + 8 <= dim) {
+        load<8>(p, x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (c + e < dim) x[e] = widen(p[e]);
+      }
+      if (d.on) drop<8>(d, step, uint64_t(row) * uint64_t(dim) + uint64_t(c), x);
+    }
+    uint16_t h[8][P];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) split<P>(x[e], h[e]);
+    uint16_t* o = dst + int64_t(blockIdx.x) * kBlkElems + r * kBlk + ((int(threadIdx.x % 8) ^ turn(r)) << 3);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      s8v v;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = short(h[e][p]);
+      *reinterpret_cast<s8v*>(o + p * part) = v;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ scores
+// Tile order: every XCD (workgroups are dealt to the eight in turn) gets a contiguous part
+// of the list in which kGroup row tiles take turns on each vocabulary tile, so that both
+// stay in its L2.
+__device__ __forceinline__ bool tile_at(int64_t id, int64_t n_v, int64_t n_t, int& v, int& t) {
+  const int64_t total = n_v * n_t, per = (total + 7) / 8, at = (id % 8) * per + id / 8;
+  if (at >= total || id / 8 >= per) return false;
+  const int64_t group = at / (n_v * kGroup), in = at % (n_v * kGroup);
+  const int64_t width = min(int64_t(kGroup), n_t - group * kGroup);
+  v = int(in / width);
+  t = int(group * kGroup + in % width);
+  return true;
+}
+
+typedef Gemm<2, 4, 4, 2, false, false> ScoreGemm;
+
+struct ScoreArgs {
+  Mat w, x;
+  Parts parts;
+  int32_t v0, v1;        // vocabulary blocks [v0, v1) of this launch
+  int32_t t0, t1;        // row blocks
+  int64_t vocab;
+  const RowInfo* info;   // from row block 0 on
+  float2* stat;          // loss: [vocabulary tile][row of the launch] maximum and sum
+  float* hit;            // loss: [row] the target's score
+  uint16_t* g;           // gradient: blocks [t1 - t0][v1 - v0]
+  int64_t g_part;
+};
+
+// Scores of 256 words x 256 rows: lane l of a wave holds words in its accumulators and row
+// l mod 32 of each of its two pieces, so a row's maximum and sum are taken within a lane, then
+// over its two lane halves and the two waves that share the row.
+template <int GP>
+__global__ __launch_bounds__(ScoreGemm::kT) void lm_scores(ScoreArgs p) {
+  __shared__ __align__(16) uint16_t sm[2 * ScoreGemm::kStage];
+  int vt, tt;
+  if (!tile_at(blockIdx.x, (p.v1 - p.v0 + kTile - 1) / kTile, (p.t1 - p.t0 + kTile - 1) / kTile, vt, tt)) return;
+  const int v0 = p.v0 + vt * kTile, t0 = p.t0 + tt * kTile;
+  f16v acc[4][2] = {};
+  ScoreGemm::run(p.w, v0, p.x, t0, 0, p.w.cb, p.parts, sm, acc);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t word0 = int64_t(v0) * kBlk + (wave / 4) * 128;  // of this wave
+  const int n_words = int(min(int64_t(128), p.vocab - word0));  // may be negative
+  const int tblk = t0 + wave % 4;                               // the wave's row block
+  const bool live = tblk < p.t1;
+  if constexpr (GP == 0) {
+    float2* joined = reinterpret_cast<float2*>(sm);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t row = int64_t(tblk) * kBlk + j * 32 + (lane & 31);
+      float m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (i * 32 + acc_row(e, lane) >= n_words) acc[i][j][e] = -INFINITY;
+          m = fmaxf(m, acc[i][j][e]);
+        }
+      m = fmaxf(m, __shfl_xor(m, 32));
+      const float base = m == -INFINITY ? 0.f : m;
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s += __expf(acc[i][j][e] - base);
+      s += __shfl_xor(s, 32);
+      const int64_t local = live ? p.info[row].target - word0 : -1;
+      const bool here = local >= 0 && local < n_words && (int(local) >> 2 & 1) == lane >> 5;
+      if (__any(here)) {
+        float hit = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (i * 32 + acc_row(e, lane) == int(local)) hit = acc[i][j][e];
+        if (here) p.hit[row] = hit;
+      }
+      // the main loop ends in a barrier: its LDS is free
+      if (lane < 32) joined[(wave / 4) * 256 + (wave % 4) * 64 + j * 32 + lane] = make_float2(m, s);
+    }
+    __syncthreads();
+    const int r = threadIdx.x;
+    if (r < 256 && t0 + r / kBlk < p.t1) {
+      const float2 a = joined[r], b = joined[256 + r];
+      const float m = fmaxf(a.x, b.x), base = m == -INFINITY ? 0.f : m;
+      p.stat[int64_t(vt) * (p.t1 - p.t0) * kBlk + int64_t(tt) * 256 + r] =
+          make_float2(m, a.y * __expf(a.x - base) + b.y * __expf(b.x - base));
+    }
+  } else {
+    uint16_t* own = sm + wave * 2 * kBlkElems;  // two blocks of g: words [0, 64) and [64, 128) of the wave
+    float coef[2], lse[2];
+    int local[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      RowInfo ri{-1, 0.f, 0.f, 0};
+      if (live) ri = p.info[int64_t(tblk) * kBlk + j * 32 + (lane & 31)];
+      coef[j] = ri.target < 0 ? 0.f : ri.coef;
+      lse[j] = ri.lse;
+      local[j] = ri.target < 0 ? -1 : int(max(int64_t(-1), min(int64_t(1 << 20), ri.target - word0)));
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int v = i * 32 + acc_row(e, lane);
+          float x = __expf(acc[i][j][e] - lse[j]);
+          if (v == local[j]) x -= 1.f;
+          acc[i][j][e] = v < n_words && coef[j] != 0.f ? x * coef[j] : 0.f;
+        }
+#pragma unroll
+    for (int part = 0; part < GP; ++part) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e4 = 0; e4 < 4; ++e4) {
+            s4v v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = acc[i][j][e4 * 4 + e];
+              const uint16_t b = narrow_bits(x);
+              v[e] = short(b);
+              if (GP > 1) acc[i][j][e4 * 4 + e] = x - widen(b);
+            }
+            const int r = j * 32 + (lane & 31), c8 = (i & 1) * 4 + e4;
+            *reinterpret_cast<s4v*>(own + (i >> 1) * kBlkElems + r * kBlk + ((c8 ^ turn(r)) << 3) + (lane >> 5) * 4) = v;
+          }
+      __syncthreads();
+      const int vb = v0 - p.v0 + (wave / 4) * 2, n_v = p.v1 - p.v0;
+      if (live) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          if (vb + b >= n_v) break;
+          uint16_t* o = p.g + part * p.g_part + (int64_t(tblk - p.t0) * n_v + vb + b) * kBlkElems;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<u4v*>(o + (k * 64 + lane) * 8) = *reinterpret_cast<const u4v*>(own + b * kBlkElems + (k * 64 + lane) * 8);
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// lse and loss of a row from its `tiles` maxima and sums: 32 rows per workgroup, 8 lanes
+// (64 apart) each.
+__global__ __launch_bounds__(kThreads) void lm_rows(const float2* stat, int32_t tiles, int64_t ld, const RowInfo* info,
+                                                    const float* hit, int64_t rows, float* losses, float* lse) {
+  __shared__ float2 sm[kThreads];
+  const int r = threadIdx.x % 32, part = threadIdx.x / 32;
+  const int64_t row = int64_t(blockIdx.x) * 32 + r;
+  float m = -INFINITY, s = 0.f;
+  if (row < rows)
+    for (int i = part; i < tiles; i += 8) {
+      const float2 a = stat[i * ld + row];
+      const float n = fmaxf(m, a.x), base = n == -INFINITY ? 0.f : n;
+      s = s * __expf(m - base) + a.y * __expf(a.x - base);
+      m = n;
+    }
+  sm[threadIdx.x] = make_float2(m, s);
+  __syncthreads();
+  if (part != 0 || row >= rows) return;
+  for (int i = 1; i < 8; ++i) {
+    const float2 a = sm[i * 32 + r];
+    const float n = fmaxf(m, a.x), base = n == -INFINITY ? 0.f : n;
+    s = s * __expf(m - base) + a.y * __expf(a.x - base);
+    m = n;
+  }
+  const bool on = info[row].target >= 0;
+  const float l = m + logf(s);
+  lse[row] = on ? l : 0.f;
+  losses[row] = on ? l - hit[row] : 0.f;
+}
+
+__global__ __launch_bounds__(kThreads) void lm_mean(const float* losses, const RowInfo* info, int64_t rows, float* mean) {
+  __shared__ double sm[kThreads / 64];
+  const int64_t at = blockIdx.x * rows;
+  double s = 0.0, n = 0.0;
+  for (int64_t i = threadIdx.x; i < rows; i += kThreads) {
+    s += double(losses[at + i]);
+    n += info[at + i].target >= 0 ? 1.0 : 0.0;
+  }
+  s = block_sum(s, sm);
+  n = block_sum(n, sm);
+  if (threadIdx.x == 0) mean[blockIdx.x] = n > 0.0 ? float(s / n) : 0.f;
+}
+
+// ------------------------------------------------------------------ products with g
+typedef Gemm<2, 4, 4, 2, false, true> DxGemm;
+typedef Gemm<2, 4, 4, 2, true, true> DwGemm;
+
+struct DxArgs {
+  Mat g, w;  // w from the piece's first block on
+  Parts parts;
+  int32_t kb, splits;
+  float* out;  // [splits][row][ld]
+  int64_t rows, ld;
+  int32_t add;
+};
+
+__global__ __launch_bounds__(DxGemm::kT) void lm_dx(DxArgs p) {
+  __shared__ __align__(16) uint16_t sm[2 * DxGemm::kStage];
+  const int n_c = (p.w.cb + kTile - 1) / kTile;
+  const int split = blockIdx.x % p.splits, c0 = int(blockIdx.x / p.splits) % n_c * kTile;
+  const int r0 = int(blockIdx.x / p.splits) / n_c * kTile;
+  const int k0 = int(int64_t(p.kb) * split / p.splits), k1 = int(int64_t(p.kb) * (split + 1) / p.splits);
+  f16v acc[4][2] = {};
+  DxGemm::run(p.g, r0, p.w, c0, k0, k1, p.parts, sm, acc);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float* out = p.out + split * p.rows * p.ld;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t c = int64_t(c0) * kBlk + (wave % 4) * 64 + j * 32 + (lane & 31);
+      const int64_t r = int64_t(r0) * kBlk + (wave / 4) * 128 + i * 32;
+      if (c >= p.ld) continue;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int64_t row = r + acc_row(e, lane);
+        if (row >= p.rows) continue;
+        float* o = out + row * p.ld + c;
+        *o = p.add ? *o + acc[i][j][e] : acc[i][j][e];
+      }
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void lm_dx_out(const float* part, int32_t splits, int64_t packed_rows, int64_t ld,
+                                                      const RowInfo* info, int64_t rows, int64_t packed, int32_t dim,
+                                                      T* out, Drop d) {
+  const int64_t row = blockIdx.x, w = row / rows, r = w * packed + row % rows;
+  const bool on = info[r].target >= 0;
+  const uint64_t step = d.on ? step_of(d) : 0;
+  for (int32_t c = int32_t(threadIdx.x) * 4; c < dim; c += kThreads * 4) {
+    float x[4] = {};
+    if (on) {
+      for (int s = 0; s < splits; ++s) {
+        float y[4];
+        load<4>(part + (s * packed_rows + r) * ld + c, y);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] += y[e];
+      }
+      if (d.on) drop<4>(d, step, uint64_t(row) * uint64_t(dim) + uint64_t(c), x);
+    }
+    T* o = out + row * dim + c;
+    if (c + 4 <= dim) {
+      store<4>(o, x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < dim) put(o + e, x[e]);
+    }
+  }
+}
+
+struct DwArgs {
+  Mat g, x;
+  Parts parts;
+  int32_t tw;         // row blocks per worker
+  int32_t v0;         // first vocabulary block of the piece
+  int64_t vocab, dim, stride;
+  int32_t add;
+};
+
+template <typename GT>
+__global__ __launch_bounds__(DwGemm::kT) void lm_dw(DwArgs p, GT* grads) {
+  __shared__ __align__(16) uint16_t sm[2 * DwGemm::kStage];
+  const int n_c = (p.x.cb + kTile - 1) / kTile;
+  const int w = blockIdx.y, c0 = int(blockIdx.x % n_c) * kTile, r0 = int(blockIdx.x / n_c) * kTile;
+  f16v acc[4][2] = {};
+  DwGemm::run(p.g, r0, p.x, c0, w * p.tw, (w + 1) * p.tw, p.parts, sm, acc);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  GT* out = grads + w * p.stride;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t c = int64_t(c0) * kBlk + (wave % 4) * 64 + j * 32 + (lane & 31);
+      const int64_t r = int64_t(r0) * kBlk + (wave / 4) * 128 + i * 32;
+      if (c >= p.dim) continue;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int64_t in = r + acc_row(e, lane), row = int64_t(p.v0) * kBlk + in;
+        if (in >= int64_t(p.g.cb) * kBlk || row >= p.vocab) continue;
+        GT* o = out + row * p.dim + c;
+        put(o, p.add ? widen(*o) + acc[i][j][e] : acc[i][j][e]);
+      }
+    }
+}
+
+// ------------------------------------------------------------------ embedding
+template <typename T>
+__global__ __launch_bounds__(64) void lm_embed(const T* table, int64_t vocab, int32_t dim, const int64_t* tokens, T* out,
+                                               Drop d) {
+  const int64_t row = blockIdx.x;
+  const int32_t c = (int32_t(blockIdx.y) * 64 + int32_t(threadIdx.x)) * 8;
+  if (c >= dim) return;
+  const int64_t t = tokens[row];
+  const int n = min(8, dim - c);
+  float x[8] = {};
+  if (uint64_t(t) < uint64_t(vocab)) {
+    const T* p = table + t * dim + c;
+    if (n == 8) {
+      load<8>(p, x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < n) x[e] = widen(p[e]);
+    }
+    if (d.on) drop<8>(d, step_of(d), uint64_t(row) * uint64_t(dim) + uint64_t(c), x);
+  }
+  T* o = out + row * dim + c;
+  if (n == 8) {
+    store<8>(o, x);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) put(o + e, x[e]);
+  }
+}
+
+// A pair is token << 32 | row; pairs of tokens outside the vocabulary come last.
+constexpr uint64_t kNoToken = 0xffffffffull;
+
+// One chunk of a worker's pairs, sorted (bitonic: a fixed network on distinct keys).
+__global__ __launch_bounds__(kSortThreads) void lm_sort(const int64_t* tokens, int64_t rows, int64_t vocab, int32_t size,
+                                                        uint64_t* keys) {
+  __shared__ uint64_t sm[kSortMax];
+  const int64_t at = int64_t(blockIdx.y) * rows, t0 = int64_t(blockIdx.x) * size;
+  for (int i = threadIdx.x; i < size; i += kSortThreads) {
+    uint64_t key = ~0ull;
+    if (t0 + i < rows) {
+      const uint64_t t = uint64_t(tokens[at + t0 + i]);
+      key = (t < uint64_t(vocab) ? t : kNoToken) << 32 | uint64_t(t0 + i);
+    }
+    sm[i] = key;
+  }
+  __syncthreads();
+  for (int k = 2; k <= size; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      for (int i = threadIdx.x; i < size / 2; i += kSortThreads) {
+        const int lo = (i & ~(j - 1)) * 2 + (i & (j - 1)), hi = lo + j;
+        const uint64_t a = sm[lo], b = sm[hi];
+        if ((a > b) == ((lo & k) == 0)) sm[lo] = b, sm[hi] = a;
+      }
+      __syncthreads();
+    }
+  for (int i = threadIdx.x; i < size; i += kSortThreads)
+    if (t0 + i < rows) keys[at + t0 + i] = sm[i];
+}
+
+// Sorted runs of `run` pairs into runs of twice that: a pair's place is its own plus the
+// number of smaller ones in the other run.
+__global__ __launch_bounds__(kThreads) void lm_merge(const uint64_t* src, uint64_t* dst, int64_t rows, int64_t run) {
+  const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  if (i >= rows) return;
+  const uint64_t* s = src + int64_t(blockIdx.y) * rows;
+  const int64_t pair = i / (2 * run) * (2 * run), mid = min(rows, pair + run), end = min(rows, pair + 2 * run);
+  const bool right = i >= mid;
+  const uint64_t key = s[i];
+  int64_t lo = right ? pair : mid, hi = right ? mid : end;
+  const int64_t from = lo;
+  while (lo < hi) {
+    const int64_t m = (lo + hi) / 2;
+    if (s[m] < key) lo = m + 1;
+    else hi = m;
+  }
+  dst[int64_t(blockIdx.y) * rows + (right ? i - mid : i - pair) + pair + (lo - from)] = key;
+}
+
+template <typename GT>
+__global__ __launch_bounds__(kThreads) void lm_zero(GT* table, int64_t n, int64_t stride) {
+  constexpr int kV = 16 / sizeof(GT);
+  const int64_t i = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * kV;
+  GT* p = table + int64_t(blockIdx.y) * stride + i;
+  if (i + kV <= n) {
+    *reinterpret_cast<u4v*>(p) = u4v{};
+  } else {
+    for (int64_t e = i; e < n; ++e) p[e - i] = GT(0);
+  }
+}
+
+template <typename GT>
+__device__ __forceinline__ void write_row(GT* o, int n, bool add, float (&x)[4]) {
+  if (n == 4) {
+    float y[4] = {};
+    if (add) load<4>(o, y);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] += x[e];
+    store<4>(o, y);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) put(o + e, (add ? widen(o[e]) : 0.f) + x[e]);
+  }
+}
+
+struct SumArgs {
+  const uint64_t* keys;
+  int64_t rows;  // per worker
+  int32_t dim, dpad, n_runs, add;
+  int64_t stride;
+  float* part;  // [worker][run][2][dpad]: a token's sum from its earlier run on, and the start of one that goes on
+};
+
+// kRun sorted pairs x 256 columns per wave, summed in their order.  A token whose pairs lie
+// in one run is written here; the others leave a part per run for lm_join.
+template <typename T, typename GT>
+__global__ __launch_bounds__(64) void lm_sum(SumArgs p, const T* dout, GT* table, Drop d) {
+  const int64_t w = blockIdx.z, run = blockIdx.x, i0 = run * kRun, i1 = min(p.rows, i0 + kRun);
+  const int32_t c = (int32_t(blockIdx.y) * 64 + int32_t(threadIdx.x)) * 4;
+  const uint64_t* keys = p.keys + w * p.rows;
+  const int n = min(4, p.dim - c);
+  if (n <= 0) return;
+  const uint64_t step = d.on ? step_of(d) : 0;
+  const uint64_t before = i0 > 0 ? keys[i0 - 1] >> 32 : ~0ull, after = i1 < p.rows ? keys[i1] >> 32 : ~0ull;
+  float* part = p.part + (w * p.n_runs + run) * 2 * p.dpad + c;
+  float sum[4] = {};
+  for (int64_t i = i0; i < i1; ++i) {
+    const uint64_t key = keys[i], token = key >> 32;
+    if (token == kNoToken) break;
+    const int64_t row = w * p.rows + int64_t(key & 0xffffffffu);
+    const T* s = dout + row * p.dim + c;
+    float x[4] = {};
+    if (n == 4) {
+      load<4>(s, x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < n) x[e] = widen(s[e]);
+    }
+    if (d.on) drop<4>(d, step, uint64_t(row) * uint64_t(p.dim) + uint64_t(c), x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] += x[e];
+    const uint64_t next = i + 1 < i1 ? keys[i + 1] >> 32 : after;
+    if (next == token && i + 1 < i1) continue;
+    // the token's pairs of this run end here
+    const bool from_before = token == before, goes_on = next == token;
+    if (from_before || goes_on) {
+      store<4>(part + (from_before ? 0 : p.dpad), sum);
+    } else {
+      write_row(table + w * p.stride + int64_t(token) * p.dim + c, n, p.add != 0, sum);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = 0.f;
+  }
+}
+
+// The tokens whose pairs start in this run and go on after it.
+template <typename GT>
+__global__ __launch_bounds__(64) void lm_join(SumArgs p, GT* table) {
+  const int64_t w = blockIdx.z, run = blockIdx.x, i0 = run * kRun, i1 = i0 + kRun;
+  const uint64_t* keys = p.keys + w * p.rows;
+  if (i1 >= p.rows) return;
+  const uint64_t token = keys[i1 - 1] >> 32;
+  if (token == kNoToken || keys[i1] >> 32 != token || (i0 > 0 && keys[i0 - 1] >> 32 == token)) return;
+  const int32_t c = (int32_t(blockIdx.y) * 64 + int32_t(threadIdx.x)) * 4;
+  const int n = min(4, p.dim - c);
+  if (n <= 0) return;
+  const float* part = p.part + (w * p.n_runs + run) * 2 * p.dpad + c;
+  float sum[4];
+  load<4>(part + p.dpad, sum);
+  for (int64_t i = i1; i < p.rows && keys[i] >> 32 == token; i += kRun) {
+    part += 2 * p.dpad;
+    float x[4];
+    load<4>(part, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] += x[e];
+  }
+  write_row(table + w * p.stride + int64_t(token) * p.dim + c, n, p.add != 0, sum);
+}
+
+// ------------------------------------------------------------------ dropout
+template <typename T>
+__global__ __launch_bounds__(kThreads) void lm_dropout(const T* x, int64_t xs, const T* residual, int64_t rs, T* out,
+                                                       int64_t os, int64_t n, int64_t cols, Drop d) {
+  const int64_t group = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  if (group * 4 >= n) return;
+  uint32_t w[4];
+  philox(uint64_t(group), step_of(d), d.key0, d.key1, w);
+  int64_t r = group * 4 / cols, c = group * 4 % cols;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (group * 4 + e >= n) break;
+    float y = uint64_t(w[e]) >= d.keep_from ? widen(x[r * xs + c]) * d.scale : 0.f;
+    if (residual != nullptr) y += widen(residual[r * rs + c]);
+    put(out + r * os + c, y);
+    if (++c == cols) c = 0, ++r;
+  }
+}
+
+// ------------------------------------------------------------------ host helpers
+psgd_status fail(psgd_status s, const std::string& msg) {
+  set_error(msg);
+  return s;
+}
+
+psgd_status hip_fail(const char* what, hipError_t e) {
+  return fail(PSGD_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
+}
+
+uint64_t a256(uint64_t x) { return (x + 255) / 256 * 256; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+psgd_status take_event(psgd_lm_plan* plan, hipEvent_t* ev) {
+  if (!plan->event_pool.empty()) {
+    *ev = plan->event_pool.back();
+    plan->event_pool.pop_back();
+    return PSGD_OK;
+  }
+  const hipError_t e = hipEventCreate(ev);
+  return e == hipSuccess ? PSGD_OK : hip_fail("hipEventCreate", e);
+}
+
+// Launch on `st`; with timing on, through hipExtLaunchKernelGGL with events the runtime
+// records with the dispatch itself.
+template <typename... KArgs, typename... Args>
+psgd_status launch(psgd_lm_plan* plan, int kid, void (*kernel)(KArgs...), dim3 grid, int threads, hipStream_t st, Args... args) {
+  hipEvent_t a = nullptr, b = nullptr;
+  if (plan->timing) {
+    room_for_timing(plan);
+    psgd_status s = take_event(plan, &a);
+    if (s == PSGD_OK) s = take_event(plan, &b);
+    if (s != PSGD_OK) {
+      if (a) plan->event_pool.push_back(a);
+      return s;
+    }
+    hipExtLaunchKernelGGL(kernel, grid, dim3(unsigned(threads)), 0, st, a, b, 0, args...);
+  } else {
+    hipLaunchKernelGGL(kernel, grid, dim3(unsigned(threads)), 0, st, args...);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) {
+    if (plan->timing) {
+      plan->event_pool.push_back(a);
+      plan->event_pool.push_back(b);
+    }
+    return hip_fail((std::string("launch ") + kNames[kid]).c_str(), e);
+  }
+  if (plan->timing) plan->pending.push_back(PendingTiming{kid, a, b});
+  return PSGD_OK;
+}
+
+// A graph must not hold the events of timed launches.
+psgd_status check_capture(const char* fn, const psgd_lm_plan* plan, hipStream_t st) {
+  if (!plan->timing) return PSGD_OK;
+  hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
+  const hipError_t e = hipStreamIsCapturing(st, &cs);
+  if (e != hipSuccess) return hip_fail("hipStreamIsCapturing", e);
+  return cs == hipStreamCaptureStatusNone
+             ? PSGD_OK
+             : fail(PSGD_ERR_INVALID_ARG, std::string(fn) + ": a call can be captured into a graph only with kernel timing off");
+}
+
+psgd_status make_drop(const char* fn, const psgd_dropout_config* c, Drop* out) {
+  *out = Drop{0, 0, 0, nullptr, 1.f, 0};
+  if (c == nullptr) return PSGD_OK;
+  if (!(c->p >= 0.0 && c->p <= 1.0)) return fail(PSGD_ERR_INVALID_ARG, std::string(fn) + ": dropout's p must be in [0, 1]");
+  if (uintptr_t(c->step) % 8 != 0) return fail(PSGD_ERR_INVALID_ARG, std::string(fn) + ": dropout's step is not 8-byte aligned");
+  out->keep_from = uint64_t(c->p * 4294967296.0);
+  out->key0 = uint32_t(c->seed);
+  out->key1 = uint32_t(c->seed >> 32);
+  out->step = c->step;
+  out->scale = c->p < 1.0 ? float(1.0 / (1.0 - c->p)) : 0.f;
+  out->on = c->p > 0.0 ? 1 : 0;
+  return PSGD_OK;
+}
+
+int parts_of(psgd_dtype t) { return t == PSGD_F32 ? 3 : 1; }
+int g_parts(const psgd_lm_plan* plan) { return plan->act == PSGD_F32 || plan->grad == PSGD_F32 ? 3 : 1; }
+
+// Part products of x (a parts) with y (b parts) that a result of 24 (or, `few`, 16) bits needs.
+Parts make_parts(int a, int b, bool few) {
+  Parts p{};
+  const int most = few ? 1 : 2;
+  for (int s = most; s >= 0; --s)  // the small ones first
+    for (int i = 0; i <= s; ++i)
+      if (i < a && s - i < b) {
+        p.a[p.n] = uint8_t(i);
+        p.b[p.n] = uint8_t(s - i);
+        ++p.n;
+      }
+  return p;
+}
+
+struct Views {
+  Mat x, w;
+  uint16_t *xp, *wp, *g;
+  RowInfo* info;
+  int32_t* count;
+  float2* stat;
+  float *hit, *dx;
+};
+
+Views views(const psgd_lm_plan* plan, void* workspace, int32_t tb) {
+  char* ws = static_cast<char*>(workspace);
+  Views v{};
+  v.xp = reinterpret_cast<uint16_t*>(ws + plan->ws_x);
+  v.wp = reinterpret_cast<uint16_t*>(ws + plan->ws_w);
+  v.g = reinterpret_cast<uint16_t*>(ws + plan->ws_g);
+  v.info = reinterpret_cast<RowInfo*>(ws + plan->ws_info);
+  v.count = reinterpret_cast<int32_t*>(ws + plan->ws_count);
+  v.stat = reinterpret_cast<float2*>(ws + plan->ws_stat);
+  v.hit = reinterpret_cast<float*>(ws + plan->ws_hit);
+  v.dx = reinterpret_cast<float*>(ws + plan->ws_dx);
+  v.x = Mat{v.xp, int64_t(tb) * plan->db * kBlkElems, tb, plan->db};
+  v.w = Mat{v.wp, int64_t(plan->vb) * plan->db * kBlkElems, plan->vb, plan->db};
+  return v;
+}
+
+// x in `groups` of `rows` rows, and the table.
+psgd_status enqueue_pack(psgd_lm_plan* plan, const Views& v, const void* x, const void* params, int64_t rows, int32_t blocks,
+                         const PackRows& pr, const Drop& d, hipStream_t st) {
+  const Drop none{0, 0, 0, nullptr, 1.f, 0};
+  const PackRows all{};
+  const dim3 gx(unsigned(int64_t(v.x.rb) * v.x.cb)), gw(unsigned(int64_t(v.w.rb) * v.w.cb));
+  const int32_t dim = int32_t(plan->dim);
+  psgd_status s;
+  if (plan->act == PSGD_F32) {
+    s = launch(plan, kPack, lm_pack<float, 3>, gx, kThreads, st, static_cast<const float*>(x), rows, dim, blocks, v.x.cb, v.xp,
+               v.x.part, pr, d);
+    if (s != PSGD_OK) return s;
+    return launch(plan, kPack, lm_pack<float, 3>, gw, kThreads, st, static_cast<const float*>(params) + plan->offset, plan->vocab,
+                  dim, v.w.rb, v.w.cb, v.wp, v.w.part, all, none);
+  }
+  s = launch(plan, kPack, lm_pack<uint16_t, 1>, gx, kThreads, st, static_cast<const uint16_t*>(x), rows, dim, blocks, v.x.cb, v.xp,
+             v.x.part, pr, d);
+  if (s != PSGD_OK) return s;
+  return launch(plan, kPack, lm_pack<uint16_t, 1>, gw, kThreads, st, static_cast<const uint16_t*>(params) + plan->offset,
+                plan->vocab, dim, v.w.rb, v.w.cb, v.wp, v.w.part, all, none);
+}
+
+unsigned score_grid(const ScoreArgs& a) {
+  return unsigned(ceil_div(ceil_div(a.v1 - a.v0, kTile) * ceil_div(a.t1 - a.t0, kTile), 8) * 8);
+}
+
+psgd_status enqueue_loss(psgd_lm_plan* plan, const void* x, const void* params, const int64_t* targets, const Drop& d,
+                         float* losses, float* lse, float* mean, void* workspace, hipStream_t st) {
+  const int64_t rows = plan->rows * plan->n_workers;
+  const Views v = views(plan, workspace, plan->tb);
+  const PackRows pr{targets, nullptr, nullptr, nullptr, v.info, plan->vocab};
+  psgd_status s = enqueue_pack(plan, v, x, params, rows, plan->tb, pr, d, st);
+  const int p = parts_of(plan->act);
+  for (int32_t t0 = 0; s == PSGD_OK && t0 < plan->tb; t0 += plan->chunk) {
+    ScoreArgs a{v.w, v.x, make_parts(p, p, false), 0, plan->vb, t0, std::min(plan->tb, t0 + plan->chunk), plan->vocab,
+                v.info, v.stat, v.hit, nullptr, 0};
+    s = launch(plan, kScores, lm_scores<0>, dim3(score_grid(a)), ScoreGemm::kT, st, a);
+    if (s != PSGD_OK) break;
+    const int64_t r0 = int64_t(t0) * kBlk, n = std::min(rows, int64_t(a.t1) * kBlk) - r0;
+    s = launch(plan, kRows, lm_rows, dim3(unsigned(ceil_div(n, 32))), kThreads, st, static_cast<const float2*>(v.stat),
+               int32_t(ceil_div(plan->vb, kTile)), int64_t(a.t1 - t0) * kBlk, static_cast<const RowInfo*>(v.info + r0),
+               static_cast<const float*>(v.hit + r0), n, losses + r0, lse + r0);
+  }
+  if (s != PSGD_OK) return s;
+  return launch(plan, kMean, lm_mean, dim3(unsigned(plan->n_workers)), kThreads, st, static_cast<const float*>(losses),
+                static_cast<const RowInfo*>(v.info), plan->rows, mean);
+}
+
+psgd_status enqueue_grad(psgd_lm_plan* plan, const void* x, const void* params, const int64_t* targets, const float* lse,
+                         const float* scale, const Drop& d, void* dx, void* grads, bool add, void* workspace, hipStream_t st) {
+  const int32_t tb = plan->tw * plan->n_workers;
+  const Views v = views(plan, workspace, tb);
+  psgd_status s = launch(plan, kCount, lm_count, dim3(unsigned(plan->n_workers)), kThreads, st, targets, plan->rows,
+                         plan->vocab, v.count);
+  if (s != PSGD_OK) return s;
+  const PackRows pr{targets, lse, scale, v.count, v.info, plan->vocab};
+  if ((s = enqueue_pack(plan, v, x, params, plan->rows, plan->tw, pr, d, st)) != PSGD_OK) return s;
+  const int p = parts_of(plan->act), gp = g_parts(plan);
+  const bool f32g = plan->grad == PSGD_F32;
+  const int64_t packed = int64_t(tb) * kBlk, ld = int64_t(plan->db) * kBlk;
+  for (int32_t v0 = 0; v0 < plan->vb; v0 += plan->piece) {
+    const int32_t v1 = std::min(plan->vb, v0 + plan->piece), n_v = v1 - v0;
+    const int64_t g_part = int64_t(tb) * n_v * kBlkElems;
+    const ScoreArgs a{v.w, v.x, make_parts(p, p, false), v0, v1, 0, tb, plan->vocab, v.info, nullptr, nullptr, v.g, g_part};
+    s = launch(plan, kScores, gp == 3 ? lm_scores<3> : lm_scores<1>, dim3(score_grid(a)), ScoreGemm::kT, st, a);
+    if (s != PSGD_OK) return s;
+    const Mat g{v.g, g_part, tb, n_v};
+    const int64_t n_c = ceil_div(plan->db, kTile);
+    if (dx != nullptr) {
+      Mat w = v.w;
+      w.p += int64_t(v0) * w.cb * kBlkElems;
+      w.rb = n_v;
+      const DxArgs b{g, w, make_parts(p == 3 ? gp : 1, p, false), n_v, plan->splits, v.dx, packed, ld, v0 > 0 ? 1 : 0};
+      s = launch(plan, kDx, lm_dx, dim3(unsigned(ceil_div(tb, kTile) * n_c * plan->splits)), DxGemm::kT, st, b);
+      if (s != PSGD_OK) return s;
+    }
+    if (grads != nullptr) {
+      const Parts parts = f32g ? make_parts(gp, p, false) : p == 3 ? make_parts(gp, p, true) : make_parts(1, 1, true);
+      const DwArgs b{g, v.x, parts, plan->tw, v0, plan->vocab, plan->dim, plan->worker_stride, add ? 1 : 0};
+      const dim3 grid(unsigned(ceil_div(n_v, kTile) * n_c), unsigned(plan->n_workers));
+      s = f32g ? launch(plan, kDw, lm_dw<float>, grid, DwGemm::kT, st, b, static_cast<float*>(grads) + plan->offset)
+               : launch(plan, kDw, lm_dw<uint16_t>, grid, DwGemm::kT, st, b, static_cast<uint16_t*>(grads) + plan->offset);
+      if (s != PSGD_OK) return s;
+    }
+  }
+  if (dx == nullptr) return PSGD_OK;
+  const dim3 grid(unsigned(plan->rows * plan->n_workers));
+  const RowInfo* info = v.info;
+  const float* part = v.dx;
+  const int64_t per = int64_t(plan->tw) * kBlk;
+  return plan->act == PSGD_F32 ? launch(plan, kDxOut, lm_dx_out<float>, grid, kThreads, st, part, plan->splits, packed, ld, info,
+                                        plan->rows, per, int32_t(plan->dim), static_cast<float*>(dx), d)
+                               : launch(plan, kDxOut, lm_dx_out<uint16_t>, grid, kThreads, st, part, plan->splits, packed, ld,
+                                        info, plan->rows, per, int32_t(plan->dim), static_cast<uint16_t*>(dx), d);
+}
+
+int32_t sort_size(int64_t rows) {
+  int32_t n = 2;
+  while (n < kSortMax && n < rows) n <<= 1;
+  return n;
+}
+
+template <typename T, typename GT>
+psgd_status enqueue_embed_grad(psgd_lm_plan* plan, const int64_t* tokens, const T* dout, const Drop& d, GT* table, bool add,
+                               void* workspace, hipStream_t st) {
+  char* ws = static_cast<char*>(workspace);
+  uint64_t* keys = reinterpret_cast<uint64_t*>(ws + plan->ws_key);
+  uint64_t* other = reinterpret_cast<uint64_t*>(ws + plan->ws_key2);
+  const unsigned W = unsigned(plan->n_workers);
+  const int32_t size = sort_size(plan->rows);
+  psgd_status s = launch(plan, kSort, lm_sort, dim3(unsigned(ceil_div(plan->rows, size)), W), kSortThreads, st, tokens, plan->rows,
+                         plan->vocab, size, keys);
+  for (int64_t run = size; s == PSGD_OK && run < plan->rows; run *= 2) {
+    s = launch(plan, kMerge, lm_merge, dim3(unsigned(ceil_div(plan->rows, kThreads)), W), kThreads, st,
+               static_cast<const uint64_t*>(keys), other, plan->rows, run);
+    std::swap(keys, other);
+  }
+  if (s != PSGD_OK) return s;
+  const int64_t n = plan->vocab * plan->dim;
+  if (!add) {
+    s = launch(plan, kZero, lm_zero<GT>, dim3(unsigned(ceil_div(n, kThreads * (16 / int64_t(sizeof(GT))))), W), kThreads, st, table,
+               n, plan->worker_stride);
+    if (s != PSGD_OK) return s;
+  }
+  const int32_t runs = int32_t(ceil_div(plan->rows, kRun)), dpad = int32_t(ceil_div(plan->dim, 4) * 4);
+  const SumArgs a{keys, plan->rows, int32_t(plan->dim), dpad, runs, add ? 1 : 0, plan->worker_stride,
+                  reinterpret_cast<float*>(ws + plan->ws_part)};
+  const dim3 grid(unsigned(runs), unsigned(ceil_div(plan->dim, 256)), W);
+  s = launch(plan, kSum, lm_sum<T, GT>, grid, 64, st, a, dout, table, d);
+  if (s != PSGD_OK || runs == 1) return s;
+  return launch(plan, kJoin, lm_join<GT>, grid, 64, st, a, table);
+}
+
+}  // namespace
+}  // namespace lm
+}  // namespace psgd
+
+using namespace psgd;
+using namespace psgd::lm;
+
+extern "C" psgd_status psgd_lm_plan_create(const psgd_layer* layers, int32_t n_layers, int32_t table, int32_t n_workers,
+                                           int64_t rows, psgd_dtype act_dtype, psgd_dtype grad_dtype, uint32_t flags,
+                                           psgd_lm_plan** out) {
+  if (out == nullptr) return refuse(PSGD_ERR_INVALID_ARG, "psgd_lm_plan_create: out is NULL");
+  *out = nullptr;
+  if (layers == nullptr) return refuse(PSGD_ERR_INVALID_ARG, "psgd_lm_plan_create: layers is NULL");
+  if (n_layers < 1) return refuse(PSGD_ERR_INVALID_ARG, "psgd_lm_plan_create: n_layers must be >= 1");
+  if (table < 0 || table >= n_layers) return refuse(PSGD_ERR_INVALID_ARG, "psgd_lm_plan_create: table is no tensor of the list");
+  if (n_workers < 1 || n_workers > 65535)
+    return refuse(PSGD_ERR_INVALID_ARG, "psgd_lm_plan_create: n_workers must be in 1..65535");
+  if (rows < 1 || rows > (int64_t(1) << 23) / n_workers)
+    return refuse(PSGD_ERR_INVALID_ARG, "psgd_lm_plan_create: n_workers * rows must be in 1..2^23");
+  for (const psgd_dtype t : {act_dtype, grad_dtype})
+    if (t != PSGD_F32 && t != PSGD_BF16) return refuse(PSGD_ERR_UNSUPPORTED, "psgd_lm_plan_create: unknown dtype");
+  if (flags != 0) return refuse(PSGD_ERR_UNSUPPORTED, "psgd_lm_plan_create: unknown flag bits");
+  psgd_lm_plan* plan = nullptr;
+  try {
+    plan = new psgd_lm_plan();
+    int64_t off = 0;
+    for (int32_t i = 0; i < n_layers; ++i) {
+      const int64_t r = layers[i].rows, c = layers[i].cols;
+      if (r < 1 || c < 1 || r > int64_t(0x7fffffff) / c) {
+        delete plan;
+        plan = nullptr;
+        return fail(PSGD_ERR_INVALID_ARG, "psgd_lm_plan_create: layer " + std::to_string(i) + " needs 1 <= rows*cols < 2^31");
+      }
+      if (i == table) plan->offset = off, plan->vocab = r, plan->dim = c;
+      off = (off + r * c + kAlignElems - 1) / kAlignElems * kAlignElems;
+    }
+    plan->n_layers = n_layers;
+    plan->n_workers = n_workers;
+    plan->table = table;
+    plan->rows = rows;
+    plan->act = act_dtype;
+    plan->grad = grad_dtype;
+    plan->worker_stride = off;
+    const int64_t n = rows * n_workers;
+    plan->vb = int32_t(ceil_div(plan->vocab, kBlk));
+    plan->db = int32_t(ceil_div(plan->dim, kBlk));
+    plan->tb = int32_t(ceil_div(n, kBlk));
+    plan->tw = int32_t(ceil_div(rows, kBlk));
+    const int64_t tbp = int64_t(plan->tw) * n_workers;  // >= tb
+    if (std::max<int64_t>(tbp, plan->vb) * plan->db > kMaxBlocks) {
+      delete plan;
+      plan = nullptr;
+      return fail(PSGD_ERR_INVALID_ARG, "psgd_lm_plan_create: the table or the workers' rows have over 2^23 blocks of 64 x 64");
+    }
+    const uint64_t blk = kBlkElems * 2, p = uint64_t(parts_of(act_dtype)), gp = uint64_t(g_parts(plan));
+    // pieces of about equal size, whole tiles each
+    const int64_t most = std::max<int64_t>(1, kPieceBytes / int64_t(gp * blk) / tbp / kTile) * kTile;
+    plan->piece = int32_t(ceil_div(ceil_div(plan->vb, ceil_div(plan->vb, most)), kTile) * kTile);
+    const int64_t dx_tiles = ceil_div(tbp, kTile) * ceil_div(plan->db, kTile);
+    plan->splits = int32_t(std::max<int64_t>(1, std::min<int64_t>({256 / dx_tiles, 16, std::min(plan->piece, plan->vb)})));
+    const int64_t v_tiles = ceil_div(plan->vb, kTile);
+    plan->chunk = int32_t(std::max<int64_t>(1, kStatBytes / (v_tiles * kTile * kBlk * 8)) * kTile);
+    uint64_t ws = 0;
+    auto take = [&](uint64_t bytes) {
+      const uint64_t at = ws;
+      ws = a256(ws + bytes);
+      return at;
+    };
+    plan->ws_x = take(p * uint64_t(tbp) * uint64_t(plan->db) * blk);
+    plan->ws_w = take(p * uint64_t(plan->vb) * uint64_t(plan->db) * blk);
+    plan->ws_info = take(uint64_t(tbp) * kBlk * sizeof(RowInfo));
+    plan->ws_count = take(uint64_t(n_workers) * 4);
+    const uint64_t common = ws;
+    plan->ws_stat = take(uint64_t(v_tiles) * uint64_t(std::min(plan->chunk, plan->tb)) * kBlk * 8);
+    plan->ws_hit = take(uint64_t(plan->tb) * kBlk * 4);
+    const uint64_t loss_end = ws;
+    ws = common;
+    plan->ws_g = take(gp * uint64_t(tbp) * uint64_t(std::min(plan->piece, plan->vb)) * blk);
+    plan->ws_dx = take(uint64_t(plan->splits) * uint64_t(tbp) * kBlk * uint64_t(plan->db) * kBlk * 4);
+    const uint64_t grad_end = ws;
+    ws = 0;
+    plan->ws_key = take(uint64_t(n) * 8);
+    plan->ws_key2 = take(uint64_t(n) * 8);
+    plan->ws_part = take(uint64_t(n_workers) * uint64_t(ceil_div(rows, kRun)) * 2 * uint64_t(ceil_div(plan->dim, 4)) * 16);
+    plan->workspace_bytes = std::max({loss_end, grad_end, ws});
+  } catch (...) {
+    delete plan;
+    return no_memory();
+  }
+  *out = plan;
+  return PSGD_OK;
+}
+
+extern "C" psgd_status psgd_lm_plan_sizes(const psgd_lm_plan* plan, psgd_lm_sizes* out) {
+  if (plan == nullptr || out == nullptr) return refuse(PSGD_ERR_INVALID_ARG, "psgd_lm_plan_sizes: NULL argument");
+  psgd_lm_sizes s{};
+  s.n_layers = plan->n_layers;
+  s.n_workers = plan->n_workers;
+  s.table = plan->table;
+  s.act_dtype = int32_t(plan->act);
+  s.grad_dtype = int32_t(plan->grad);
+  s.vocab = plan->vocab;
+  s.dim = plan->dim;
+  s.rows = plan->rows;
+  s.worker_stride = plan->worker_stride;
+  s.table_offset = plan->offset;
+  s.workspace_bytes = plan->workspace_bytes;
+  *out = s;
+  return PSGD_OK;
+}
+
+extern "C" psgd_status psgd_lm_plan_destroy(psgd_lm_plan* plan) {
+  if (plan == nullptr) return PSGD_OK;
+  for (const PendingTiming& t : plan->pending) {
+    (void)hipEventDestroy(t.start);
+    (void)hipEventDestroy(t.stop);
+  }
+  for (hipEvent_t ev : plan->event_pool) (void)hipEventDestroy(ev);
+  delete plan;
+  return PSGD_OK;
+}
+
+extern "C" psgd_status psgd_lm_plan_set_timing(psgd_lm_plan* plan, int32_t enable) {
+  if (plan == nullptr) return refuse(PSGD_ERR_INVALID_ARG, "psgd_lm_plan_set_timing: plan is NULL");
+  plan->timing = enable != 0;
+  return PSGD_OK;
+}
+
+extern "C" psgd_status psgd_lm_plan_kernel_stats(psgd_lm_plan* plan, psgd_kernel_stat* out, int32_t capacity, int32_t* count,
+                                                 int32_t reset) {
+  if (plan == nullptr) return refuse(PSGD_ERR_INVALID_ARG, "psgd_lm_plan_kernel_stats: plan is NULL");
+  if (capacity > 0 && out == nullptr) return refuse(PSGD_ERR_INVALID_ARG, "psgd_lm_plan_kernel_stats: out is NULL");
+  psgd_status st = PSGD_OK;
+  try {
+    st = collect_timings("psgd_lm_plan_kernel_stats", plan->pending, plan->event_pool, plan->stats);
+  } catch (...) {
+    return no_memory();
+  }
+  int32_t n = 0;
+  for (int k = 0; k < kNumK; ++k) {
+    if (plan->stats[k].launches == 0) continue;
+    if (n < capacity) {
+      psgd_kernel_stat ks{};
+      std::snprintf(ks.name, sizeof(ks.name), "%s", kNames[k]);
+      ks.launches = plan->stats[k].launches;
+      ks.total_ms = plan->stats[k].total_ms;
+      out[n] = ks;
+    }
+    ++n;
+  }
+  if (count != nullptr) *count = std::min(n, std::max<int32_t>(capacity, 0));
+  if (reset)
+    for (auto& k : plan->stats) k = KernelStat{};
+  return st;
+}
+
+namespace {
+
+uint64_t size_of(psgd_dtype t) { return t == PSGD_BF16 ? 2 : 4; }
+
+uint64_t act_bytes(const psgd_lm_plan* plan) {
+  return uint64_t(plan->rows) * uint64_t(plan->n_workers) * uint64_t(plan->dim) * size_of(plan->act);
+}
+
+ArgSpan act_span(const psgd_lm_plan* plan, const char* name, const void* p, bool nullable) {
+  return ArgSpan{name, p, act_bytes(plan), unsigned(size_of(plan->act)), nullable};
+}
+
+ArgSpan row_span(const psgd_lm_plan* plan, const char* name, const void* p, unsigned bytes) {
+  return ArgSpan{name, p, uint64_t(plan->rows) * uint64_t(plan->n_workers) * bytes, bytes, false};
+}
+
+ArgSpan params_span(const psgd_lm_plan* plan, const void* p) {
+  return ArgSpan{"params", p, uint64_t(plan->worker_stride) * size_of(plan->act), 16, false};
+}
+
+ArgSpan grads_span(const psgd_lm_plan* plan, const void* p, bool nullable) {
+  return ArgSpan{"grads", p, uint64_t(plan->n_workers) * uint64_t(plan->worker_stride) * size_of(plan->grad), 16, nullable};
+}
+
+ArgSpan step_span(const psgd_dropout_config* d) { return ArgSpan{"dropout's step", d != nullptr ? d->step : nullptr, 8, 8, true}; }
+
+}  // namespace
+
+extern "C" psgd_status psgd_lm_embed(psgd_lm_plan* plan, const void* params, const int64_t* tokens,
+                                     const psgd_dropout_config* dropout, void* out, void* stream) {
+  static const char* const fn = "psgd_lm_embed";
+  try {
+    if (plan == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_lm_embed: plan is NULL");
+    Drop d;
+    psgd_status s = make_drop(fn, dropout, &d);
+    if (s != PSGD_OK) return s;
+    const ArgSpan spans[] = {params_span(plan, params), row_span(plan, "tokens", tokens, 8), act_span(plan, "out", out, false),
+                          step_span(dropout)};
+    if ((s = check_spans(fn, spans, 4)) != PSGD_OK) return s;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if ((s = check_capture(fn, plan, st)) != PSGD_OK) return s;
+    const dim3 grid(unsigned(plan->rows * plan->n_workers), unsigned(ceil_div(plan->dim, 512)));
+    const int32_t dim = int32_t(plan->dim);
+    return plan->act == PSGD_F32
+               ? launch(plan, kEmbed, lm_embed<float>, grid, 64, st, static_cast<const float*>(params) + plan->offset,
+                        plan->vocab, dim, tokens, static_cast<float*>(out), d)
+               : launch(plan, kEmbed, lm_embed<uint16_t>, grid, 64, st, static_cast<const uint16_t*>(params) + plan->offset,
+                        plan->vocab, dim, tokens, static_cast<uint16_t*>(out), d);
+  } catch (...) {
+    return no_memory();
+  }
+}
+
+extern "C" psgd_status psgd_lm_embed_grad(psgd_lm_plan* plan, const int64_t* tokens, const void* dout,
+                                          const psgd_dropout_config* dropout, void* grads, uint32_t flags, void* workspace,
+                                          void* stream) {
+  static const char* const fn = "psgd_lm_embed_grad";
+  try {
+    if (plan == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_lm_embed_grad: plan is NULL");
+    if (flags & ~PSGD_LM_ACCUMULATE) return fail(PSGD_ERR_UNSUPPORTED, "psgd_lm_embed_grad: unknown flag bits");
+    Drop d;
+    psgd_status s = make_drop(fn, dropout, &d);
+    if (s != PSGD_OK) return s;
+    const ArgSpan spans[] = {row_span(plan, "tokens", tokens, 8), act_span(plan, "dout", dout, false),
+                          grads_span(plan, grads, false), {"workspace", workspace, plan->workspace_bytes, 16, false},
+                          step_span(dropout)};
+    if ((s = check_spans(fn, spans, 5)) != PSGD_OK) return s;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if ((s = check_capture(fn, plan, st)) != PSGD_OK) return s;
+    const bool add = flags & PSGD_LM_ACCUMULATE;
+    auto with = [&](auto* dy) {
+      return plan->grad == PSGD_F32
+                 ? enqueue_embed_grad(plan, tokens, dy, d, static_cast<float*>(grads) + plan->offset, add, workspace, st)
+                 : enqueue_embed_grad(plan, tokens, dy, d, static_cast<uint16_t*>(grads) + plan->offset, add, workspace, st);
+    };
+    return plan->act == PSGD_F32 ? with(static_cast<const float*>(dout)) : with(static_cast<const uint16_t*>(dout));
+  } catch (...) {
+    return no_memory();
+  }
+}
+
+extern "C" psgd_status psgd_lm_loss(psgd_lm_plan* plan, const void* x, const void* params, const int64_t* targets,
+                                    const psgd_dropout_config* dropout, float* losses, float* lse, float* mean,
+                                    void* workspace, void* stream) {
+  static const char* const fn = "psgd_lm_loss";
+  try {
+    if (plan == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_lm_loss: plan is NULL");
+    Drop d;
+    psgd_status s = make_drop(fn, dropout, &d);
+    if (s != PSGD_OK) return s;
+    const ArgSpan spans[] = {act_span(plan, "x", x, false), params_span(plan, params), row_span(plan, "targets", targets, 8),
+                          row_span(plan, "losses", losses, 4), row_span(plan, "lse", lse, 4),
+                          {"mean", mean, uint64_t(plan->n_workers) * 4, 4, false},
+                          {"workspace", workspace, plan->workspace_bytes, 16, false}, step_span(dropout)};
+    if ((s = check_spans(fn, spans, 8)) != PSGD_OK) return s;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if ((s = check_capture(fn, plan, st)) != PSGD_OK) return s;
+    return enqueue_loss(plan, x, params, targets, d, losses, lse, mean, workspace, st);
+  } catch (...) {
+    return no_memory();
+  }
+}
+
+extern "C" psgd_status psgd_lm_loss_grad(psgd_lm_plan* plan, const void* x, const void* params, const int64_t* targets,
+                                         const float* lse, const float* scale, const psgd_dropout_config* dropout, void* dx,
+                                         void* grads, uint32_t flags, void* workspace, void* stream) {
+  static const char* const fn = "psgd_lm_loss_grad";
+  try {
+    if (plan == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_lm_loss_grad: plan is NULL");
+    if (flags & ~PSGD_LM_ACCUMULATE) return fail(PSGD_ERR_UNSUPPORTED, "psgd_lm_loss_grad: unknown flag bits");
+    if (dx == nullptr && grads == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_lm_loss_grad: dx and grads are both NULL");
+    Drop d;
+    psgd_status s = make_drop(fn, dropout, &d);
+    if (s != PSGD_OK) return s;
+    const ArgSpan spans[] = {act_span(plan, "x", x, false), params_span(plan, params), row_span(plan, "targets", targets, 8),
+                          row_span(plan, "lse", lse, 4), {"scale", scale, uint64_t(plan->n_workers) * 4, 4, true},
+                          act_span(plan, "dx", dx, true), grads_span(plan, grads, true),
+                          {"workspace", workspace, plan->workspace_bytes, 16, false}, step_span(dropout)};
+    if ((s = check_spans(fn, spans, 9)) != PSGD_OK) return s;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if ((s = check_capture(fn, plan, st)) != PSGD_OK) return s;
+    return enqueue_grad(plan, x, params, targets, lse, scale, d, dx, grads, (flags & PSGD_LM_ACCUMULATE) != 0, workspace, st);
+  } catch (...) {
+    return no_memory();
+  }
+}
+
+extern "C" psgd_status psgd_dropout(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, void* out,
+                                    int64_t out_stride, int64_t rows, int64_t cols, psgd_dtype dtype,
+                                    const psgd_dropout_config* config, void* stream) {
+  static const char* const fn = "psgd_dropout";
+  try {
+    if (config == nullptr) return fail(PSGD_ERR_INVALID_ARG, "psgd_dropout: config is NULL");
+    if (dtype != PSGD_F32 && dtype != PSGD_BF16) return fail(PSGD_ERR_UNSUPPORTED, "psgd_dropout: unknown dtype");
+    if (rows < 0 || cols < 0 || (cols > 0 && rows > (int64_t(1) << 62) / cols))
+      return fail(PSGD_ERR_INVALID_ARG, "psgd_dropout: rows and cols must be >= 0, rows * cols at most 2^62");
+    Drop d;
+    psgd_status s = make_drop(fn, config, &d);
+    if (s != PSGD_OK) return s;
+    if (rows == 0 || cols == 0) return PSGD_OK;
+    if (rows == 1) x_stride = residual_stride = out_stride = cols;
+    if (residual == nullptr) residual_stride = cols;
+    const int64_t far = std::max({x_stride, residual_stride, out_stride});
+    if (std::min({x_stride, residual_stride, out_stride}) < cols || far > (int64_t(1) << 60) / rows)
+      return fail(PSGD_ERR_INVALID_ARG, "psgd_dropout: a stride is less than cols, or its rows span over 2^60 elements");
+    if (rows * cols > int64_t(0x7fffffff) * kThreads * 4)
+      return fail(PSGD_ERR_INVALID_ARG, "psgd_dropout: rows * cols is too large for one launch");
+    const unsigned e = unsigned(size_of(dtype));
+    auto span = [&](const char* name, const void* p, int64_t stride, bool nullable) {
+      return ArgSpan{name, p, (uint64_t(rows - 1) * uint64_t(stride) + uint64_t(cols)) * e, e, nullable};
+    };
+    const ArgSpan spans[] = {span("x", x, x_stride, false), span("residual", residual, residual_stride, true),
+                          span("out", out, out_stride, false), step_span(config)};
+    // in place: out over x, or over residual; x and residual may be one buffer (they are read)
+    const bool over_x = out == x && out_stride == x_stride, over_r = out == residual && out_stride == residual_stride;
+    for (int skip = 0; skip < 2; ++skip) {
+      const ArgSpan three[] = {spans[skip], spans[2], spans[3]};
+      const bool same = skip == 0 ? over_x : over_r;
+      if ((s = check_spans(fn, three, 3, same ? 0 : -1, same ? 1 : -1)) != PSGD_OK) return s;
+    }
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const int64_t n = rows * cols;
+    const dim3 grid(unsigned(ceil_div(n, kThreads * 4)));
+    if (dtype == PSGD_F32)
+      hipLaunchKernelGGL(lm_dropout<float>, grid, dim3(kThreads), 0, st, static_cast<const float*>(x), x_stride,
+                         static_cast<const float*>(residual), residual_stride, static_cast<float*>(out), out_stride, n, cols, d);
+    else
+      hipLaunchKernelGGL(lm_dropout<uint16_t>, grid, dim3(kThreads), 0, st, static_cast<const uint16_t*>(x), x_stride,
+                         static_cast<const uint16_t*>(residual), residual_stride, static_cast<uint16_t*>(out), out_stride, n, cols,
+                         d);
+    const hipError_t err = hipGetLastError();
+    return err == hipSuccess ? PSGD_OK : hip_fail("launch lm_dropout", err);
+  } catch (...) {
+    return no_memory();
+  }
+}

@@ -37,6 +37,32 @@ psgd_status refuse(psgd_status s, const char* msg) noexcept try {
   return no_memory();
 }
 
+psgd_status check_spans(const char* fn, const ArgSpan* spans, int n, int same_a, int same_b) {
+  auto bad = [](const std::string& msg) {
+    set_error(msg);
+    return PSGD_ERR_INVALID_ARG;
+  };
+  for (int i = 0; i < n; ++i) {
+    const ArgSpan& a = spans[i];
+    if (a.ptr == nullptr) {
+      if (a.nullable) continue;
+      return bad(std::string(fn) + ": " + a.name + " is NULL");
+    }
+    if (uintptr_t(a.ptr) % a.align != 0)
+      return bad(std::string(fn) + ": " + a.name + " is not " + std::to_string(a.align) + "-byte aligned");
+  }
+  for (int i = 0; i < n; ++i)
+    for (int j = i + 1; j < n; ++j) {
+      const ArgSpan &a = spans[i], &b = spans[j];
+      if (a.ptr == nullptr || b.ptr == nullptr) continue;
+      if (i == same_a && j == same_b && a.ptr == b.ptr) continue;
+      const uintptr_t al = uintptr_t(a.ptr), bl = uintptr_t(b.ptr);
+      if (al < bl + b.bytes && bl < al + a.bytes)
+        return bad(std::string(fn) + ": " + a.name + " and " + b.name + " overlap");
+    }
+  return PSGD_OK;
+}
+
 psgd_status collect_timings(const char* fn, std::vector<PendingTiming>& pending, std::vector<hipEvent_t>& pool,
                             KernelStat* stats) {
   pool.reserve(pool.size() + 2 * pending.size());

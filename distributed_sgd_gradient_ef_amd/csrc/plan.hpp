@@ -121,6 +121,18 @@ psgd_status no_memory() noexcept;
 // An error set outside a try block: no exception leaves it.
 psgd_status refuse(psgd_status s, const char* msg) noexcept;
 
+struct ArgSpan {
+  const char* name;
+  const void* ptr;
+  uint64_t bytes;
+  unsigned align;
+  bool nullable;
+};
+
+// Every pointer given, aligned, and no two ranges overlapping; same_a and same_b name the one
+// pair (by index) that may be the same buffer.
+psgd_status check_spans(const char* fn, const ArgSpan* spans, int n, int same_a = -1, int same_b = -1);
+
 enum KernelId {
   kKFirst = 0, kKMgs, kKQPartial, kKQReduce, kKApply, kKUpdate, kKPMbar, kKQwPartial, kKQwReduce,
   kKTallRows, kKTallApply, kNumKernels

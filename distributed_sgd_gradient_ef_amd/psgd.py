@@ -1,5 +1,5 @@
 """Thin ctypes binding of libpsgd (C ABI declared in include/psgd.h,
-include/psgd_rtopk.h, include/psgd_atomo.h and include/psgd_clip.h).
+include/psgd_rtopk.h, include/psgd_atomo.h, include/psgd_clip.h and include/psgd_lm.h).
 
 Functions carry the C names.  The step functions take torch tensors on a ROCm device
 and pass their device pointers and the current HIP stream; every step of the
@@ -38,6 +38,7 @@ PSGD_NORM_L2 = 0
 PSGD_NORM_MAX = 1
 PSGD_ADAMW_DECAY_MATRICES_ONLY = 0x1
 PSGD_ADAMW_SKIP_NONFINITE = 0x2
+PSGD_LM_ACCUMULATE = 0x1
 
 EXPORTED = [
     "psgd_plan_create", "psgd_plan_sizes", "psgd_plan_layer_info", "psgd_plan_destroy",
@@ -53,6 +54,9 @@ EXPORTED = [
     "psgd_clip_plan_create", "psgd_clip_plan_sizes", "psgd_clip_plan_layer_info", "psgd_clip_plan_destroy",
     "psgd_grad_norm", "psgd_grad_clip", "psgd_adamw_apply",
     "psgd_clip_plan_set_timing", "psgd_clip_plan_kernel_stats",
+    "psgd_lm_plan_create", "psgd_lm_plan_sizes", "psgd_lm_plan_destroy",
+    "psgd_lm_embed", "psgd_lm_embed_grad", "psgd_lm_loss", "psgd_lm_loss_grad", "psgd_dropout",
+    "psgd_lm_plan_set_timing", "psgd_lm_plan_kernel_stats",
 ]
 PSGD_ATOMO_MAX_K = 1024
 _STRING_FUNCS = ("psgd_status_string", "psgd_last_error")
@@ -144,6 +148,25 @@ class AdamwConfig(ctypes.Structure):
         super().__init__(lr, beta1, beta2, eps, weight_decay, max_norm, norm_kind, flags)
 
 
+class _LmSizes(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int32), ("n_workers", ctypes.c_int32), ("table", ctypes.c_int32),
+                ("act_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("worker_stride", ctypes.c_int64), ("table_offset", ctypes.c_int64),
+                ("workspace_bytes", ctypes.c_uint64)]
+
+
+class DropoutConfig(ctypes.Structure):
+    """psgd_dropout_config (see include/psgd_lm.h); `step` is an int64 device tensor of one
+    element, which the configuration keeps alive, or None."""
+
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("step", ctypes.c_void_p)]
+
+    def __init__(self, p: float, seed: int = 0, step=None):
+        super().__init__(p, seed, None if step is None else _buffer("step", step, _int64(), 1, _call_device(step)))
+        self.step_tensor = step
+
+
 _lib = None
 
 
@@ -204,6 +227,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.psgd_adamw_apply.argtypes = [vp, ctypes.POINTER(AdamwConfig), vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.psgd_clip_plan_set_timing.argtypes = [vp, i32]
     lib.psgd_clip_plan_kernel_stats.argtypes = [vp, ctypes.POINTER(_KernelStat), i32, ctypes.POINTER(i32), i32]
+    drop = ctypes.POINTER(DropoutConfig)
+    lib.psgd_lm_plan_create.argtypes = [ctypes.POINTER(_Layer), i32, i32, i32, i64, i32, i32, ctypes.c_uint32,
+                                        ctypes.POINTER(vp)]
+    lib.psgd_lm_plan_sizes.argtypes = [vp, ctypes.POINTER(_LmSizes)]
+    lib.psgd_lm_plan_destroy.argtypes = [vp]
+    lib.psgd_lm_embed.argtypes = [vp, vp, vp, drop, vp, vp]
+    lib.psgd_lm_embed_grad.argtypes = [vp, vp, vp, drop, vp, ctypes.c_uint32, vp, vp]
+    lib.psgd_lm_loss.argtypes = [vp, vp, vp, vp, drop, vp, vp, vp, vp, vp]
+    lib.psgd_lm_loss_grad.argtypes = [vp, vp, vp, vp, vp, vp, drop, vp, vp, ctypes.c_uint32, vp, vp]
+    lib.psgd_dropout.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, i32, drop, vp]
+    lib.psgd_lm_plan_set_timing.argtypes = [vp, i32]
+    lib.psgd_lm_plan_kernel_stats.argtypes = [vp, ctypes.POINTER(_KernelStat), i32, ctypes.POINTER(i32), i32]
     for name in EXPORTED:
         if name not in _STRING_FUNCS:
             getattr(lib, name).restype = ctypes.c_int
@@ -726,6 +761,148 @@ def psgd_adamw_apply(plan: ClipPlan, config: AdamwConfig, update, params, exp_av
              _buffer("step", step, torch.int64, 1, dev),
              None if norm is None else _buffer("norm", norm, f32, 1, dev),
              _buffer("workspace", workspace, torch.uint8, s["workspace_bytes"], dev))
+
+
+# ------------------------------------------------------------------------ a language model's two ends, dropout
+class LmPlan:
+    """Owns a psgd_lm_plan*; freed by psgd_lm_plan_destroy (or when collected)."""
+
+    def __init__(self, handle: int, shapes: Sequence[Tuple[int, int]]):
+        self.handle = handle
+        self.shapes = [tuple(int(v) for v in s) for s in shapes]
+        self.sizes = psgd_lm_plan_sizes(self)
+
+    def __del__(self):
+        if getattr(self, "handle", None):
+            try:
+                psgd_lm_plan_destroy(self)
+            except Exception:
+                pass
+
+
+def psgd_lm_plan_create(shapes: Sequence[Tuple[int, int]], table: int, n_workers: int, rows: int,
+                        act_dtype: int = PSGD_F32, grad_dtype: int = PSGD_F32, flags: int = 0) -> LmPlan:
+    lib = load_library()
+    n = len(shapes)
+    arr = (_Layer * max(1, n))(*[_Layer(int(r), int(c)) for r, c in shapes])
+    h = ctypes.c_void_p()
+    _check(lib.psgd_lm_plan_create(arr, n, int(table), int(n_workers), int(rows), int(act_dtype), int(grad_dtype),
+                                   int(flags), ctypes.byref(h)))
+    return LmPlan(h.value, shapes)
+
+
+def psgd_lm_plan_sizes(plan: LmPlan) -> dict:
+    s = _LmSizes()
+    _check(load_library().psgd_lm_plan_sizes(plan.handle, ctypes.byref(s)))
+    return {name: getattr(s, name) for name, _ in _LmSizes._fields_}
+
+
+def psgd_lm_plan_destroy(plan: LmPlan) -> None:
+    h, plan.handle = plan.handle, None
+    if h:
+        _check(load_library().psgd_lm_plan_destroy(h))
+
+
+def psgd_lm_plan_set_timing(plan: LmPlan, enable: bool) -> None:
+    _check(load_library().psgd_lm_plan_set_timing(plan.handle, 1 if enable else 0))
+
+
+def psgd_lm_plan_kernel_stats(plan: LmPlan, reset: bool = False) -> dict:
+    """{kernel name: (launches, total_ms)}; waits for every timed launch so far."""
+    arr = (_KernelStat * 16)()
+    n = ctypes.c_int32()
+    _check(load_library().psgd_lm_plan_kernel_stats(plan.handle, arr, 16, ctypes.byref(n), 1 if reset else 0))
+    return {arr[i].name.decode(): (arr[i].launches, arr[i].total_ms) for i in range(n.value)}
+
+
+def _int64():
+    import torch
+
+    return torch.int64
+
+
+def _dtype(code: int):
+    import torch
+
+    return torch.bfloat16 if code == PSGD_BF16 else torch.float32
+
+
+def _dropout(config: Optional[DropoutConfig], device: int):
+    if config is None:
+        return None
+    if config.step_tensor is not None and config.step_tensor.get_device() != device:
+        raise PsgdError(PSGD_ERR_INVALID_ARG, "dropout's step must be on the call's device")
+    return ctypes.byref(config)
+
+
+def psgd_lm_embed(plan: LmPlan, params, tokens, dropout: Optional[DropoutConfig], out, stream=None) -> None:
+    """Enqueue the lookup of every worker's tokens (see include/psgd_lm.h)."""
+    s, dev = plan.sizes, _call_device(params)
+    act, n = _dtype(s["act_dtype"]), s["n_workers"] * s["rows"]
+    _enqueue(load_library().psgd_lm_embed, dev, stream, plan.handle,
+             _buffer("params", params, act, s["worker_stride"], dev), _buffer("tokens", tokens, _int64(), n, dev),
+             _dropout(dropout, dev), _buffer("out", out, act, n * s["dim"], dev))
+
+
+def psgd_lm_embed_grad(plan: LmPlan, tokens, dout, dropout: Optional[DropoutConfig], grads, flags: int, workspace,
+                       stream=None) -> None:
+    """Enqueue the lookup's table gradient into every worker's slice (see include/psgd_lm.h)."""
+    import torch
+
+    s, dev = plan.sizes, _call_device(grads)
+    n, W = s["n_workers"] * s["rows"], s["n_workers"]
+    _enqueue(load_library().psgd_lm_embed_grad, dev, stream, plan.handle, _buffer("tokens", tokens, _int64(), n, dev),
+             _buffer("dout", dout, _dtype(s["act_dtype"]), n * s["dim"], dev), _dropout(dropout, dev),
+             _buffer("grads", grads, _dtype(s["grad_dtype"]), W * s["worker_stride"], dev), int(flags),
+             _buffer("workspace", workspace, torch.uint8, s["workspace_bytes"], dev))
+
+
+def psgd_lm_loss(plan: LmPlan, x, params, targets, dropout: Optional[DropoutConfig], losses, lse, mean, workspace,
+                 stream=None) -> None:
+    """Enqueue the cross entropy of every row and every worker's mean (see include/psgd_lm.h)."""
+    import torch
+
+    s, dev, f32 = plan.sizes, _call_device(x), torch.float32
+    act, n = _dtype(s["act_dtype"]), s["n_workers"] * s["rows"]
+    _enqueue(load_library().psgd_lm_loss, dev, stream, plan.handle, _buffer("x", x, act, n * s["dim"], dev),
+             _buffer("params", params, act, s["worker_stride"], dev), _buffer("targets", targets, _int64(), n, dev),
+             _dropout(dropout, dev), _buffer("losses", losses, f32, n, dev), _buffer("lse", lse, f32, n, dev),
+             _buffer("mean", mean, f32, s["n_workers"], dev),
+             _buffer("workspace", workspace, torch.uint8, s["workspace_bytes"], dev))
+
+
+def psgd_lm_loss_grad(plan: LmPlan, x, params, targets, lse, scale, dropout: Optional[DropoutConfig], dx, grads,
+                      flags: int, workspace, stream=None) -> None:
+    """Enqueue the gradients of every worker's mean cross entropy (see include/psgd_lm.h)."""
+    import torch
+
+    s, dev, f32 = plan.sizes, _call_device(x), torch.float32
+    act, n, W = _dtype(s["act_dtype"]), s["n_workers"] * s["rows"], s["n_workers"]
+    _enqueue(load_library().psgd_lm_loss_grad, dev, stream, plan.handle, _buffer("x", x, act, n * s["dim"], dev),
+             _buffer("params", params, act, s["worker_stride"], dev), _buffer("targets", targets, _int64(), n, dev),
+             _buffer("lse", lse, f32, n, dev), None if scale is None else _buffer("scale", scale, f32, W, dev),
+             _dropout(dropout, dev), None if dx is None else _buffer("dx", dx, act, n * s["dim"], dev),
+             None if grads is None else _buffer("grads", grads, _dtype(s["grad_dtype"]), W * s["worker_stride"], dev),
+             int(flags), _buffer("workspace", workspace, torch.uint8, s["workspace_bytes"], dev))
+
+
+def psgd_dropout(x, residual, out, config: DropoutConfig, stream=None) -> None:
+    """Enqueue out = residual + dropout(x) of matrices whose rows may lie apart (`residual`
+    may be None, `out` may be x or residual; see include/psgd_lm.h)."""
+    import torch
+
+    dev = _call_device(x)
+    for name, t in (("x", x), ("residual", residual), ("out", out)):
+        if t is not None and (t.dim() != 2 or t.shape != x.shape or t.dtype is not x.dtype or t.get_device() != dev
+                              or (t.shape[1] > 1 and t.stride(1) != 1)):
+            raise PsgdError(PSGD_ERR_INVALID_ARG, f"{name} must be a matrix of x's shape and type on its device, "
+                                                  f"with elements of a row next to each other")
+    codes = {torch.float32: PSGD_F32, torch.bfloat16: PSGD_BF16}
+    if x.dtype not in codes:
+        raise PsgdError(PSGD_ERR_UNSUPPORTED, "dropout takes float32 and bfloat16")
+    _enqueue(load_library().psgd_dropout, dev, stream, x.data_ptr(), x.stride(0),
+             None if residual is None else residual.data_ptr(), 0 if residual is None else residual.stride(0),
+             out.data_ptr(), out.stride(0), x.shape[0], x.shape[1], codes[x.dtype], _dropout(config, dev))
 
 
 # ------------------------------------------------------------------------ layout helpers
