@@ -185,22 +185,28 @@ struct Mat {
 
 __device__ __forceinline__ int turn(int r) { return ((r >> 1) & 1) << 2 | ((r >> 2) & 1) << 1 | ((r >> 3) & 1); }
 
-// The part products of one contraction, one after the other.
+// The part products of one contraction, one after the other: product i takes part
+// a >> 4 i & 15 of one operand and b >> 4 i & 15 of the other.
 struct Parts {
-  int32_t n;
-  uint8_t a[6], b[6];
+  uint32_t n, a, b;
 };
 
-// C += A B over K blocks for a tile of WM FM x WN FN pieces of 32 x 32, each wave FM x FN of
+typedef __attribute__((address_space(3))) uint16_t lds_t;
+
+// C += A B over K blocks (at least one) for a tile of WM FM x WN FN pieces of 32 x 32, each wave FM x FN of
 // them.  TA, TB: the operand's contraction runs along its blocks' rows instead of along
 // their columns; it is then read from LDS with the transposing load.  Two LDS stages; the
 // next blocks are on their way in registers while the matrix cores work on a stage.
 template <int WM, int WN, int FM, int FN, bool TA, bool TB>
 struct Gemm {
+  static_assert(TB || !TA, "not needed");
   static constexpr int kT = WM * WN * 64;
   static constexpr int kA = WM * FM / 2, kB = WN * FN / 2;  // blocks of the tile's sides
   static constexpr int kPer = kBlkElems / 8 / kT;           // 16-byte pieces of a block per thread
   static constexpr int kStage = (kA + kB) * kBlkElems;
+  static constexpr int kRowsA = FM * 32, kRowsB = FN * 32;  // of a wave
+  typedef f16v Acc[FM][FN];
+  static constexpr int kFM = FM, kFN = FN, kWN = WN, kWM = WM;
   static_assert(kPer * kT * 8 == kBlkElems, "a block is a whole number of pieces per thread");
 
   template <bool T>
@@ -211,10 +217,11 @@ struct Gemm {
 
   // 32 x 16 operand piece f of step kk: row (column) lane % 32, contraction 8 (lane / 32) on.
   template <bool T>
-  static __device__ __forceinline__ bf8 piece(const uint16_t* s, int f, int kk, int lane) {
+  static __device__ __forceinline__ bf8 piece(const lds_t* s, int f, int kk, int lane) {
     if constexpr (!T) {
       const int r = (f & 1) * 32 + (lane & 31);
-      return *reinterpret_cast<const bf8*>(s + (f >> 1) * kBlkElems + r * kBlk + (((kk * 2 + (lane >> 5)) ^ turn(lane)) << 3));
+      typedef __attribute__((address_space(3))) bf8 lds8;
+      return *(const lds8*)(s + (f >> 1) * kBlkElems + r * kBlk + (((kk * 2 + (lane >> 5)) ^ turn(lane)) << 3));
     } else {
       typedef __attribute__((address_space(3))) s4v lds4;
       s8v v;
@@ -222,7 +229,7 @@ struct Gemm {
       for (int j = 0; j < 2; ++j) {
         const int k = (lane >> 5) * 8 + j * 4 + ((lane & 15) >> 2);
         const int c = (f & 1) * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-        const uint16_t* at = s + (f >> 1) * kBlkElems + (kk * 16 + k) * kBlk + ((c ^ turn(k)) << 3) + (lane & 1) * 4;
+        const lds_t* at = s + (f >> 1) * kBlkElems + (kk * 16 + k) * kBlk + ((c ^ turn(k)) << 3) + (lane & 1) * 4;
         const s4v q = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)at);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[4 * j + e] = q[e];
@@ -231,63 +238,88 @@ struct Gemm {
     }
   }
 
+  // A block from memory into LDS, 16 bytes a lane, past the registers.
+  template <bool T>
+  static __device__ __forceinline__ void fetch(const Mat& m, int part, int side, int k, lds_t* s) {
+    typedef __attribute__((address_space(1))) void from_t;
+    typedef __attribute__((address_space(3))) void to_t;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint16_t* g = block<T>(m, part, side, k) + threadIdx.x * 8;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      __builtin_amdgcn_global_load_lds((from_t*)(g + j * kT * 8), (to_t*)(s + (j * kT + wave * 64) * 8), 16, 0, 0);
+  }
+
   static __device__ __forceinline__ void run(const Mat& a, int a0, const Mat& b, int b0, int k0, int k1, const Parts& parts,
-                                             uint16_t* sm, f16v (&acc)[FM][FN]) {
+                                             lds_t* s0, lds_t* s1, Acc& acc) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wa = (wave / WN) * FM, wb = (wave % WN) * FN;
-    u4v ra[kA][kPer], rb[kB][kPer];
-    auto fetch = [&](int q, int k) {
+    int k = k0;
+    uint32_t pa = parts.a, pb = parts.b;
+    auto stage = [&](lds_t* s) {
 #pragma unroll
-      for (int i = 0; i < kA; ++i)
+      for (int i = 0; i < kA; ++i) fetch<TA>(a, pa & 15, a0 + i, k, s + i * kBlkElems);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          ra[i][j] = *reinterpret_cast<const u4v*>(block<TA>(a, parts.a[q], a0 + i, k) + (j * kT + int(threadIdx.x)) * 8);
-#pragma unroll
-      for (int i = 0; i < kB; ++i)
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          rb[i][j] = *reinterpret_cast<const u4v*>(block<TB>(b, parts.b[q], b0 + i, k) + (j * kT + int(threadIdx.x)) * 8);
+      for (int i = 0; i < kB; ++i) fetch<TB>(b, pb & 15, b0 + i, k, s + (kA + i) * kBlkElems);
+      if (++k == k1) k = k0, pa >>= 4, pb >>= 4;
     };
-    auto stage = [&](uint16_t* s) {
+    auto load_a = [&](const lds_t* cur, int kk, bf8 (&x)[FM]) {
 #pragma unroll
-      for (int i = 0; i < kA; ++i)
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          *reinterpret_cast<u4v*>(s + i * kBlkElems + (j * kT + int(threadIdx.x)) * 8) = ra[i][j];
-#pragma unroll
-      for (int i = 0; i < kB; ++i)
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          *reinterpret_cast<u4v*>(s + (kA + i) * kBlkElems + (j * kT + int(threadIdx.x)) * 8) = rb[i][j];
+      for (int i = 0; i < FM; ++i) x[i] = piece<TA>(cur, wa + i, kk, lane);
     };
-    int q = 0, k = k0;
-    const int steps = parts.n * (k1 - k0);
-    if (steps <= 0) return;
-    fetch(q, k);
-    stage(sm);
-    __syncthreads();
-    for (int s = 0; s < steps; ++s) {
-      const bool more = s + 1 < steps;
-      if (more) {
-        if (++k == k1) k = k0, ++q;
-        fetch(q, k);
+    auto load_b = [&](const lds_t* cur, int kk, bf8 (&y)[FN]) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) y[j] = piece<TB>(cur + kA * kBlkElems, wb + j, kk, lane);
+    };
+    auto multiply = [&](const bf8 (&x)[FM], const bf8 (&y)[FN]) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
+    };
+    auto step = [&](const lds_t* cur, lds_t* next, bool more) {
+      __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's part of `cur` is there
+      __syncthreads();                     // everybody's is, and nobody reads `next` any more
+      // The compiler makes a transposing read wait for every load into LDS that is under way:
+      // the next stage's start after the last of them.
+      if constexpr (TA && TB) {
+        bf8 x[2][FM], y[2][FN];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk) load_a(cur, half * 2 + kk, x[kk]), load_b(cur, half * 2 + kk, y[kk]);
+          __builtin_amdgcn_sched_barrier(0);
+          if (half == 1 && more) stage(next);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk) multiply(x[kk], y[kk]);
+        }
+      } else {
+        bf8 x[FM], y[4][FN];
+        if constexpr (TB) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) load_b(cur, kk, y[kk]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (more) stage(next);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          load_a(cur, kk, x);
+          if constexpr (!TB) load_b(cur, kk, y[kk]);
+          multiply(x, y[kk]);
+        }
       }
-      const uint16_t* cur = sm + (s & 1) * kStage;
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        bf8 x[FM], y[FN];
-#pragma unroll
-        for (int i = 0; i < FM; ++i) x[i] = piece<TA>(cur, wa + i, kk, lane);
-#pragma unroll
-        for (int j = 0; j < FN; ++j) y[j] = piece<TB>(cur + kA * kBlkElems, wb + j, kk, lane);
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-          for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
-      }
-      if (more) stage(sm + ((s + 1) & 1) * kStage);
-      __syncthreads();
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    stage(s0);
+    for (int left = int(parts.n) * (k1 - k0);;) {
+      step(s0, s1, left > 1);
+      if (--left == 0) break;
+      step(s1, s0, left > 1);
+      if (--left == 0) break;
     }
+    __syncthreads();
   }
 };
 
@@ -420,25 +452,25 @@ struct ScoreArgs {
 // over its two lane halves and the two waves that share the row.
 template <int GP>
 __global__ __launch_bounds__(ScoreGemm::kT) void lm_scores(ScoreArgs p) {
-  __shared__ __align__(16) uint16_t sm[2 * ScoreGemm::kStage];
+  typedef ScoreGemm G;
+  __shared__ __align__(16) uint16_t s0[G::kStage], s1[G::kStage];
   int vt, tt;
   if (!tile_at(blockIdx.x, (p.v1 - p.v0 + kTile - 1) / kTile, (p.t1 - p.t0 + kTile - 1) / kTile, vt, tt)) return;
   const int v0 = p.v0 + vt * kTile, t0 = p.t0 + tt * kTile;
-  f16v acc[4][2] = {};
-  ScoreGemm::run(p.w, v0, p.x, t0, 0, p.w.cb, p.parts, sm, acc);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t word0 = int64_t(v0) * kBlk + (wave / 4) * 128;  // of this wave
-  const int n_words = int(min(int64_t(128), p.vocab - word0));  // may be negative
-  const int tblk = t0 + wave % 4;                               // the wave's row block
-  const bool live = tblk < p.t1;
+  G::Acc acc = {};
+  G::run(p.w, v0, p.x, t0, 0, p.w.cb, p.parts, (lds_t*)s0, (lds_t*)s1, acc);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / G::kWN, wn = wave % G::kWN;
+  const int64_t word0 = int64_t(v0) * kBlk + wm * G::kRowsA;  // of this wave
+  const int n_words = int(min(int64_t(G::kRowsA), p.vocab - word0));  // may be negative
   if constexpr (GP == 0) {
-    float2* joined = reinterpret_cast<float2*>(sm);
+    float2* joined = reinterpret_cast<float2*>(s0);  // the main loop ends in a barrier: its LDS is free
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t row = int64_t(tblk) * kBlk + j * 32 + (lane & 31);
+    for (int j = 0; j < G::kFN; ++j) {
+      const int at = wn * G::kRowsB + j * 32 + (lane & 31);  // the row's place in the tile
+      const int64_t row = int64_t(t0) * kBlk + at;
       float m = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           if (i * 32 + acc_row(e, lane) >= n_words) acc[i][j][e] = -INFINITY;
@@ -448,61 +480,62 @@ __global__ __launch_bounds__(ScoreGemm::kT) void lm_scores(ScoreArgs p) {
       const float base = m == -INFINITY ? 0.f : m;
       float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e) s += __expf(acc[i][j][e] - base);
       s += __shfl_xor(s, 32);
-      const int64_t local = live ? p.info[row].target - word0 : -1;
+      const int64_t local = t0 + at / kBlk < p.t1 ? p.info[row].target - word0 : -1;
       const bool here = local >= 0 && local < n_words && (int(local) >> 2 & 1) == lane >> 5;
       if (__any(here)) {
         float hit = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             if (i * 32 + acc_row(e, lane) == int(local)) hit = acc[i][j][e];
         if (here) p.hit[row] = hit;
       }
-      // the main loop ends in a barrier: its LDS is free
-      if (lane < 32) joined[(wave / 4) * 256 + (wave % 4) * 64 + j * 32 + lane] = make_float2(m, s);
+      if (lane < 32) joined[wm * 256 + at] = make_float2(m, s);
     }
     __syncthreads();
     const int r = threadIdx.x;
     if (r < 256 && t0 + r / kBlk < p.t1) {
-      const float2 a = joined[r], b = joined[256 + r];
-      const float m = fmaxf(a.x, b.x), base = m == -INFINITY ? 0.f : m;
-      p.stat[int64_t(vt) * (p.t1 - p.t0) * kBlk + int64_t(tt) * 256 + r] =
-          make_float2(m, a.y * __expf(a.x - base) + b.y * __expf(b.x - base));
+      float2 a = joined[r];
+#pragma unroll
+      for (int k = 1; k < G::kWM; ++k) {
+        const float2 b = joined[k * 256 + r];
+        const float m = fmaxf(a.x, b.x), base = m == -INFINITY ? 0.f : m;
+        a = make_float2(m, a.y * __expf(a.x - base) + b.y * __expf(b.x - base));
+      }
+      p.stat[int64_t(vt) * (p.t1 - p.t0) * kBlk + int64_t(tt) * 256 + r] = a;
     }
   } else {
-    uint16_t* own = sm + wave * 2 * kBlkElems;  // two blocks of g: words [0, 64) and [64, 128) of the wave
-    float coef[2], lse[2];
-    int local[2];
+    constexpr int kWb = G::kRowsA / kBlk, kRb = G::kRowsB / kBlk;  // blocks of g per wave
+    constexpr int kHalf = G::kT / 128;  // waves whose blocks fit a stage
+    uint16_t* own = (wave < kHalf ? s0 : s1) + wave % kHalf * kWb * kRb * kBlkElems;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < G::kFN; ++j) {
+      const int at = wn * G::kRowsB + j * 32 + (lane & 31);
       RowInfo ri{-1, 0.f, 0.f, 0};
-      if (live) ri = p.info[int64_t(tblk) * kBlk + j * 32 + (lane & 31)];
-      coef[j] = ri.target < 0 ? 0.f : ri.coef;
-      lse[j] = ri.lse;
-      local[j] = ri.target < 0 ? -1 : int(max(int64_t(-1), min(int64_t(1 << 20), ri.target - word0)));
-    }
+      if (t0 + at / kBlk < p.t1) ri = p.info[int64_t(t0) * kBlk + at];
+      const float coef = ri.target < 0 ? 0.f : ri.coef;
+      const int local = ri.target < 0 ? -1 : int(max(int64_t(-1), min(int64_t(1 << 20), ri.target - word0)));
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int v = i * 32 + acc_row(e, lane);
-          float x = __expf(acc[i][j][e] - lse[j]);
-          if (v == local[j]) x -= 1.f;
-          acc[i][j][e] = v < n_words && coef[j] != 0.f ? x * coef[j] : 0.f;
+          float x = __expf(acc[i][j][e] - ri.lse);
+          if (v == local) x -= 1.f;
+          acc[i][j][e] = v < n_words && coef != 0.f ? x * coef : 0.f;
         }
+    }
 #pragma unroll
     for (int part = 0; part < GP; ++part) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < G::kFN; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
           for (int e4 = 0; e4 < 4; ++e4) {
             s4v v;
@@ -513,19 +546,23 @@ __global__ __launch_bounds__(ScoreGemm::kT) void lm_scores(ScoreArgs p) {
               v[e] = short(b);
               if (GP > 1) acc[i][j][e4 * 4 + e] = x - widen(b);
             }
-            const int r = j * 32 + (lane & 31), c8 = (i & 1) * 4 + e4;
-            *reinterpret_cast<s4v*>(own + (i >> 1) * kBlkElems + r * kBlk + ((c8 ^ turn(r)) << 3) + (lane >> 5) * 4) = v;
+            const int r = (j & 1) * 32 + (lane & 31), c8 = (i & 1) * 4 + e4;
+            *reinterpret_cast<s4v*>(own + ((j >> 1) * kWb + (i >> 1)) * kBlkElems + r * kBlk + ((c8 ^ turn(r)) << 3) +
+                                    (lane >> 5) * 4) = v;
           }
       __syncthreads();
-      const int vb = v0 - p.v0 + (wave / 4) * 2, n_v = p.v1 - p.v0;
-      if (live) {
+      const int vb = v0 - p.v0 + wm * kWb, n_v = p.v1 - p.v0;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          if (vb + b >= n_v) break;
-          uint16_t* o = p.g + part * p.g_part + (int64_t(tblk - p.t0) * n_v + vb + b) * kBlkElems;
+      for (int rb = 0; rb < kRb; ++rb) {
+        const int tb = t0 + wn * kRb + rb;
+#pragma unroll
+        for (int b = 0; b < kWb; ++b) {
+          if (tb >= p.t1 || vb + b >= n_v) continue;
+          uint16_t* o = p.g + part * p.g_part + (int64_t(tb - p.t0) * n_v + vb + b) * kBlkElems;
+          const uint16_t* from = own + (rb * kWb + b) * kBlkElems;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<u4v*>(o + (k * 64 + lane) * 8) = *reinterpret_cast<const u4v*>(own + b * kBlkElems + (k * 64 + lane) * 8);
+            *reinterpret_cast<u4v*>(o + (k * 64 + lane) * 8) = *reinterpret_cast<const u4v*>(from + (k * 64 + lane) * 8);
         }
       }
       __syncthreads();
@@ -590,21 +627,21 @@ struct DxArgs {
 };
 
 __global__ __launch_bounds__(DxGemm::kT) void lm_dx(DxArgs p) {
-  __shared__ __align__(16) uint16_t sm[2 * DxGemm::kStage];
+  __shared__ __align__(16) uint16_t s0[DxGemm::kStage], s1[DxGemm::kStage];
   const int n_c = (p.w.cb + kTile - 1) / kTile;
   const int split = blockIdx.x % p.splits, c0 = int(blockIdx.x / p.splits) % n_c * kTile;
   const int r0 = int(blockIdx.x / p.splits) / n_c * kTile;
   const int k0 = int(int64_t(p.kb) * split / p.splits), k1 = int(int64_t(p.kb) * (split + 1) / p.splits);
-  f16v acc[4][2] = {};
-  DxGemm::run(p.g, r0, p.w, c0, k0, k1, p.parts, sm, acc);
+  DxGemm::Acc acc = {};
+  DxGemm::run(p.g, r0, p.w, c0, k0, k1, p.parts, (lds_t*)s0, (lds_t*)s1, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float* out = p.out + split * p.rows * p.ld;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < DxGemm::kFM; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t c = int64_t(c0) * kBlk + (wave % 4) * 64 + j * 32 + (lane & 31);
-      const int64_t r = int64_t(r0) * kBlk + (wave / 4) * 128 + i * 32;
+    for (int j = 0; j < DxGemm::kFN; ++j) {
+      const int64_t c = int64_t(c0) * kBlk + (wave % DxGemm::kWN) * DxGemm::kRowsB + j * 32 + (lane & 31);
+      const int64_t r = int64_t(r0) * kBlk + (wave / DxGemm::kWN) * DxGemm::kRowsA + i * 32;
       if (c >= p.ld) continue;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
@@ -656,19 +693,19 @@ struct DwArgs {
 
 template <typename GT>
 __global__ __launch_bounds__(DwGemm::kT) void lm_dw(DwArgs p, GT* grads) {
-  __shared__ __align__(16) uint16_t sm[2 * DwGemm::kStage];
+  __shared__ __align__(16) uint16_t s0[DwGemm::kStage], s1[DwGemm::kStage];
   const int n_c = (p.x.cb + kTile - 1) / kTile;
   const int w = blockIdx.y, c0 = int(blockIdx.x % n_c) * kTile, r0 = int(blockIdx.x / n_c) * kTile;
-  f16v acc[4][2] = {};
-  DwGemm::run(p.g, r0, p.x, c0, w * p.tw, (w + 1) * p.tw, p.parts, sm, acc);
+  DwGemm::Acc acc = {};
+  DwGemm::run(p.g, r0, p.x, c0, w * p.tw, (w + 1) * p.tw, p.parts, (lds_t*)s0, (lds_t*)s1, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   GT* out = grads + w * p.stride;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < DwGemm::kFM; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t c = int64_t(c0) * kBlk + (wave % 4) * 64 + j * 32 + (lane & 31);
-      const int64_t r = int64_t(r0) * kBlk + (wave / 4) * 128 + i * 32;
+    for (int j = 0; j < DwGemm::kFN; ++j) {
+      const int64_t c = int64_t(c0) * kBlk + (wave % DwGemm::kWN) * DwGemm::kRowsB + j * 32 + (lane & 31);
+      const int64_t r = int64_t(r0) * kBlk + (wave / DwGemm::kWN) * DwGemm::kRowsA + i * 32;
       if (c >= p.dim) continue;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
@@ -968,8 +1005,8 @@ Parts make_parts(int a, int b, bool few) {
   for (int s = most; s >= 0; --s)  // the small ones first
     for (int i = 0; i <= s; ++i)
       if (i < a && s - i < b) {
-        p.a[p.n] = uint8_t(i);
-        p.b[p.n] = uint8_t(s - i);
+        p.a |= uint32_t(i) << (4 * p.n);
+        p.b |= uint32_t(s - i) << (4 * p.n);
         ++p.n;
       }
   return p;
@@ -1192,7 +1229,7 @@ extern "C" psgd_status psgd_lm_plan_create(const psgd_layer* layers, int32_t n_l
     const int64_t most = std::max<int64_t>(1, kPieceBytes / int64_t(gp * blk) / tbp / kTile) * kTile;
     plan->piece = int32_t(ceil_div(ceil_div(plan->vb, ceil_div(plan->vb, most)), kTile) * kTile);
     const int64_t dx_tiles = ceil_div(tbp, kTile) * ceil_div(plan->db, kTile);
-    plan->splits = int32_t(std::max<int64_t>(1, std::min<int64_t>({256 / dx_tiles, 16, std::min(plan->piece, plan->vb)})));
+    plan->splits = int32_t(std::max<int64_t>(1, std::min<int64_t>({256 / dx_tiles, 16, plan->vb - (plan->vb - 1) / plan->piece * plan->piece})));
     const int64_t v_tiles = ceil_div(plan->vb, kTile);
     plan->chunk = int32_t(std::max<int64_t>(1, kStatBytes / (v_tiles * kTile * kBlk * 8)) * kTile);
     uint64_t ws = 0;
