@@ -31,6 +31,7 @@
 #include <cmath>
 #include <cstdio>
 #include <string>
+#include <type_traits>
 #include <vector>
 
 #include "plan.hpp"
@@ -199,7 +200,7 @@ typedef __attribute__((address_space(3))) uint16_t lds_t;
 // next blocks are on their way in registers while the matrix cores work on a stage.
 template <int WM, int WN, int FM, int FN, bool TA, bool TB>
 struct Gemm {
-  static_assert(TB || !TA, "not needed");
+  static_assert(FM == 4 && FN == 2 && (TB || !TA), "what columns_of is written out for");
   static constexpr int kT = WM * WN * 64;
   static constexpr int kA = WM * FM / 2, kB = WN * FN / 2;  // blocks of the tile's sides
   static constexpr int kPer = kBlkElems / 8 / kT;           // 16-byte pieces of a block per thread
@@ -215,27 +216,106 @@ struct Gemm {
     return m.p + part * m.part + (int64_t(r) * m.cb + c) * kBlkElems;
   }
 
-  // 32 x 16 operand piece f of step kk: row (column) lane % 32, contraction 8 (lane / 32) on.
-  template <bool T>
-  static __device__ __forceinline__ bf8 piece(const lds_t* s, int f, int kk, int lane) {
-    if constexpr (!T) {
-      const int r = (f & 1) * 32 + (lane & 31);
-      typedef __attribute__((address_space(3))) bf8 lds8;
-      return *(const lds8*)(s + (f >> 1) * kBlkElems + r * kBlk + (((kk * 2 + (lane >> 5)) ^ turn(lane)) << 3));
-    } else {
-      typedef __attribute__((address_space(3))) s4v lds4;
-      s8v v;
+  // Operand pieces of step kk, 32 x 16 each: row (column) lane % 32, contraction 8 (lane / 32)
+  // on.  at: a lane's byte address in every step.
+  static __device__ __forceinline__ void rows_at(int f0, int lane, uint32_t (&at)[4]) {
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+      at[kk] = 2 * ((f0 >> 1) * kBlkElems + (lane & 31) * kBlk + (((kk * 2 + (lane >> 5)) ^ turn(lane)) << 3));
+  }
+
+  static __device__ __forceinline__ void rows_of(uint32_t a, bf8 (&x)[4]) {
+    asm volatile(
+        "ds_read_b128 %0, %4\n"
+        "ds_read_b128 %1, %4 offset:4096\n"
+        "ds_read_b128 %2, %4 offset:8192\n"
+        "ds_read_b128 %3, %4 offset:12288\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+        : "v"(a)
+        : "memory");
+  }
+
+  static __device__ __forceinline__ void rows_of(uint32_t a, uint32_t b, bf8 (&x)[4], bf8 (&y)[2]) {
+    asm volatile(
+        "ds_read_b128 %0, %6\n"
+        "ds_read_b128 %1, %6 offset:4096\n"
+        "ds_read_b128 %2, %6 offset:8192\n"
+        "ds_read_b128 %3, %6 offset:12288\n"
+        "ds_read_b128 %4, %7\n"
+        "ds_read_b128 %5, %7 offset:4096\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(y[0]), "=&v"(y[1])
+        : "v"(a), "v"(b)
+        : "memory");
+  }
+
+  // The same from an operand whose contraction runs along the blocks' rows: a transposing read
+  // takes 4 rows x 16 columns per 16 lanes.  at[p][j]: a lane's byte addresses for even and
+  // odd pieces and for the two halves of its eight contraction slots.
+  static __device__ __forceinline__ void columns_at(int f0, int lane, uint32_t (&at)[2][2]) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int k = (lane >> 5) * 8 + j * 4 + ((lane & 15) >> 2);
-        const int c = (f & 1) * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-        const lds_t* at = s + (f >> 1) * kBlkElems + (kk * 16 + k) * kBlk + ((c ^ turn(k)) << 3) + (lane & 1) * 4;
-        const s4v q = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)at);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * j + e] = q[e];
+        const int c = p * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+        at[p][j] = 2 * ((f0 >> 1) * kBlkElems + k * kBlk + ((c ^ turn(k)) << 3) + (lane & 1) * 4);
       }
-      return __builtin_bit_cast(bf8, v);
-    }
+  }
+
+  static __device__ __forceinline__ bf8 join(const s4v& lo, const s4v& hi) {
+    s8v v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = lo[e], v[4 + e] = hi[e];
+    return __builtin_bit_cast(bf8, v);
+  }
+
+  // The reads are written out because the compiler makes its own transposing reads wait for
+  // every load into LDS that is under way; each block waits for its reads before it ends.
+  template <int OFF>
+  static __device__ __forceinline__ void columns_of(const uint32_t (&b)[2][2], bf8 (&y)[2]) {
+    s4v v[4];
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %4 offset:%8\n"
+        "ds_read_b64_tr_b16 %1, %5 offset:%8\n"
+        "ds_read_b64_tr_b16 %2, %6 offset:%8\n"
+        "ds_read_b64_tr_b16 %3, %7 offset:%8\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+        : "v"(b[0][0]), "v"(b[0][1]), "v"(b[1][0]), "v"(b[1][1]), "n"(OFF)
+        : "memory");
+    y[0] = join(v[0], v[1]);
+    y[1] = join(v[2], v[3]);
+  }
+
+  template <int OFF>
+  static __device__ __forceinline__ void columns_of(const uint32_t (&a)[2][2], const uint32_t (&b)[2][2], bf8 (&x)[4],
+                                                    bf8 (&y)[2]) {
+    s4v v[12];
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %12 offset:%20\n"
+        "ds_read_b64_tr_b16 %1, %13 offset:%20\n"
+        "ds_read_b64_tr_b16 %2, %14 offset:%20\n"
+        "ds_read_b64_tr_b16 %3, %15 offset:%20\n"
+        "ds_read_b64_tr_b16 %4, %12 offset:%21\n"
+        "ds_read_b64_tr_b16 %5, %13 offset:%21\n"
+        "ds_read_b64_tr_b16 %6, %14 offset:%21\n"
+        "ds_read_b64_tr_b16 %7, %15 offset:%21\n"
+        "ds_read_b64_tr_b16 %8, %16 offset:%20\n"
+        "ds_read_b64_tr_b16 %9, %17 offset:%20\n"
+        "ds_read_b64_tr_b16 %10, %18 offset:%20\n"
+        "ds_read_b64_tr_b16 %11, %19 offset:%20\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7]),
+          "=&v"(v[8]), "=&v"(v[9]), "=&v"(v[10]), "=&v"(v[11])
+        : "v"(a[0][0]), "v"(a[0][1]), "v"(a[1][0]), "v"(a[1][1]), "v"(b[0][0]), "v"(b[0][1]), "v"(b[1][0]), "v"(b[1][1]),
+          "n"(OFF), "n"(OFF + 2 * kBlkElems)
+        : "memory");
+#pragma unroll
+    for (int f = 0; f < 4; ++f) x[f] = join(v[2 * f], v[2 * f + 1]);
+#pragma unroll
+    for (int f = 0; f < 2; ++f) y[f] = join(v[8 + 2 * f], v[9 + 2 * f]);
   }
 
   // A block from memory into LDS, 16 bytes a lane, past the registers.
@@ -263,15 +343,23 @@ struct Gemm {
       for (int i = 0; i < kB; ++i) fetch<TB>(b, pb & 15, b0 + i, k, s + (kA + i) * kBlkElems);
       if (++k == k1) k = k0, pa >>= 4, pb >>= 4;
     };
-    auto load_a = [&](const lds_t* cur, int kk, bf8 (&x)[FM]) {
-#pragma unroll
-      for (int i = 0; i < FM; ++i) x[i] = piece<TA>(cur, wa + i, kk, lane);
-    };
-    auto load_b = [&](const lds_t* cur, int kk, bf8 (&y)[FN]) {
-#pragma unroll
-      for (int j = 0; j < FN; ++j) y[j] = piece<TB>(cur + kA * kBlkElems, wb + j, kk, lane);
-    };
-    auto multiply = [&](const bf8 (&x)[FM], const bf8 (&y)[FN]) {
+    uint32_t at_a[2][2], at_b[2][2];
+    columns_at(wa, lane, at_a);
+    columns_at(wb, lane, at_b);
+    uint32_t at_ra[4], at_rb[4];
+    rows_at(wa, lane, at_ra);
+    rows_at(wb, lane, at_rb);
+    auto multiply = [&](uint32_t base, const uint32_t (&ca)[2][2], const uint32_t (&cb)[2][2], auto kk) {
+      constexpr int K = decltype(kk)::value;
+      bf8 x[FM], y[FN];
+      if constexpr (TA) {
+        columns_of<K * 32 * kBlk>(ca, cb, x, y);
+      } else if constexpr (TB) {
+        rows_of(base + at_ra[K], x);
+        columns_of<K * 32 * kBlk>(cb, y);
+      } else {
+        rows_of(base + at_ra[K], base + 2 * kA * kBlkElems + at_rb[K], x, y);
+      }
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -280,36 +368,18 @@ struct Gemm {
     auto step = [&](const lds_t* cur, lds_t* next, bool more) {
       __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's part of `cur` is there
       __syncthreads();                     // everybody's is, and nobody reads `next` any more
-      // The compiler makes a transposing read wait for every load into LDS that is under way:
-      // the next stage's start after the last of them.
-      if constexpr (TA && TB) {
-        bf8 x[2][FM], y[2][FN];
+      if (more) stage(next);
+      __builtin_amdgcn_sched_barrier(0);
+      const uint32_t base = uint32_t(uintptr_t(cur));
+      uint32_t ca[2][2], cb[2][2];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+      for (int p = 0; p < 2; ++p)
 #pragma unroll
-          for (int kk = 0; kk < 2; ++kk) load_a(cur, half * 2 + kk, x[kk]), load_b(cur, half * 2 + kk, y[kk]);
-          __builtin_amdgcn_sched_barrier(0);
-          if (half == 1 && more) stage(next);
-          __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk) multiply(x[kk], y[kk]);
-        }
-      } else {
-        bf8 x[FM], y[4][FN];
-        if constexpr (TB) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) load_b(cur, kk, y[kk]);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        if (more) stage(next);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          load_a(cur, kk, x);
-          if constexpr (!TB) load_b(cur, kk, y[kk]);
-          multiply(x, y[kk]);
-        }
-      }
+        for (int j = 0; j < 2; ++j) ca[p][j] = base + at_a[p][j], cb[p][j] = base + 2 * kA * kBlkElems + at_b[p][j];
+      multiply(base, ca, cb, std::integral_constant<int, 0>());
+      multiply(base, ca, cb, std::integral_constant<int, 1>());
+      multiply(base, ca, cb, std::integral_constant<int, 2>());
+      multiply(base, ca, cb, std::integral_constant<int, 3>());
       __builtin_amdgcn_sched_barrier(0);
     };
     stage(s0);
