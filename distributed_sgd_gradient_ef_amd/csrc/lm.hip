@@ -4,10 +4,12 @@
 // Products run on bf16 matrix cores from packed operands: 64 x 64 blocks of bf16, 8 KB each
 // and one after the other, so that a tile is a few contiguous runs of 16-byte loads, zero
 // past a matrix's edges, so that no product loop has an edge of its own.  A float32 operand
-// is held as three such bf16 parts, x = h + m + l, and a product of two of them is the sum
-// of the six part products above 2^-24: the loop over the contraction simply gets longer.
+// is scaled by a power of two and held as two fp16 parts, x = h + l / 2048, which carry 22
+// bits; a product of two of them is h l' + l h' (divided by 2048) + h h': the loop over the
+// contraction simply runs three times.
 //
-//   lm_count   counted rows of every worker
+//   lm_prep    the largest entries of float32 operands, the counted rows of every worker
+//   lm_scale   these operands' powers of two
 //   lm_pack    x (through dropout, zero where a row does not count) and the table, packed
 //   lm_scores  a 256 x 256 tile of T drop(x)^T: its columns' running maximum and sum
 //              (loss), or g of its entries, packed (gradient)
@@ -53,9 +55,9 @@ constexpr int kSortThreads = 512;
 constexpr int kRun = 32;           // sorted pairs summed by one wave
 
 enum KernelId {
-  kCount = 0, kPack, kScores, kRows, kMean, kDx, kDxOut, kDw, kEmbed, kSort, kMerge, kZero, kSum, kJoin, kDrop, kNumK
+  kPrep = 0, kScale, kPack, kScores, kRows, kMean, kDx, kDxOut, kDw, kEmbed, kSort, kMerge, kZero, kSum, kJoin, kDrop, kNumK
 };
-const char* const kNames[kNumK] = {"lm_count", "lm_pack", "lm_scores", "lm_rows", "lm_mean", "lm_dx", "lm_dx_out", "lm_dw",
+const char* const kNames[kNumK] = {"lm_prep", "lm_scale", "lm_pack", "lm_scores", "lm_rows", "lm_mean", "lm_dx", "lm_dx_out", "lm_dw",
                                    "lm_embed", "lm_sort", "lm_merge", "lm_zero", "lm_sum", "lm_join", "lm_dropout"};
 
 }  // namespace lm
@@ -69,7 +71,7 @@ struct psgd_lm_plan {
   int32_t tb = 0, tw = 0;        // blocks of all rows together, and of one worker's rows
   int32_t piece = 0, splits = 1;  // blocks of the vocabulary per piece, splits of its sum in lm_dx
   int32_t chunk = 0;             // row blocks per chunk in psgd_lm_loss
-  uint64_t ws_x = 0, ws_w = 0, ws_info = 0, ws_count = 0, ws_stat = 0, ws_hit = 0, ws_g = 0, ws_dx = 0;
+  uint64_t ws_x = 0, ws_cx = 0, ws_w = 0, ws_peak = 0, ws_exps = 0, ws_info = 0, ws_count = 0, ws_stat = 0, ws_hit = 0, ws_g = 0, ws_dx = 0;
   uint64_t ws_key = 0, ws_key2 = 0, ws_part = 0, workspace_bytes = 0;
   bool timing = false;
   std::vector<psgd::PendingTiming> pending;
@@ -82,6 +84,7 @@ namespace lm {
 namespace {
 
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef short s4v __attribute__((ext_vector_type(4)));
 typedef short s8v __attribute__((ext_vector_type(8)));
 typedef float f16v __attribute__((ext_vector_type(16)));
@@ -114,17 +117,12 @@ __device__ __forceinline__ void store(uint16_t* p, const float (&x)[N]) {
   __builtin_memcpy(p, v, sizeof(v));
 }
 
-// x = sum of P bf16 parts, each the nearest to what is left.  A number past the largest
-// bf16 takes that as its first part; infinities and NaN have one part.
-template <int P>
-__device__ __forceinline__ void split(float x, uint16_t (&h)[P]) {
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    uint16_t b = narrow_bits(x);
-    if (P > 1 && (b & 0x7fff) == 0x7f80 && (__float_as_uint(x) & 0x7fffffffu) < 0x7f800000u) b -= 1;
-    h[p] = b;
-    x = (b & 0x7f80) == 0x7f80 ? 0.f : x - widen(b);
-  }
+// The two fp16 parts of x, |x| < 2^15 or not finite: x = h + l / 2048.
+__device__ __forceinline__ void split16(float x, uint16_t& h, uint16_t& l) {
+  const _Float16 a = _Float16(x);
+  const float rest = fabsf(x) < 65536.f ? (x - float(a)) * 2048.f : 0.f;
+  h = __builtin_bit_cast(uint16_t, a);
+  l = __builtin_bit_cast(uint16_t, _Float16(rest));
 }
 
 struct Drop {
@@ -194,11 +192,11 @@ struct Parts {
 
 typedef __attribute__((address_space(3))) uint16_t lds_t;
 
-// C += A B over K blocks (at least one) for a tile of WM FM x WN FN pieces of 32 x 32, each wave FM x FN of
+// C += A B over blocks [k0, k1) (at least one; of the last, `tail` steps of 16) for a tile of WM FM x WN FN pieces of 32 x 32, each wave FM x FN of
 // them.  TA, TB: the operand's contraction runs along its blocks' rows instead of along
 // their columns; it is then read from LDS with the transposing load.  Two LDS stages; the
 // next blocks are on their way in registers while the matrix cores work on a stage.
-template <int WM, int WN, int FM, int FN, bool TA, bool TB>
+template <int WM, int WN, int FM, int FN, bool TA, bool TB, bool F16>
 struct Gemm {
   static_assert(FM == 4 && FN == 2 && (TB || !TA), "what columns_of is written out for");
   static constexpr int kT = WM * WN * 64;
@@ -330,8 +328,8 @@ struct Gemm {
       __builtin_amdgcn_global_load_lds((from_t*)(g + j * kT * 8), (to_t*)(s + (j * kT + wave * 64) * 8), 16, 0, 0);
   }
 
-  static __device__ __forceinline__ void run(const Mat& a, int a0, const Mat& b, int b0, int k0, int k1, const Parts& parts,
-                                             lds_t* s0, lds_t* s1, Acc& acc) {
+  static __device__ __forceinline__ void sweep(const Mat& a, int a0, const Mat& b, int b0, int k0, int k1, int tail, const Parts& parts,
+                                                 lds_t* s0, lds_t* s1, Acc& acc) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wa = (wave / WN) * FM, wb = (wave % WN) * FN;
     int k = k0;
@@ -363,8 +361,14 @@ struct Gemm {
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < FN; ++j) {
+          if constexpr (F16)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, x[i]), __builtin_bit_cast(h8, y[j]), acc[i][j], 0, 0, 0);
+          else
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
+        }
     };
+    int at = k0;  // the block that `cur` holds
     auto step = [&](const lds_t* cur, lds_t* next, bool more) {
       __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's part of `cur` is there
       __syncthreads();                     // everybody's is, and nobody reads `next` any more
@@ -376,10 +380,12 @@ struct Gemm {
       for (int p = 0; p < 2; ++p)
 #pragma unroll
         for (int j = 0; j < 2; ++j) ca[p][j] = base + at_a[p][j], cb[p][j] = base + 2 * kA * kBlkElems + at_b[p][j];
+      const int n = ++at == k1 ? tail : 4;
+      if (at == k1) at = k0;
       multiply(base, ca, cb, std::integral_constant<int, 0>());
-      multiply(base, ca, cb, std::integral_constant<int, 1>());
-      multiply(base, ca, cb, std::integral_constant<int, 2>());
-      multiply(base, ca, cb, std::integral_constant<int, 3>());
+      if (n > 1) multiply(base, ca, cb, std::integral_constant<int, 1>());
+      if (n > 2) multiply(base, ca, cb, std::integral_constant<int, 2>());
+      if (n > 3) multiply(base, ca, cb, std::integral_constant<int, 3>());
       __builtin_amdgcn_sched_barrier(0);
     };
     stage(s0);
@@ -391,19 +397,50 @@ struct Gemm {
     }
     __syncthreads();
   }
+
+  // The whole product.  With fp16 parts the products with a low part come first and are
+  // scaled back before the product of the high parts is added.
+  static __device__ __forceinline__ void run(const Mat& a, int a0, const Mat& b, int b0, int k0, int k1, int tail,
+                                             const Parts& parts, lds_t* s0, lds_t* s1, Acc& acc) {
+    if constexpr (!F16) {
+      sweep(a, a0, b, b0, k0, k1, tail, parts, s0, s1, acc);
+    } else {
+      if (parts.n > 1) {
+        sweep(a, a0, b, b0, k0, k1, tail, Parts{parts.n - 1, parts.a, parts.b}, s0, s1, acc);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] *= 1.f / 2048.f;
+      }
+      sweep(a, a0, b, b0, k0, k1, tail, Parts{1, 0, 0}, s0, s1, acc);
+    }
+  }
 };
 
 // Accumulator i of a 32 x 32 piece: its row for this lane; its column is lane % 32.
 __device__ __forceinline__ int acc_row(int i, int lane) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
 
 // ------------------------------------------------------------------ rows and packing
-// What lm_scores needs of a packed row.
+// What the products with g need of a packed row.  exp(s - lse) is taken as
+// exp2(s log2(e) - (hi + lo)), with the float32 next to log2(e) in both places.
 struct RowInfo {
   int32_t target;  // -1: the row does not count
   float coef;      // scale / counted
-  float lse;
-  int32_t pad;
+  float hi, lo;    // lse * kLog2e
 };
+
+constexpr float kLog2e = 1.44269504f;
+constexpr int kGExp = 14;  // g is held in fp16 as g 2^14: it is below 1 but for rounding
+
+// float32 operands: their powers of two.  An operand is scaled so that its largest finite
+// entry lies in [2^14, 2^15): its fp16 parts hold 22 bits of entries down to 2^-28 of it.
+struct Scales {
+  int32_t x, w, cx;  // of drop(x), the table, coef * drop(x)
+};
+
+constexpr int kPeakW = 256, kPeakX = 64;  // workgroups that look for the largest entry
 
 template <typename F>
 __device__ __forceinline__ F block_sum(F x, F* sm) {
@@ -416,13 +453,87 @@ __device__ __forceinline__ F block_sum(F x, F* sm) {
   return t;
 }
 
-__global__ __launch_bounds__(kThreads) void lm_count(const int64_t* targets, int64_t rows, int64_t vocab, int32_t* count) {
+__device__ __forceinline__ bool counts(int64_t target, int64_t vocab) { return uint64_t(target) < uint64_t(vocab); }
+
+// Largest finite magnitude of every part of the table and of x, and the counted rows of every
+// worker: what the first kPeakW + kPeakX workgroups and the ones after them do (`peaks` 0:
+// there are only the latter).
+__global__ __launch_bounds__(kThreads) void lm_prep(int32_t peaks, const float* table, int64_t n_table, const float* x,
+                                                    int64_t n_x, float* peak, const int64_t* targets, int64_t rows,
+                                                    int64_t vocab, int32_t* count) {
   __shared__ int32_t sm[kThreads / 64];
-  const int64_t* t = targets + blockIdx.x * rows;
+  const int job = blockIdx.x;
+  if (job < peaks) {
+    const bool t = job < kPeakW;
+    const float* p = t ? table : x;
+    const int64_t n = t ? n_table : n_x, part = t ? job : job - kPeakW, of = t ? kPeakW : kPeakX;
+    const int64_t per = (n + of * 4 - 1) / (of * 4) * 4, end = min(n, (part + 1) * per);
+    uint32_t m = 0;
+    for (int64_t i = part * per + threadIdx.x * 4; i < end; i += kThreads * 4) {
+      float v[4] = {};
+      if (i + 4 <= end) {
+        load<4>(p + i, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (i + e < end) v[e] = p[i + e];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t u = __float_as_uint(v[e]) & 0x7fffffffu;
+        if (u < 0x7f800000u) m = max(m, u);
+      }
+    }
+    for (int o = 32; o > 0; o >>= 1) m = max(m, uint32_t(__shfl_xor(int(m), o)));
+    if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = int32_t(m);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < kThreads / 64; ++i) m = max(m, uint32_t(sm[i]));
+      peak[job] = __uint_as_float(m);
+    }
+    return;
+  }
+  const int w = job - peaks;
   int32_t n = 0;
-  for (int64_t i = threadIdx.x; i < rows; i += kThreads) n += uint64_t(t[i]) < uint64_t(vocab) ? 1 : 0;
+  for (int64_t i = threadIdx.x; i < rows; i += kThreads) n += counts(targets[w * rows + i], vocab) ? 1 : 0;
   n = block_sum(n, sm);
-  if (threadIdx.x == 0) count[blockIdx.x] = n;
+  if (threadIdx.x == 0) count[w] = n;
+}
+
+__device__ __forceinline__ float coef_of(const float* scale, const int32_t* count, int64_t w) {
+  return float((scale != nullptr ? double(scale[w]) : 1.0) / double(max(1, count[w])));
+}
+
+__device__ __forceinline__ int32_t exponent_for(double largest) {
+  return largest > 0.0 && largest < 1e300 ? max(-200, min(200, 14 - ilogb(largest))) : 0;
+}
+
+// The operands' powers of two.
+__global__ __launch_bounds__(kThreads) void lm_scale(const float* peak, const float* scale, const int32_t* count,
+                                                     int32_t workers, float drop_scale, Scales* out) {
+  __shared__ float sm[3][kThreads / 64];
+  float m[3] = {0.f, 0.f, 0.f};  // table, x, coef
+  for (int i = threadIdx.x; i < kPeakW; i += kThreads) m[0] = fmaxf(m[0], peak[i]);
+  for (int i = threadIdx.x; i < kPeakX; i += kThreads) m[1] = fmaxf(m[1], peak[kPeakW + i]);
+  if (count != nullptr)
+    for (int w = threadIdx.x; w < workers; w += kThreads) {
+      const float c = fabsf(coef_of(scale, count, w));
+      if (c < INFINITY) m[2] = fmaxf(m[2], c);
+    }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    for (int o = 32; o > 0; o >>= 1) m[k] = fmaxf(m[k], __shfl_xor(m[k], o));
+    if ((threadIdx.x & 63) == 0) sm[k][threadIdx.x >> 6] = m[k];
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int k = 0; k < 3; ++k)
+    for (int i = 0; i < kThreads / 64; ++i) m[k] = fmaxf(m[k], sm[k][i]);
+  // twice a float32 rounding below the bound: the entries' own scaling rounds
+  const double x = double(m[1]) * double(drop_scale) * (1.0 + 1e-6);
+  out->w = exponent_for(double(m[0]));
+  out->x = exponent_for(x);
+  out->cx = exponent_for(x * double(m[2]) * (1.0 + 1e-6));
 }
 
 struct PackRows {
@@ -434,11 +545,27 @@ struct PackRows {
   int64_t vocab;
 };
 
+// Where a matrix is packed: bf16 as it is; float32 in two fp16 parts, scaled, and if `scaled`
+// is given once more with every row times its coef.
+struct PackTo {
+  uint16_t *plain, *scaled;
+  int64_t part;
+  const Scales* exps;
+  int32_t table;  // which of the powers of two
+};
+
+__device__ __forceinline__ s8v pack8(const uint16_t (&h)[8]) {
+  s8v v;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = short(h[e]);
+  return v;
+}
+
 // One block per workgroup.  Groups of `rows` source rows start at a block of their own
 // (`blocks` of them each).
-template <typename T, int P>
+template <typename T>
 __global__ __launch_bounds__(kThreads) void lm_pack(const T* src, int64_t rows, int32_t dim, int32_t blocks, int32_t cb,
-                                                    uint16_t* dst, int64_t part, PackRows pr, Drop d) {
+                                                    PackTo to, PackRows pr, Drop d) {
   const int64_t rb = blockIdx.x / cb;
   const int32_t c0 = int32_t(blockIdx.x % cb) * kBlk;
   const int64_t w = rb / blocks, t0 = (rb % blocks) * kBlk;
@@ -447,17 +574,18 @@ __global__ __launch_bounds__(kThreads) void lm_pack(const T* src, int64_t rows, 
   for (int it = 0; it < 2; ++it) {
     const int r = it * 32 + int(threadIdx.x) / 8, c = c0 + int(threadIdx.x % 8) * 8;
     const int64_t t = t0 + r, row = w * rows + t;
-    int64_t target = 0;
     bool on = t < rows;
+    float coef = 0.f;
     if (pr.targets != nullptr) {
-      target = on ? pr.targets[row] : -1;
-      on = uint64_t(target) < uint64_t(pr.vocab);
+      const int64_t target = on ? pr.targets[row] : -1;
+      on = counts(target, pr.vocab);
+      if (on && pr.count != nullptr) coef = coef_of(pr.scale, pr.count, w);
       if (c == 0) {
-        RowInfo ri{};
-        ri.target = on ? int32_t(target) : -1;
-        if (on && pr.count != nullptr) {
-          ri.coef = float((pr.scale != nullptr ? double(pr.scale[w]) : 1.0) / double(pr.count[w]));
-          ri.lse = pr.lse[row];
+        RowInfo ri{on ? int32_t(target) : -1, coef, 0.f, 0.f};
+        if (on && pr.lse != nullptr) {
+          const double l = double(pr.lse[row]) * double(kLog2e);
+          ri.hi = float(l);
+          ri.lo = fabs(l) < 1e38 ? float(l - double(ri.hi)) : 0.f;
         }
         pr.info[rb * kBlk + r] = ri;
       }
@@ -474,16 +602,25 @@ __global__ __launch_bounds__(kThreads) void lm_pack(const T* src, int64_t rows, 
       }
       if (d.on) drop<8>(d, step, uint64_t(row) * uint64_t(dim) + uint64_t(c), x);
     }
-    uint16_t h[8][P];
+    const int64_t o = int64_t(blockIdx.x) * kBlkElems + r * kBlk + ((int(threadIdx.x % 8) ^ turn(r)) << 3);
+    uint16_t h[8], l[8];
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) split<P>(x[e], h[e]);
-    uint16_t* o = dst + int64_t(blockIdx.x) * kBlkElems + r * kBlk + ((int(threadIdx.x % 8) ^ turn(r)) << 3);
+      for (int e = 0; e < 8; ++e) h[e] = narrow_bits(x[e]);
+      *reinterpret_cast<s8v*>(to.plain + o) = pack8(h);
+    } else {
+      const int32_t e0 = to.table ? to.exps->w : to.exps->x;
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      s8v v;
+      for (int e = 0; e < 8; ++e) split16(ldexpf(x[e], e0), h[e], l[e]);
+      *reinterpret_cast<s8v*>(to.plain + o) = pack8(h);
+      *reinterpret_cast<s8v*>(to.plain + to.part + o) = pack8(l);
+      if (to.scaled != nullptr) {
+        const int32_t e1 = to.exps->cx;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = short(h[e][p]);
-      *reinterpret_cast<s8v*>(o + p * part) = v;
+        for (int e = 0; e < 8; ++e) split16(on ? ldexpf(coef * x[e], e1) : 0.f, h[e], l[e]);
+        *reinterpret_cast<s8v*>(to.scaled + o) = pack8(h);
+        *reinterpret_cast<s8v*>(to.scaled + to.part + o) = pack8(l);
+      }
     }
   }
 }
@@ -502,37 +639,59 @@ __device__ __forceinline__ bool tile_at(int64_t id, int64_t n_v, int64_t n_t, in
   return true;
 }
 
-typedef Gemm<2, 4, 4, 2, false, false> ScoreGemm;
-
 struct ScoreArgs {
   Mat w, x;
   Parts parts;
+  int32_t tail;          // steps of 16 in the last block of a row
   int32_t v0, v1;        // vocabulary blocks [v0, v1) of this launch
   int32_t t0, t1;        // row blocks
   int64_t vocab;
   const RowInfo* info;   // from row block 0 on
+  const Scales* exps;    // float32 operands
   float2* stat;          // loss: [vocabulary tile][row of the launch] maximum and sum
   float* hit;            // loss: [row] the target's score
   uint16_t* g;           // gradient: blocks [t1 - t0][v1 - v0]
   int64_t g_part;
 };
 
+// What a launch of lm_scores leaves.
+enum ScoreKind {
+  kLossBf16, kLossF32,
+  kGradBf16,   // g in bf16
+  kGradBf16x3,  // g in three bf16 parts
+  kGradF32     // g / coef in two fp16 parts
+};
+
 // Scores of 256 words x 256 rows: lane l of a wave holds words in its accumulators and row
 // l mod 32 of each of its two pieces, so a row's maximum and sum are taken within a lane, then
-// over its two lane halves and the two waves that share the row.
-template <int GP>
-__global__ __launch_bounds__(ScoreGemm::kT) void lm_scores(ScoreArgs p) {
-  typedef ScoreGemm G;
+// over its two lane halves and the two waves that share the row.  Maxima and sums are those of
+// exp2 of s log2(e): m the largest of them, and sum exp2(s log2(e) - m).
+template <int KIND>
+__global__ __launch_bounds__(512) void lm_scores(ScoreArgs p) {
+  constexpr bool kF16 = KIND == kLossF32 || KIND == kGradF32;
+  typedef Gemm<2, 4, 4, 2, false, false, kF16> G;
   __shared__ __align__(16) uint16_t s0[G::kStage], s1[G::kStage];
   int vt, tt;
   if (!tile_at(blockIdx.x, (p.v1 - p.v0 + kTile - 1) / kTile, (p.t1 - p.t0 + kTile - 1) / kTile, vt, tt)) return;
   const int v0 = p.v0 + vt * kTile, t0 = p.t0 + tt * kTile;
-  G::Acc acc = {};
-  G::run(p.w, v0, p.x, t0, 0, p.w.cb, p.parts, (lds_t*)s0, (lds_t*)s1, acc);
+  typename G::Acc acc = {};
+  G::run(p.w, v0, p.x, t0, 0, p.w.cb, p.tail, p.parts, (lds_t*)s0, (lds_t*)s1, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / G::kWN, wn = wave % G::kWN;
   const int64_t word0 = int64_t(v0) * kBlk + wm * G::kRowsA;  // of this wave
   const int n_words = int(min(int64_t(G::kRowsA), p.vocab - word0));  // may be negative
-  if constexpr (GP == 0) {
+  float unit = 1.f;  // a score is an accumulator times this
+  if constexpr (kF16) unit = ldexpf(1.f, -(p.exps->x + p.exps->w));
+  const float c = kLog2e * unit;
+  if constexpr (KIND == kLossBf16 || KIND == kLossF32) {
+    if (n_words < G::kRowsA) {
+#pragma unroll
+      for (int j = 0; j < G::kFN; ++j)
+#pragma unroll
+        for (int i = 0; i < G::kFM; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (i * 32 + acc_row(e, lane) >= n_words) acc[i][j][e] = -INFINITY;
+    }
     float2* joined = reinterpret_cast<float2*>(s0);  // the main loop ends in a barrier: its LDS is free
 #pragma unroll
     for (int j = 0; j < G::kFN; ++j) {
@@ -542,17 +701,14 @@ __global__ __launch_bounds__(ScoreGemm::kT) void lm_scores(ScoreArgs p) {
 #pragma unroll
       for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (i * 32 + acc_row(e, lane) >= n_words) acc[i][j][e] = -INFINITY;
-          m = fmaxf(m, acc[i][j][e]);
-        }
-      m = fmaxf(m, __shfl_xor(m, 32));
+        for (int e = 0; e < 16; ++e) m = fmaxf(m, acc[i][j][e]);
+      m = fmaxf(m, __shfl_xor(m, 32)) * c;
       const float base = m == -INFINITY ? 0.f : m;
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s += __expf(acc[i][j][e] - base);
+        for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], c, -base));
       s += __shfl_xor(s, 32);
       const int64_t local = t0 + at / kBlk < p.t1 ? p.info[row].target - word0 : -1;
       const bool here = local >= 0 && local < n_words && (int(local) >> 2 & 1) == lane >> 5;
@@ -563,7 +719,7 @@ __global__ __launch_bounds__(ScoreGemm::kT) void lm_scores(ScoreArgs p) {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             if (i * 32 + acc_row(e, lane) == int(local)) hit = acc[i][j][e];
-        if (here) p.hit[row] = hit;
+        if (here) p.hit[row] = hit * unit;
       }
       if (lane < 32) joined[wm * 256 + at] = make_float2(m, s);
     }
@@ -575,33 +731,49 @@ __global__ __launch_bounds__(ScoreGemm::kT) void lm_scores(ScoreArgs p) {
       for (int k = 1; k < G::kWM; ++k) {
         const float2 b = joined[k * 256 + r];
         const float m = fmaxf(a.x, b.x), base = m == -INFINITY ? 0.f : m;
-        a = make_float2(m, a.y * __expf(a.x - base) + b.y * __expf(b.x - base));
+        a = make_float2(m, a.y * __builtin_amdgcn_exp2f(a.x - base) + b.y * __builtin_amdgcn_exp2f(b.x - base));
       }
       p.stat[int64_t(vt) * (p.t1 - p.t0) * kBlk + int64_t(tt) * 256 + r] = a;
     }
   } else {
-    constexpr int kWb = G::kRowsA / kBlk, kRb = G::kRowsB / kBlk;  // blocks of g per wave
-    constexpr int kHalf = G::kT / 128;  // waves whose blocks fit a stage
-    uint16_t* own = (wave < kHalf ? s0 : s1) + wave % kHalf * kWb * kRb * kBlkElems;
+    constexpr int kParts = KIND == kGradBf16 ? 1 : KIND == kGradF32 ? 2 : 3;
+    constexpr int kWb = G::kRowsA / kBlk;  // blocks of g per wave: kWb x 1
+    static_assert(G::kRowsB == kBlk, "a wave's rows are one block");
+    uint16_t* own = (wave < 4 ? s0 : s1) + wave % 4 * kWb * kBlkElems;
 #pragma unroll
     for (int j = 0; j < G::kFN; ++j) {
       const int at = wn * G::kRowsB + j * 32 + (lane & 31);
-      RowInfo ri{-1, 0.f, 0.f, 0};
+      RowInfo ri{-1, 0.f, 0.f, 0.f};
       if (t0 + at / kBlk < p.t1) ri = p.info[int64_t(t0) * kBlk + at];
-      const float coef = ri.target < 0 ? 0.f : ri.coef;
-      const int local = ri.target < 0 ? -1 : int(max(int64_t(-1), min(int64_t(1 << 20), ri.target - word0)));
+      const bool on = ri.target >= 0;
+      const int64_t local = ri.target - word0;
+      const bool here = on && local >= 0 && local < n_words;
+      const float mul = kF16 ? float(1 << kGExp) : ri.coef;
 #pragma unroll
       for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int v = i * 32 + acc_row(e, lane);
-          float x = __expf(acc[i][j][e] - ri.lse);
-          if (v == local) x -= 1.f;
-          acc[i][j][e] = v < n_words && coef != 0.f ? x * coef : 0.f;
-        }
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], c, -ri.hi) - ri.lo);
+      if (__any(here)) {
+#pragma unroll
+        for (int i = 0; i < G::kFM; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (here && i * 32 + acc_row(e, lane) == int(local)) acc[i][j][e] -= 1.f;
+      }
+#pragma unroll
+      for (int i = 0; i < G::kFM; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] *= mul;
+      if (n_words < G::kRowsA || __any(!on)) {
+#pragma unroll
+        for (int i = 0; i < G::kFM; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (!on || i * 32 + acc_row(e, lane) >= n_words) acc[i][j][e] = 0.f;
+      }
     }
 #pragma unroll
-    for (int part = 0; part < GP; ++part) {
+    for (int part = 0; part < kParts; ++part) {
 #pragma unroll
       for (int j = 0; j < G::kFN; ++j)
 #pragma unroll
@@ -612,28 +784,28 @@ __global__ __launch_bounds__(ScoreGemm::kT) void lm_scores(ScoreArgs p) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float x = acc[i][j][e4 * 4 + e];
-              const uint16_t b = narrow_bits(x);
-              v[e] = short(b);
-              if (GP > 1) acc[i][j][e4 * 4 + e] = x - widen(b);
+              if constexpr (kF16) {
+                const _Float16 h = _Float16(x);
+                v[e] = __builtin_bit_cast(short, h);
+                if (part == 0) acc[i][j][e4 * 4 + e] = (x - float(h)) * 2048.f;
+              } else {
+                const uint16_t h = narrow_bits(x);
+                v[e] = short(h);
+                if (part + 1 < kParts) acc[i][j][e4 * 4 + e] = x - widen(h);
+              }
             }
-            const int r = (j & 1) * 32 + (lane & 31), c8 = (i & 1) * 4 + e4;
-            *reinterpret_cast<s4v*>(own + ((j >> 1) * kWb + (i >> 1)) * kBlkElems + r * kBlk + ((c8 ^ turn(r)) << 3) +
-                                    (lane >> 5) * 4) = v;
+            const int r = j * 32 + (lane & 31), c8 = (i & 1) * 4 + e4;
+            *reinterpret_cast<s4v*>(own + (i >> 1) * kBlkElems + r * kBlk + ((c8 ^ turn(r)) << 3) + (lane >> 5) * 4) = v;
           }
       __syncthreads();
-      const int vb = v0 - p.v0 + wm * kWb, n_v = p.v1 - p.v0;
+      const int vb = v0 - p.v0 + wm * kWb, n_v = p.v1 - p.v0, tb = t0 + wn;
 #pragma unroll
-      for (int rb = 0; rb < kRb; ++rb) {
-        const int tb = t0 + wn * kRb + rb;
+      for (int b = 0; b < kWb; ++b) {
+        if (tb >= p.t1 || vb + b >= n_v) continue;
+        uint16_t* o = p.g + part * p.g_part + (int64_t(tb - p.t0) * n_v + vb + b) * kBlkElems;
 #pragma unroll
-        for (int b = 0; b < kWb; ++b) {
-          if (tb >= p.t1 || vb + b >= n_v) continue;
-          uint16_t* o = p.g + part * p.g_part + (int64_t(tb - p.t0) * n_v + vb + b) * kBlkElems;
-          const uint16_t* from = own + (rb * kWb + b) * kBlkElems;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<u4v*>(o + (k * 64 + lane) * 8) = *reinterpret_cast<const u4v*>(from + (k * 64 + lane) * 8);
-        }
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<u4v*>(o + (k * 64 + lane) * 8) = *reinterpret_cast<const u4v*>(own + b * kBlkElems + (k * 64 + lane) * 8);
       }
       __syncthreads();
     }
@@ -652,7 +824,7 @@ __global__ __launch_bounds__(kThreads) void lm_rows(const float2* stat, int32_t 
     for (int i = part; i < tiles; i += 8) {
       const float2 a = stat[i * ld + row];
       const float n = fmaxf(m, a.x), base = n == -INFINITY ? 0.f : n;
-      s = s * __expf(m - base) + a.y * __expf(a.x - base);
+      s = s * __builtin_amdgcn_exp2f(m - base) + a.y * __builtin_amdgcn_exp2f(a.x - base);
       m = n;
     }
   sm[threadIdx.x] = make_float2(m, s);
@@ -661,11 +833,11 @@ __global__ __launch_bounds__(kThreads) void lm_rows(const float2* stat, int32_t 
   for (int i = 1; i < 8; ++i) {
     const float2 a = sm[i * 32 + r];
     const float n = fmaxf(m, a.x), base = n == -INFINITY ? 0.f : n;
-    s = s * __expf(m - base) + a.y * __expf(a.x - base);
+    s = s * __builtin_amdgcn_exp2f(m - base) + a.y * __builtin_amdgcn_exp2f(a.x - base);
     m = n;
   }
   const bool on = info[row].target >= 0;
-  const float l = m + logf(s);
+  const float l = float((double(m) + double(log2f(s))) / double(kLog2e));
   lse[row] = on ? l : 0.f;
   losses[row] = on ? l - hit[row] : 0.f;
 }
@@ -684,41 +856,43 @@ __global__ __launch_bounds__(kThreads) void lm_mean(const float* losses, const R
 }
 
 // ------------------------------------------------------------------ products with g
-typedef Gemm<2, 4, 4, 2, false, true> DxGemm;
-typedef Gemm<2, 4, 4, 2, true, true> DwGemm;
-
 struct DxArgs {
   Mat g, w;  // w from the piece's first block on
   Parts parts;
-  int32_t kb, splits;
+  int32_t kb, tail, splits;
+  const Scales* exps;
   float* out;  // [splits][row][ld]
   int64_t rows, ld;
   int32_t add;
 };
 
-__global__ __launch_bounds__(DxGemm::kT) void lm_dx(DxArgs p) {
-  __shared__ __align__(16) uint16_t s0[DxGemm::kStage], s1[DxGemm::kStage];
+template <bool F16>
+__global__ __launch_bounds__(512) void lm_dx(DxArgs p) {
+  typedef Gemm<2, 4, 4, 2, false, true, F16> G;
+  __shared__ __align__(16) uint16_t s0[G::kStage], s1[G::kStage];
   const int n_c = (p.w.cb + kTile - 1) / kTile;
   const int split = blockIdx.x % p.splits, c0 = int(blockIdx.x / p.splits) % n_c * kTile;
   const int r0 = int(blockIdx.x / p.splits) / n_c * kTile;
   const int k0 = int(int64_t(p.kb) * split / p.splits), k1 = int(int64_t(p.kb) * (split + 1) / p.splits);
-  DxGemm::Acc acc = {};
-  DxGemm::run(p.g, r0, p.w, c0, k0, k1, p.parts, (lds_t*)s0, (lds_t*)s1, acc);
+  typename G::Acc acc = {};
+  G::run(p.g, r0, p.w, c0, k0, k1, k1 == p.kb ? p.tail : 4, p.parts, (lds_t*)s0, (lds_t*)s1, acc);
+  const float unit = F16 ? ldexpf(1.f, -(kGExp + p.exps->w)) : 1.f;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float* out = p.out + split * p.rows * p.ld;
 #pragma unroll
-  for (int i = 0; i < DxGemm::kFM; ++i)
+  for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
-    for (int j = 0; j < DxGemm::kFN; ++j) {
-      const int64_t c = int64_t(c0) * kBlk + (wave % DxGemm::kWN) * DxGemm::kRowsB + j * 32 + (lane & 31);
-      const int64_t r = int64_t(r0) * kBlk + (wave / DxGemm::kWN) * DxGemm::kRowsA + i * 32;
+    for (int j = 0; j < G::kFN; ++j) {
+      const int64_t c = int64_t(c0) * kBlk + (wave % G::kWN) * G::kRowsB + j * 32 + (lane & 31);
+      const int64_t r = int64_t(r0) * kBlk + (wave / G::kWN) * G::kRowsA + i * 32;
       if (c >= p.ld) continue;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const int64_t row = r + acc_row(e, lane);
         if (row >= p.rows) continue;
         float* o = out + row * p.ld + c;
-        *o = p.add ? *o + acc[i][j][e] : acc[i][j][e];
+        const float x = F16 ? acc[i][j][e] * unit : acc[i][j][e];
+        *o = p.add ? *o + x : x;
       }
     }
 }
@@ -739,6 +913,10 @@ __global__ __launch_bounds__(kThreads) void lm_dx_out(const float* part, int32_t
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] += y[e];
       }
+      if (sizeof(T) == 4) {  // g was held without its row's coef
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] *= info[r].coef;
+      }
       if (d.on) drop<4>(d, step, uint64_t(row) * uint64_t(dim) + uint64_t(c), x);
     }
     T* o = out + row * dim + c;
@@ -755,34 +933,38 @@ __global__ __launch_bounds__(kThreads) void lm_dx_out(const float* part, int32_t
 struct DwArgs {
   Mat g, x;
   Parts parts;
-  int32_t tw;         // row blocks per worker
+  int32_t tw, tail;   // row blocks per worker
+  const Scales* exps;
   int32_t v0;         // first vocabulary block of the piece
   int64_t vocab, dim, stride;
   int32_t add;
 };
 
-template <typename GT>
-__global__ __launch_bounds__(DwGemm::kT) void lm_dw(DwArgs p, GT* grads) {
-  __shared__ __align__(16) uint16_t s0[DwGemm::kStage], s1[DwGemm::kStage];
+template <bool F16, typename GT>
+__global__ __launch_bounds__(512) void lm_dw(DwArgs p, GT* grads) {
+  typedef Gemm<2, 4, 4, 2, true, true, F16> G;
+  __shared__ __align__(16) uint16_t s0[G::kStage], s1[G::kStage];
   const int n_c = (p.x.cb + kTile - 1) / kTile;
   const int w = blockIdx.y, c0 = int(blockIdx.x % n_c) * kTile, r0 = int(blockIdx.x / n_c) * kTile;
-  DwGemm::Acc acc = {};
-  DwGemm::run(p.g, r0, p.x, c0, w * p.tw, (w + 1) * p.tw, p.parts, (lds_t*)s0, (lds_t*)s1, acc);
+  typename G::Acc acc = {};
+  G::run(p.g, r0, p.x, c0, w * p.tw, (w + 1) * p.tw, p.tail, p.parts, (lds_t*)s0, (lds_t*)s1, acc);
+  const float unit = F16 ? ldexpf(1.f, -(kGExp + p.exps->cx)) : 1.f;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   GT* out = grads + w * p.stride;
 #pragma unroll
-  for (int i = 0; i < DwGemm::kFM; ++i)
+  for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
-    for (int j = 0; j < DwGemm::kFN; ++j) {
-      const int64_t c = int64_t(c0) * kBlk + (wave % DwGemm::kWN) * DwGemm::kRowsB + j * 32 + (lane & 31);
-      const int64_t r = int64_t(r0) * kBlk + (wave / DwGemm::kWN) * DwGemm::kRowsA + i * 32;
+    for (int j = 0; j < G::kFN; ++j) {
+      const int64_t c = int64_t(c0) * kBlk + (wave % G::kWN) * G::kRowsB + j * 32 + (lane & 31);
+      const int64_t r = int64_t(r0) * kBlk + (wave / G::kWN) * G::kRowsA + i * 32;
       if (c >= p.dim) continue;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const int64_t in = r + acc_row(e, lane), row = int64_t(p.v0) * kBlk + in;
         if (in >= int64_t(p.g.cb) * kBlk || row >= p.vocab) continue;
         GT* o = out + row * p.dim + c;
-        put(o, p.add ? widen(*o) + acc[i][j][e] : acc[i][j][e]);
+        const float x = F16 ? acc[i][j][e] * unit : acc[i][j][e];
+        put(o, p.add ? widen(*o) + x : x);
       }
     }
 }
@@ -1065,28 +1247,22 @@ psgd_status make_drop(const char* fn, const psgd_dropout_config* c, Drop* out) {
   return PSGD_OK;
 }
 
-int parts_of(psgd_dtype t) { return t == PSGD_F32 ? 3 : 1; }
-int g_parts(const psgd_lm_plan* plan) { return plan->act == PSGD_F32 || plan->grad == PSGD_F32 ? 3 : 1; }
+int parts_of(psgd_dtype t) { return t == PSGD_F32 ? 2 : 1; }
+int g_parts(const psgd_lm_plan* plan) { return plan->act == PSGD_F32 ? 2 : plan->grad == PSGD_F32 ? 3 : 1; }
 
-// Part products of x (a parts) with y (b parts) that a result of 24 (or, `few`, 16) bits needs.
-Parts make_parts(int a, int b, bool few) {
-  Parts p{};
-  const int most = few ? 1 : 2;
-  for (int s = most; s >= 0; --s)  // the small ones first
-    for (int i = 0; i <= s; ++i)
-      if (i < a && s - i < b) {
-        p.a |= uint32_t(i) << (4 * p.n);
-        p.b |= uint32_t(s - i) << (4 * p.n);
-        ++p.n;
-      }
-  return p;
-}
+constexpr Parts kOne{1, 0, 0};
+constexpr Parts kF32{3, 0x001, 0x010};        // high x low, low x high, high x high
+constexpr Parts kThreeByOne{3, 0x012, 0x000};  // the smallest part first
+
+int32_t steps_of_last(int64_t n) { return int32_t(ceil_div((n - 1) % kBlk + 1, 16)); }
 
 struct Views {
-  Mat x, w;
-  uint16_t *xp, *wp, *g;
+  Mat x, cx, w;
+  uint16_t *xp, *cxp, *wp, *g;
   RowInfo* info;
   int32_t* count;
+  float* peak;
+  Scales* exps;
   float2* stat;
   float *hit, *dx;
 };
@@ -1095,7 +1271,10 @@ Views views(const psgd_lm_plan* plan, void* workspace, int32_t tb) {
   char* ws = static_cast<char*>(workspace);
   Views v{};
   v.xp = reinterpret_cast<uint16_t*>(ws + plan->ws_x);
+  v.cxp = reinterpret_cast<uint16_t*>(ws + plan->ws_cx);
   v.wp = reinterpret_cast<uint16_t*>(ws + plan->ws_w);
+  v.peak = reinterpret_cast<float*>(ws + plan->ws_peak);
+  v.exps = reinterpret_cast<Scales*>(ws + plan->ws_exps);
   v.g = reinterpret_cast<uint16_t*>(ws + plan->ws_g);
   v.info = reinterpret_cast<RowInfo*>(ws + plan->ws_info);
   v.count = reinterpret_cast<int32_t*>(ws + plan->ws_count);
@@ -1103,30 +1282,40 @@ Views views(const psgd_lm_plan* plan, void* workspace, int32_t tb) {
   v.hit = reinterpret_cast<float*>(ws + plan->ws_hit);
   v.dx = reinterpret_cast<float*>(ws + plan->ws_dx);
   v.x = Mat{v.xp, int64_t(tb) * plan->db * kBlkElems, tb, plan->db};
+  v.cx = Mat{v.cxp, v.x.part, tb, plan->db};
   v.w = Mat{v.wp, int64_t(plan->vb) * plan->db * kBlkElems, plan->vb, plan->db};
   return v;
 }
 
-// x in `groups` of `rows` rows, and the table.
+// The powers of two of float32 operands, x in groups of `rows` rows, and the table.
 psgd_status enqueue_pack(psgd_lm_plan* plan, const Views& v, const void* x, const void* params, int64_t rows, int32_t blocks,
                          const PackRows& pr, const Drop& d, hipStream_t st) {
   const Drop none{0, 0, 0, nullptr, 1.f, 0};
   const PackRows all{};
   const dim3 gx(unsigned(int64_t(v.x.rb) * v.x.cb)), gw(unsigned(int64_t(v.w.rb) * v.w.cb));
   const int32_t dim = int32_t(plan->dim);
-  psgd_status s;
-  if (plan->act == PSGD_F32) {
-    s = launch(plan, kPack, lm_pack<float, 3>, gx, kThreads, st, static_cast<const float*>(x), rows, dim, blocks, v.x.cb, v.xp,
-               v.x.part, pr, d);
-    if (s != PSGD_OK) return s;
-    return launch(plan, kPack, lm_pack<float, 3>, gw, kThreads, st, static_cast<const float*>(params) + plan->offset, plan->vocab,
-                  dim, v.w.rb, v.w.cb, v.wp, v.w.part, all, none);
-  }
-  s = launch(plan, kPack, lm_pack<uint16_t, 1>, gx, kThreads, st, static_cast<const uint16_t*>(x), rows, dim, blocks, v.x.cb, v.xp,
-             v.x.part, pr, d);
+  const bool f32 = plan->act == PSGD_F32, grad = pr.count != nullptr;
+  const float* fx = static_cast<const float*>(x);
+  const float* ft = static_cast<const float*>(params) + plan->offset;
+  const int32_t peaks = f32 ? kPeakW + kPeakX : 0, counts = grad ? plan->n_workers : 0;
+  psgd_status s = PSGD_OK;
+  if (peaks + counts > 0)
+    s = launch(plan, kPrep, lm_prep, dim3(unsigned(peaks + counts)), kThreads, st, peaks, ft, plan->vocab * plan->dim, fx,
+               plan->rows * plan->n_workers * plan->dim, v.peak, pr.targets, plan->rows, plan->vocab, v.count);
+  if (s == PSGD_OK && f32)
+    s = launch(plan, kScale, lm_scale, dim3(1), kThreads, st, static_cast<const float*>(v.peak), pr.scale, pr.count,
+               plan->n_workers, d.on ? d.scale : 1.f, v.exps);
   if (s != PSGD_OK) return s;
-  return launch(plan, kPack, lm_pack<uint16_t, 1>, gw, kThreads, st, static_cast<const uint16_t*>(params) + plan->offset,
-                plan->vocab, dim, v.w.rb, v.w.cb, v.wp, v.w.part, all, none);
+  const PackTo tx{v.xp, f32 && grad ? v.cxp : nullptr, v.x.part, v.exps, 0}, tw{v.wp, nullptr, v.w.part, v.exps, 1};
+  if (f32) {
+    s = launch(plan, kPack, lm_pack<float>, gx, kThreads, st, fx, rows, dim, blocks, v.x.cb, tx, pr, d);
+    if (s != PSGD_OK) return s;
+    return launch(plan, kPack, lm_pack<float>, gw, kThreads, st, ft, plan->vocab, dim, v.w.rb, v.w.cb, tw, all, none);
+  }
+  s = launch(plan, kPack, lm_pack<uint16_t>, gx, kThreads, st, static_cast<const uint16_t*>(x), rows, dim, blocks, v.x.cb, tx, pr, d);
+  if (s != PSGD_OK) return s;
+  return launch(plan, kPack, lm_pack<uint16_t>, gw, kThreads, st, static_cast<const uint16_t*>(params) + plan->offset,
+                plan->vocab, dim, v.w.rb, v.w.cb, tw, all, none);
 }
 
 unsigned score_grid(const ScoreArgs& a) {
@@ -1139,11 +1328,11 @@ psgd_status enqueue_loss(psgd_lm_plan* plan, const void* x, const void* params, 
   const Views v = views(plan, workspace, plan->tb);
   const PackRows pr{targets, nullptr, nullptr, nullptr, v.info, plan->vocab};
   psgd_status s = enqueue_pack(plan, v, x, params, rows, plan->tb, pr, d, st);
-  const int p = parts_of(plan->act);
+  const bool f32 = plan->act == PSGD_F32;
   for (int32_t t0 = 0; s == PSGD_OK && t0 < plan->tb; t0 += plan->chunk) {
-    ScoreArgs a{v.w, v.x, make_parts(p, p, false), 0, plan->vb, t0, std::min(plan->tb, t0 + plan->chunk), plan->vocab,
-                v.info, v.stat, v.hit, nullptr, 0};
-    s = launch(plan, kScores, lm_scores<0>, dim3(score_grid(a)), ScoreGemm::kT, st, a);
+    const ScoreArgs a{v.w, v.x, f32 ? kF32 : kOne, steps_of_last(plan->dim), 0, plan->vb, t0, std::min(plan->tb, t0 + plan->chunk),
+                      plan->vocab, v.info, v.exps, v.stat, v.hit, nullptr, 0};
+    s = launch(plan, kScores, f32 ? lm_scores<kLossF32> : lm_scores<kLossBf16>, dim3(score_grid(a)), 512, st, a);
     if (s != PSGD_OK) break;
     const int64_t r0 = int64_t(t0) * kBlk, n = std::min(rows, int64_t(a.t1) * kBlk) - r0;
     s = launch(plan, kRows, lm_rows, dim3(unsigned(ceil_div(n, 32))), kThreads, st, static_cast<const float2*>(v.stat),
@@ -1159,36 +1348,39 @@ psgd_status enqueue_grad(psgd_lm_plan* plan, const void* x, const void* params, 
                          const float* scale, const Drop& d, void* dx, void* grads, bool add, void* workspace, hipStream_t st) {
   const int32_t tb = plan->tw * plan->n_workers;
   const Views v = views(plan, workspace, tb);
-  psgd_status s = launch(plan, kCount, lm_count, dim3(unsigned(plan->n_workers)), kThreads, st, targets, plan->rows,
-                         plan->vocab, v.count);
-  if (s != PSGD_OK) return s;
   const PackRows pr{targets, lse, scale, v.count, v.info, plan->vocab};
-  if ((s = enqueue_pack(plan, v, x, params, plan->rows, plan->tw, pr, d, st)) != PSGD_OK) return s;
-  const int p = parts_of(plan->act), gp = g_parts(plan);
-  const bool f32g = plan->grad == PSGD_F32;
-  const int64_t packed = int64_t(tb) * kBlk, ld = int64_t(plan->db) * kBlk;
+  psgd_status s = enqueue_pack(plan, v, x, params, plan->rows, plan->tw, pr, d, st);
+  if (s != PSGD_OK) return s;
+  const bool f32 = plan->act == PSGD_F32, f32g = plan->grad == PSGD_F32;
+  const int64_t packed = int64_t(tb) * kBlk, ld = int64_t(plan->db) * kBlk, n_c = ceil_div(plan->db, kTile);
   for (int32_t v0 = 0; v0 < plan->vb; v0 += plan->piece) {
     const int32_t v1 = std::min(plan->vb, v0 + plan->piece), n_v = v1 - v0;
     const int64_t g_part = int64_t(tb) * n_v * kBlkElems;
-    const ScoreArgs a{v.w, v.x, make_parts(p, p, false), v0, v1, 0, tb, plan->vocab, v.info, nullptr, nullptr, v.g, g_part};
-    s = launch(plan, kScores, gp == 3 ? lm_scores<3> : lm_scores<1>, dim3(score_grid(a)), ScoreGemm::kT, st, a);
+    const ScoreArgs a{v.w, v.x, f32 ? kF32 : kOne, steps_of_last(plan->dim), v0, v1, 0, tb, plan->vocab, v.info, v.exps, nullptr,
+                      nullptr, v.g, g_part};
+    s = launch(plan, kScores, f32 ? lm_scores<kGradF32> : f32g ? lm_scores<kGradBf16x3> : lm_scores<kGradBf16>,
+               dim3(score_grid(a)), 512, st, a);
     if (s != PSGD_OK) return s;
     const Mat g{v.g, g_part, tb, n_v};
-    const int64_t n_c = ceil_div(plan->db, kTile);
     if (dx != nullptr) {
       Mat w = v.w;
       w.p += int64_t(v0) * w.cb * kBlkElems;
       w.rb = n_v;
-      const DxArgs b{g, w, make_parts(p == 3 ? gp : 1, p, false), n_v, plan->splits, v.dx, packed, ld, v0 > 0 ? 1 : 0};
-      s = launch(plan, kDx, lm_dx, dim3(unsigned(ceil_div(tb, kTile) * n_c * plan->splits)), DxGemm::kT, st, b);
+      const int32_t tail = v1 == plan->vb ? steps_of_last(plan->vocab) : 4;
+      const DxArgs b{g, w, f32 ? kF32 : kOne, n_v, tail, plan->splits, v.exps, v.dx, packed, ld, v0 > 0 ? 1 : 0};
+      s = launch(plan, kDx, f32 ? lm_dx<true> : lm_dx<false>, dim3(unsigned(ceil_div(tb, kTile) * n_c * plan->splits)), 512, st, b);
       if (s != PSGD_OK) return s;
     }
     if (grads != nullptr) {
-      const Parts parts = f32g ? make_parts(gp, p, false) : p == 3 ? make_parts(gp, p, true) : make_parts(1, 1, true);
-      const DwArgs b{g, v.x, parts, plan->tw, v0, plan->vocab, plan->dim, plan->worker_stride, add ? 1 : 0};
+      const DwArgs b{g, f32 ? v.cx : v.x, !f32g ? kOne : f32 ? kF32 : kThreeByOne, plan->tw, steps_of_last(plan->rows), v.exps, v0,
+                     plan->vocab, plan->dim, plan->worker_stride, add ? 1 : 0};
       const dim3 grid(unsigned(ceil_div(n_v, kTile) * n_c), unsigned(plan->n_workers));
-      s = f32g ? launch(plan, kDw, lm_dw<float>, grid, DwGemm::kT, st, b, static_cast<float*>(grads) + plan->offset)
-               : launch(plan, kDw, lm_dw<uint16_t>, grid, DwGemm::kT, st, b, static_cast<uint16_t*>(grads) + plan->offset);
+      if (f32g)
+        s = launch(plan, kDw, f32 ? lm_dw<true, float> : lm_dw<false, float>, grid, 512, st, b,
+                   static_cast<float*>(grads) + plan->offset);
+      else
+        s = launch(plan, kDw, f32 ? lm_dw<true, uint16_t> : lm_dw<false, uint16_t>, grid, 512, st, b,
+                   static_cast<uint16_t*>(grads) + plan->offset);
       if (s != PSGD_OK) return s;
     }
   }
@@ -1309,6 +1501,9 @@ extern "C" psgd_status psgd_lm_plan_create(const psgd_layer* layers, int32_t n_l
       return at;
     };
     plan->ws_x = take(p * uint64_t(tbp) * uint64_t(plan->db) * blk);
+    plan->ws_cx = take(p > 1 ? p * uint64_t(tbp) * uint64_t(plan->db) * blk : 0);
+    plan->ws_peak = take((kPeakW + kPeakX) * sizeof(float));
+    plan->ws_exps = take(sizeof(Scales));
     plan->ws_w = take(p * uint64_t(plan->vb) * uint64_t(plan->db) * blk);
     plan->ws_info = take(uint64_t(tbp) * kBlk * sizeof(RowInfo));
     plan->ws_count = take(uint64_t(n_workers) * 4);

@@ -2,10 +2,13 @@
 
 Tolerances are error bounds, formed for every entry from the oracle's own numbers.  With
 u = 2^-24 and n additions in float32 (the matrix cores' may drop the bits below the last,
-hence 2u each), a product of factors known to 24 bits is off by at most
-(2 n + 8) u sum |a||b|; __expf(x) by (|x| + 3) 2u relatively; a result of type t by half a
-step, eps(t) / 2.  What an error of a score does to lse, g, dx and the table gradient follows
-from their formulas."""
+hence 2u each), a product of exact factors is off by at most (2 n + 8) u sum |a||b|.  A float32
+factor is x 2^e = h + l / 2048 in fp16: h is off by at most 2^-11 of x, l by 2^-11 of that,
+2^-22 of x, and by 2^-36 where l has no more bits, with the largest x 2^e above 2^14: 2^-50 of
+the largest entry (h alone: 2^-11 of x, and 2^-25 / 2^14 = 2^-39 of the largest).  The product
+leaves l l' out, another 2^-22: 3 2^-22 = 12 u together.  exp2 of a difference x is off by
+(|x| + 3) 2u relatively; a result of type t by half a step, eps(t) / 2.  What an error of a
+score does to lse, g, dx and the table gradient follows from their formulas."""
 
 import numpy as np
 import pytest
@@ -95,10 +98,14 @@ class Case:
 
     # -- error bounds
     def n_adds(self, k):
-        return (6 if self.act == "f32" else 1) * (-(-k // 16) + 4)
+        return (3 if self.act == "f32" else 1) * (-(-k // 16) + 4)
 
     def score_error(self, h):
-        return (2 * self.n_adds(self.s["dim"]) + 8) * U * (np.abs(h) @ np.abs(self.table).T) + 2.0 ** -120
+        a, T = np.abs(h), np.abs(self.table)
+        err = (2 * self.n_adds(self.s["dim"]) + 8) * U * (a @ T.T) + 2.0 ** -120
+        if self.act == "f32":
+            err += 12 * U * (a @ T.T) + 2.0 ** -49 * (a.max() * T.sum(1) + T.max() * a.sum(-1, keepdims=True))
+        return err
 
     def bounds_loss(self):
         h, s, ok = O.scores(self.np(self.x), self.table, self.words_np, self.drop)
@@ -134,13 +141,22 @@ class Case:
         eg = c[..., None] * (p * (np.expm1(es) + 2 * U * (np.abs(s - lse[..., None]) + 3)) + 4 * U * p) + 4 * U * np.abs(g)
         eg = np.where(ok[..., None], eg, 0)
         n_x = self.n_adds(self.s["vocab"]) + 20  # pieces and splits are added in float32
-        n_w = 6 * (-(-self.s["rows"] // 16) + 4)
-        T = np.abs(self.table)
-        bf_x = HALF["bf16"] if self.act == "bf16" else 0
-        bf_w = HALF["bf16"] if self.act == self.grad == "bf16" else 2.0 ** -15 if self.act == "f32" and self.grad == "bf16" else 0
-        e_dx = (eg + bf_x * np.abs(g)) @ T + (2 * n_x + 8) * U * (np.abs(g) @ T)
+        n_w = 3 * (-(-self.s["rows"] // 16) + 4)
+        T, H = np.abs(self.table), np.abs(h)
         gt = np.swapaxes(np.abs(g), 1, 2)
-        e_gw = np.swapaxes(eg, 1, 2) @ np.abs(h) + (bf_w + (2 * n_w + 8) * U) * (gt @ np.abs(h)) + gt @ eh
+        e_dx = eg @ T + (2 * n_x + 8) * U * (np.abs(g) @ T)
+        e_gw = np.swapaxes(eg, 1, 2) @ H + (2 * n_w + 8) * U * (gt @ H) + gt @ eh
+        if self.act == "bf16":  # g is rounded to bf16 for dx, and for the table unless that is float32
+            e_dx += HALF["bf16"] * (np.abs(g) @ T)
+            if self.grad == "bf16":
+                e_gw += HALF["bf16"] * (gt @ H)
+        else:  # fp16 parts of g / c (up to 1) and the table, and of g / c and c drop(x)
+            one = c[..., None] > 0
+            unit = np.where(one, np.abs(g) / np.where(one, c[..., None], 1), 0)  # |g / c|
+            cH = c[..., None] * H
+            e_dx += 12 * U * (np.abs(g) @ T) + 2.0 ** -49 * (c[..., None] * T.sum(0) + T.max() * np.abs(g).sum(-1, keepdims=True))
+            part, floor = (12 * U, 2.0 ** -49) if self.grad == "f32" else (2.01 * 2.0 ** -11, 2.0 ** -38)
+            e_gw += (part + 4 * U) * (gt @ H) + floor * (cH.sum(1)[:, None, :] + cH.max() * np.swapaxes(unit, 1, 2).sum(-1, keepdims=True))
         dx, gw = O.loss_grad(x, self.table, self.words_np, lse, scale, self.drop)
         if self.drop is not None:
             e_dx = np.where(O.kept(x.shape, *self.drop), e_dx / max(1e-30, 1 - self.drop[0]), 0) + 4 * U * np.abs(dx)
