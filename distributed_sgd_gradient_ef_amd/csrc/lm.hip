@@ -8,16 +8,16 @@
 // bits; a product of two of them is h l' + l h' (divided by 2048) + h h': the loop over the
 // contraction simply runs three times.
 //
-//   lm_prep    the largest entries of float32 operands, the counted rows of every worker
-//   lm_scale   these operands' powers of two
-//   lm_pack    x (through dropout, zero where a row does not count) and the table, packed
-//   lm_scores  a 256 x 256 tile of T drop(x)^T: its columns' running maximum and sum
-//              (loss), or g of its entries, packed (gradient)
+//   lm_peak    the largest entries of float32 operands
+//   lm_pack    x (through dropout, zero where a row does not count) and the table, packed; the
+//              counted rows of every worker
+//   lm_scores  tiles of T drop(x)^T: their rows' maximum and sum (loss), or g of their entries,
+//              packed (gradient)
 //   lm_rows    lse and loss of every row from the tiles' maxima and sums
 //   lm_mean    the workers' means
-//   lm_dx      g T, added up over the pieces of the vocabulary in float32
-//   lm_dx_out  the sum of its splits, through dropout
-//   lm_dw      g^T drop(x) into the gradient slices
+//   lm_products  g T, added up over the pieces of the vocabulary in float32, and g^T drop(x)
+//              into the gradient slices
+//   lm_dx_out  the sum of g T's splits, through dropout
 //   lm_embed   rows of the table
 //   lm_sort, lm_merge  every worker's (token, row) pairs in order
 //   lm_zero, lm_sum, lm_join  the table gradient from runs of these pairs
@@ -47,18 +47,20 @@ constexpr int kBlkElems = kBlk * kBlk;
 constexpr int64_t kMaxBlocks = int64_t(1) << 23;  // of x or the table: launches of 256 threads each stay below 2^32
 constexpr int kTile = 4;           // blocks per side of a workgroup's tile
 constexpr int kThreads = 256;      // of the kernels around the products
-constexpr int kGroup = 4;          // row tiles that take turns on one vocabulary tile (lm_scores)
-constexpr int64_t kPieceBytes = int64_t(256) << 20;  // g of one piece of the vocabulary
+constexpr int kGroup = 16;         // row blocks that take turns on one vocabulary tile (lm_scores)
+constexpr int64_t kFewStats = 16384;  // maxima and sums of a worker that one workgroup takes in
+constexpr int kSplitBlocks = 8;    // vocabulary blocks of a split of lm_products' dx, at least
+constexpr int64_t kPieceBytes = int64_t(512) << 20;  // g of one piece of the vocabulary
 constexpr int64_t kStatBytes = int64_t(64) << 20;    // maxima and sums of one chunk of rows
 constexpr int kSortMax = 4096;     // pairs sorted by one workgroup
 constexpr int kSortThreads = 512;
 constexpr int kRun = 32;           // sorted pairs summed by one wave
 
 enum KernelId {
-  kPrep = 0, kScale, kPack, kScores, kRows, kMean, kDx, kDxOut, kDw, kEmbed, kSort, kMerge, kZero, kSum, kJoin, kDrop, kNumK
+  kPeak = 0, kPack, kScores, kRows, kMean, kProducts, kDxOut, kEmbed, kSort, kMerge, kZero, kSum, kJoin, kDrop, kNumK
 };
-const char* const kNames[kNumK] = {"lm_prep", "lm_scale", "lm_pack", "lm_scores", "lm_rows", "lm_mean", "lm_dx", "lm_dx_out", "lm_dw",
-                                   "lm_embed", "lm_sort", "lm_merge", "lm_zero", "lm_sum", "lm_join", "lm_dropout"};
+const char* const kNames[kNumK] = {"lm_peak", "lm_pack", "lm_scores", "lm_rows", "lm_mean", "lm_products", "lm_dx_out", "lm_embed",
+                                   "lm_sort", "lm_merge", "lm_zero", "lm_sum", "lm_join", "lm_dropout"};
 
 }  // namespace lm
 }  // namespace psgd
@@ -71,7 +73,9 @@ struct psgd_lm_plan {
   int32_t tb = 0, tw = 0;        // blocks of all rows together, and of one worker's rows
   int32_t piece = 0, splits = 1;  // blocks of the vocabulary per piece, splits of its sum in lm_dx
   int32_t chunk = 0;             // row blocks per chunk in psgd_lm_loss
-  uint64_t ws_x = 0, ws_cx = 0, ws_w = 0, ws_peak = 0, ws_exps = 0, ws_info = 0, ws_count = 0, ws_stat = 0, ws_hit = 0, ws_g = 0, ws_dx = 0;
+  bool direct = false;           // the table is read as it is
+  bool loss_small = false, scores_small = false, grad_small = false;  // which tiles are the small ones
+  uint64_t ws_x = 0, ws_w = 0, ws_peak = 0, ws_exps = 0, ws_info = 0, ws_count = 0, ws_stat = 0, ws_hit = 0, ws_g = 0, ws_dx = 0;
   uint64_t ws_key = 0, ws_key2 = 0, ws_part = 0, workspace_bytes = 0;
   bool timing = false;
   std::vector<psgd::PendingTiming> pending;
@@ -151,9 +155,9 @@ __device__ __forceinline__ void philox(uint64_t i, uint64_t step, uint32_t k0, u
 
 __device__ __forceinline__ uint64_t step_of(const Drop& d) { return d.step != nullptr ? uint64_t(*d.step) : 0u; }
 
-// Entries i to i + N - 1 through dropout.
+// Entries i to i + N - 1 through dropout, the kept ones times `scale`.
 template <int N>
-__device__ __forceinline__ void drop(const Drop& d, uint64_t step, uint64_t i, float (&x)[N]) {
+__device__ __forceinline__ void drop(const Drop& d, uint64_t step, uint64_t i, float scale, float (&x)[N]) {
   const int lead = int(i & 3);
 #pragma unroll
   for (int g = 0; g < (N + 6) / 4; ++g) {
@@ -165,7 +169,7 @@ __device__ __forceinline__ void drop(const Drop& d, uint64_t step, uint64_t i, f
       const int at = e + lead - 4 * g;  // its word, if in 0..3
       if (at >= 0 && at < 4) {
         const uint32_t v = at == 0 ? w[0] : at == 1 ? w[1] : at == 2 ? w[2] : w[3];
-        x[e] = uint64_t(v) >= d.keep_from ? x[e] * d.scale : 0.f;
+        x[e] = uint64_t(v) >= d.keep_from ? x[e] * scale : 0.f;
       }
     }
   }
@@ -176,10 +180,15 @@ __device__ __forceinline__ void drop(const Drop& d, uint64_t step, uint64_t i, f
 // Inside a block element (r, c) is at 64 r + 8 (c / 8 ^ turn(r)) + c % 8: the 16-byte pieces
 // of a row are turned so that neither the reads along rows (16 rows, one piece each) nor the
 // transposing ones (4 rows, two pieces each) meet on a bank.
+//
+// A bfloat16 table whose rows are whole blocks (dim a multiple of 64) needs no packing: its
+// blocks are gathered, 16 bytes a lane, as they go into LDS.  Against packing it first,
+// 131,072 x 2048 for 4096 rows: @@DIRECT@@.
 struct Mat {
   const uint16_t* p;
   int64_t part;  // elements between parts
   int32_t rb, cb;
+  int32_t last;  // not packed: its last row
 };
 
 __device__ __forceinline__ int turn(int r) { return ((r >> 1) & 1) << 2 | ((r >> 2) & 1) << 1 | ((r >> 3) & 1); }
@@ -192,14 +201,15 @@ struct Parts {
 
 typedef __attribute__((address_space(3))) uint16_t lds_t;
 
-// C += A B over blocks [k0, k1) (at least one; of the last, `tail` steps of 16) for a tile of WM FM x WN FN pieces of 32 x 32, each wave FM x FN of
-// them.  TA, TB: the operand's contraction runs along its blocks' rows instead of along
-// their columns; it is then read from LDS with the transposing load.  Two LDS stages; the
-// next blocks are on their way in registers while the matrix cores work on a stage.
-template <int WM, int WN, int FM, int FN, bool TA, bool TB, bool F16>
+// C += A B over blocks [k0, k1) (at least one; of the last, `tail` steps of 16) for a tile of
+// WM FM x WN FN pieces of 32 x 32, each wave FM x FN of them.  TA, TB: the operand's
+// contraction runs along its blocks' rows instead of along their columns; it is then read
+// from LDS with the transposing load.  RA, RB: the operand is not packed.  Two LDS stages: the
+// next blocks go from memory straight into one while the matrix cores work on the other.
+template <int WM, int WN, int FM, int FN, bool TA, bool TB, bool F16, bool RA, bool RB>
 struct Gemm {
-  static_assert(FM == 4 && FN == 2 && (TB || !TA), "what columns_of is written out for");
-  static constexpr int kT = WM * WN * 64;
+  static_assert((FM == 4 && FN == 2) || (FM == 1 && FN == 1), "what the LDS reads are written out for");
+  static constexpr int kWaves = WM * WN, kT = kWaves * 64;
   static constexpr int kA = WM * FM / 2, kB = WN * FN / 2;  // blocks of the tile's sides
   static constexpr int kPer = kBlkElems / 8 / kT;           // 16-byte pieces of a block per thread
   static constexpr int kStage = (kA + kB) * kBlkElems;
@@ -208,10 +218,23 @@ struct Gemm {
   static constexpr int kFM = FM, kFN = FN, kWN = WN, kWM = WM;
   static_assert(kPer * kT * 8 == kBlkElems, "a block is a whole number of pieces per thread");
 
-  template <bool T>
-  static __device__ __forceinline__ const uint16_t* block(const Mat& m, int part, int side, int k) {
+  // Block (side, k) of an operand into LDS.
+  template <bool T, bool R>
+  static __device__ __forceinline__ void fetch(const Mat& m, int part, int side, int k, lds_t* s) {
+    typedef __attribute__((address_space(1))) void from_t;
+    typedef __attribute__((address_space(3))) void to_t;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = T ? k : min(side, m.rb - 1), c = T ? min(side, m.cb - 1) : k;
-    return m.p + part * m.part + (int64_t(r) * m.cb + c) * kBlkElems;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = j * kT + int(threadIdx.x);
+      const uint16_t* g;
+      if constexpr (R)
+        g = m.p + int64_t(min(r * kBlk + i / 8, m.last)) * (m.cb * kBlk) + c * kBlk + ((i % 8 ^ turn(i / 8)) << 3);
+      else
+        g = m.p + part * m.part + (int64_t(r) * m.cb + c) * kBlkElems + i * 8;
+      __builtin_amdgcn_global_load_lds((from_t*)g, (to_t*)(s + (j * kT + wave * 64) * 8), 16, 0, 0);
+    }
   }
 
   // Operand pieces of step kk, 32 x 16 each: row (column) lane % 32, contraction 8 (lane / 32)
@@ -219,7 +242,7 @@ struct Gemm {
   static __device__ __forceinline__ void rows_at(int f0, int lane, uint32_t (&at)[4]) {
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
-      at[kk] = 2 * ((f0 >> 1) * kBlkElems + (lane & 31) * kBlk + (((kk * 2 + (lane >> 5)) ^ turn(lane)) << 3));
+      at[kk] = 2 * ((f0 >> 1) * kBlkElems + ((f0 & 1) * 32 + (lane & 31)) * kBlk + (((kk * 2 + (lane >> 5)) ^ turn(lane)) << 3));
   }
 
   static __device__ __forceinline__ void rows_of(uint32_t a, bf8 (&x)[4]) {
@@ -231,6 +254,25 @@ struct Gemm {
         "s_waitcnt lgkmcnt(0)"
         : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
         : "v"(a)
+        : "memory");
+  }
+
+  static __device__ __forceinline__ void rows_of(uint32_t a, bf8 (&x)[1]) {
+    asm volatile(
+        "ds_read_b128 %0, %1\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(x[0])
+        : "v"(a)
+        : "memory");
+  }
+
+  static __device__ __forceinline__ void rows_of(uint32_t a, uint32_t b, bf8 (&x)[1], bf8 (&y)[1]) {
+    asm volatile(
+        "ds_read_b128 %0, %2\n"
+        "ds_read_b128 %1, %3\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(x[0]), "=&v"(y[0])
+        : "v"(a), "v"(b)
         : "memory");
   }
 
@@ -249,15 +291,15 @@ struct Gemm {
   }
 
   // The same from an operand whose contraction runs along the blocks' rows: a transposing read
-  // takes 4 rows x 16 columns per 16 lanes.  at[p][j]: a lane's byte addresses for even and
-  // odd pieces and for the two halves of its eight contraction slots.
+  // takes 4 rows x 16 columns per 16 lanes.  at[p][j]: a lane's byte addresses for pieces
+  // f0 + p of a block and for the two halves of its eight contraction slots.
   static __device__ __forceinline__ void columns_at(int f0, int lane, uint32_t (&at)[2][2]) {
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int k = (lane >> 5) * 8 + j * 4 + ((lane & 15) >> 2);
-        const int c = p * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+        const int c = ((f0 + p) & 1) * 4 + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
         at[p][j] = 2 * ((f0 >> 1) * kBlkElems + k * kBlk + ((c ^ turn(k)) << 3) + (lane & 1) * 4);
       }
   }
@@ -285,6 +327,36 @@ struct Gemm {
         : "memory");
     y[0] = join(v[0], v[1]);
     y[1] = join(v[2], v[3]);
+  }
+
+  template <int OFF>
+  static __device__ __forceinline__ void columns_of(const uint32_t (&b)[2][2], bf8 (&y)[1]) {
+    s4v v[2];
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %2 offset:%4\n"
+        "ds_read_b64_tr_b16 %1, %3 offset:%4\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1])
+        : "v"(b[0][0]), "v"(b[0][1]), "n"(OFF)
+        : "memory");
+    y[0] = join(v[0], v[1]);
+  }
+
+  template <int OFF>
+  static __device__ __forceinline__ void columns_of(const uint32_t (&a)[2][2], const uint32_t (&b)[2][2], bf8 (&x)[1],
+                                                    bf8 (&y)[1]) {
+    s4v v[4];
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %4 offset:%8\n"
+        "ds_read_b64_tr_b16 %1, %5 offset:%8\n"
+        "ds_read_b64_tr_b16 %2, %6 offset:%8\n"
+        "ds_read_b64_tr_b16 %3, %7 offset:%8\n"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+        : "v"(a[0][0]), "v"(a[0][1]), "v"(b[0][0]), "v"(b[0][1]), "n"(OFF)
+        : "memory");
+    x[0] = join(v[0], v[1]);
+    y[0] = join(v[2], v[3]);
   }
 
   template <int OFF>
@@ -316,18 +388,6 @@ struct Gemm {
     for (int f = 0; f < 2; ++f) y[f] = join(v[8 + 2 * f], v[9 + 2 * f]);
   }
 
-  // A block from memory into LDS, 16 bytes a lane, past the registers.
-  template <bool T>
-  static __device__ __forceinline__ void fetch(const Mat& m, int part, int side, int k, lds_t* s) {
-    typedef __attribute__((address_space(1))) void from_t;
-    typedef __attribute__((address_space(3))) void to_t;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint16_t* g = block<T>(m, part, side, k) + threadIdx.x * 8;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      __builtin_amdgcn_global_load_lds((from_t*)(g + j * kT * 8), (to_t*)(s + (j * kT + wave * 64) * 8), 16, 0, 0);
-  }
-
   static __device__ __forceinline__ void sweep(const Mat& a, int a0, const Mat& b, int b0, int k0, int k1, int tail, const Parts& parts,
                                                  lds_t* s0, lds_t* s1, Acc& acc) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -336,9 +396,9 @@ struct Gemm {
     uint32_t pa = parts.a, pb = parts.b;
     auto stage = [&](lds_t* s) {
 #pragma unroll
-      for (int i = 0; i < kA; ++i) fetch<TA>(a, pa & 15, a0 + i, k, s + i * kBlkElems);
+      for (int i = 0; i < kA; ++i) fetch<TA, RA>(a, pa & 15, a0 + i, k, s + i * kBlkElems);
 #pragma unroll
-      for (int i = 0; i < kB; ++i) fetch<TB>(b, pb & 15, b0 + i, k, s + (kA + i) * kBlkElems);
+      for (int i = 0; i < kB; ++i) fetch<TB, RB>(b, pb & 15, b0 + i, k, s + (kA + i) * kBlkElems);
       if (++k == k1) k = k0, pa >>= 4, pb >>= 4;
     };
     uint32_t at_a[2][2], at_b[2][2];
@@ -423,12 +483,12 @@ struct Gemm {
 __device__ __forceinline__ int acc_row(int i, int lane) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
 
 // ------------------------------------------------------------------ rows and packing
-// What the products with g need of a packed row.  exp(s - lse) is taken as
+// What the score tiles need of a packed row.  exp(s - lse) is taken as
 // exp2(s log2(e) - (hi + lo)), with the float32 next to log2(e) in both places.
 struct RowInfo {
   int32_t target;  // -1: the row does not count
-  float coef;      // scale / counted
   float hi, lo;    // lse * kLog2e
+  float pad;
 };
 
 constexpr float kLog2e = 1.44269504f;
@@ -437,10 +497,10 @@ constexpr int kGExp = 14;  // g is held in fp16 as g 2^14: it is below 1 but for
 // float32 operands: their powers of two.  An operand is scaled so that its largest finite
 // entry lies in [2^14, 2^15): its fp16 parts hold 22 bits of entries down to 2^-28 of it.
 struct Scales {
-  int32_t x, w, cx;  // of drop(x), the table, coef * drop(x)
+  int32_t w, x;  // of the table, of x
 };
 
-constexpr int kPeakW = 256, kPeakX = 64;  // workgroups that look for the largest entry
+constexpr int kPeakW = 768, kPeakX = 256;  // workgroups that look for the largest entry
 
 template <typename F>
 __device__ __forceinline__ F block_sum(F x, F* sm) {
@@ -455,187 +515,177 @@ __device__ __forceinline__ F block_sum(F x, F* sm) {
 
 __device__ __forceinline__ bool counts(int64_t target, int64_t vocab) { return uint64_t(target) < uint64_t(vocab); }
 
-// Largest finite magnitude of every part of the table and of x, and the counted rows of every
-// worker: what the first kPeakW + kPeakX workgroups and the ones after them do (`peaks` 0:
-// there are only the latter).
-__global__ __launch_bounds__(kThreads) void lm_prep(int32_t peaks, const float* table, int64_t n_table, const float* x,
-                                                    int64_t n_x, float* peak, const int64_t* targets, int64_t rows,
-                                                    int64_t vocab, int32_t* count) {
-  __shared__ int32_t sm[kThreads / 64];
+// Largest finite magnitude (as its bits) of every part of the table and of x.
+__global__ __launch_bounds__(kThreads) void lm_peak(const float* table, int64_t n_table, const float* x, int64_t n_x,
+                                                    uint32_t* peak) {
+  __shared__ uint32_t sm[kThreads / 64];
   const int job = blockIdx.x;
-  if (job < peaks) {
-    const bool t = job < kPeakW;
-    const float* p = t ? table : x;
-    const int64_t n = t ? n_table : n_x, part = t ? job : job - kPeakW, of = t ? kPeakW : kPeakX;
-    const int64_t per = (n + of * 4 - 1) / (of * 4) * 4, end = min(n, (part + 1) * per);
-    uint32_t m = 0;
-    for (int64_t i = part * per + threadIdx.x * 4; i < end; i += kThreads * 4) {
-      float v[4] = {};
-      if (i + 4 <= end) {
-        load<4>(p + i, v);
+  const bool t = job < kPeakW;
+  const float* p = t ? table : x;
+  const int64_t n = t ? n_table : n_x, part = t ? job : job - kPeakW, of = t ? kPeakW : kPeakX;
+  const int64_t per = (n + of * 4 - 1) / (of * 4) * 4, end = min(n, (part + 1) * per);
+  uint32_t m = 0;
+  for (int64_t i = part * per + threadIdx.x * 4; i < end; i += kThreads * 16) {
+    float v[4][4] = {};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t at = i + k * kThreads * 4;
+      if (at + 4 <= end) {
+        load<4>(p + at, v[k]);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (i + e < end) v[e] = p[i + e];
+          if (at + e < end) v[k][e] = p[at + e];
       }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint32_t u = __float_as_uint(v[e]) & 0x7fffffffu;
-        if (u < 0x7f800000u) m = max(m, u);
+        const uint32_t u = __float_as_uint(v[k][e]) & 0x7fffffffu;
+        m = max(m, u < 0x7f800000u ? u : 0u);
       }
-    }
-    for (int o = 32; o > 0; o >>= 1) m = max(m, uint32_t(__shfl_xor(int(m), o)));
-    if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = int32_t(m);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int i = 1; i < kThreads / 64; ++i) m = max(m, uint32_t(sm[i]));
-      peak[job] = __uint_as_float(m);
-    }
-    return;
   }
-  const int w = job - peaks;
-  int32_t n = 0;
-  for (int64_t i = threadIdx.x; i < rows; i += kThreads) n += counts(targets[w * rows + i], vocab) ? 1 : 0;
-  n = block_sum(n, sm);
-  if (threadIdx.x == 0) count[w] = n;
-}
-
-__device__ __forceinline__ float coef_of(const float* scale, const int32_t* count, int64_t w) {
-  return float((scale != nullptr ? double(scale[w]) : 1.0) / double(max(1, count[w])));
-}
-
-__device__ __forceinline__ int32_t exponent_for(double largest) {
-  return largest > 0.0 && largest < 1e300 ? max(-200, min(200, 14 - ilogb(largest))) : 0;
-}
-
-// The operands' powers of two.
-__global__ __launch_bounds__(kThreads) void lm_scale(const float* peak, const float* scale, const int32_t* count,
-                                                     int32_t workers, float drop_scale, Scales* out) {
-  __shared__ float sm[3][kThreads / 64];
-  float m[3] = {0.f, 0.f, 0.f};  // table, x, coef
-  for (int i = threadIdx.x; i < kPeakW; i += kThreads) m[0] = fmaxf(m[0], peak[i]);
-  for (int i = threadIdx.x; i < kPeakX; i += kThreads) m[1] = fmaxf(m[1], peak[kPeakW + i]);
-  if (count != nullptr)
-    for (int w = threadIdx.x; w < workers; w += kThreads) {
-      const float c = fabsf(coef_of(scale, count, w));
-      if (c < INFINITY) m[2] = fmaxf(m[2], c);
-    }
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    for (int o = 32; o > 0; o >>= 1) m[k] = fmaxf(m[k], __shfl_xor(m[k], o));
-    if ((threadIdx.x & 63) == 0) sm[k][threadIdx.x >> 6] = m[k];
-  }
+  for (int o = 32; o > 0; o >>= 1) m = max(m, uint32_t(__shfl_xor(int(m), o)));
+  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
   __syncthreads();
   if (threadIdx.x != 0) return;
-  for (int k = 0; k < 3; ++k)
-    for (int i = 0; i < kThreads / 64; ++i) m[k] = fmaxf(m[k], sm[k][i]);
-  // twice a float32 rounding below the bound: the entries' own scaling rounds
-  const double x = double(m[1]) * double(drop_scale) * (1.0 + 1e-6);
-  out->w = exponent_for(double(m[0]));
-  out->x = exponent_for(x);
-  out->cx = exponent_for(x * double(m[2]) * (1.0 + 1e-6));
+  for (int i = 1; i < kThreads / 64; ++i) m = max(m, sm[i]);
+  peak[job] = m;
 }
 
-struct PackRows {
-  const int64_t* targets;  // NULL: no rows are left out and no RowInfo is written
-  const float* lse;        // NULL for the loss
-  const float* scale;
-  const int32_t* count;
-  RowInfo* info;
-  int64_t vocab;
-};
-
-// Where a matrix is packed: bf16 as it is; float32 in two fp16 parts, scaled, and if `scaled`
-// is given once more with every row times its coef.
-struct PackTo {
-  uint16_t *plain, *scaled;
-  int64_t part;
-  const Scales* exps;
-  int32_t table;  // which of the powers of two
-};
-
-__device__ __forceinline__ s8v pack8(const uint16_t (&h)[8]) {
-  s8v v;
+// The power of two that brings the largest of `n` peaks into [2^14, 2^15).
+__device__ __forceinline__ int32_t power_of_two(const uint32_t* peak, int n) {
+  __shared__ uint32_t sm[kThreads / 64];
+  uint32_t m = 0;
+  for (int i = threadIdx.x; i < n; i += kThreads) m = max(m, peak[i]);
+  for (int o = 32; o > 0; o >>= 1) m = max(m, uint32_t(__shfl_xor(int(m), o)));
+  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
+  __syncthreads();
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = short(h[e]);
-  return v;
+  for (int i = 0; i < kThreads / 64; ++i) m = max(m, sm[i]);
+  return m != 0 ? 14 - ilogbf(__uint_as_float(m)) : 0;
 }
 
-// One block per workgroup.  Groups of `rows` source rows start at a block of their own
-// (`blocks` of them each).
+// What every row of a worker's g is multiplied by.
+__device__ __forceinline__ float coef_of(const float* scale, const int32_t* count, int64_t w) {
+  return count[w] > 0 ? float((scale != nullptr ? double(scale[w]) : 1.0) / double(count[w])) : 0.f;
+}
+
+struct PackArgs {
+  const void *x, *table;
+  Mat x_to, w_to;        // packed (p is written); w_to.p NULL: the table is read as it is
+  int64_t rows;          // of x in each group, which starts at a block of its own ...
+  int32_t blocks, groups;  // ... of `blocks`
+  int64_t workers, worker_rows;  // how the targets are counted
+  int64_t vocab;
+  int32_t dim;
+  const int64_t* targets;
+  const float* lse;      // NULL for the loss
+  RowInfo* info;
+  int32_t* count;        // counted rows of every worker, or NULL
+  const uint32_t* peak;  // float32 operands
+  Scales* exps;
+};
+
+// One block per workgroup: those of x (through dropout, but not scaled: the products' results
+// are; zero where a row does not count), those of the table, and after them one workgroup per
+// worker that counts its rows.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void lm_pack(const T* src, int64_t rows, int32_t dim, int32_t blocks, int32_t cb,
-                                                    PackTo to, PackRows pr, Drop d) {
-  const int64_t rb = blockIdx.x / cb;
-  const int32_t c0 = int32_t(blockIdx.x % cb) * kBlk;
-  const int64_t w = rb / blocks, t0 = (rb % blocks) * kBlk;
-  const uint64_t step = d.on ? step_of(d) : 0;
+__global__ __launch_bounds__(kThreads) void lm_pack(PackArgs p, Drop d) {
+  const int32_t cb = p.x_to.cb;
+  const int64_t n_x = int64_t(p.x_to.rb) * cb, n_w = p.w_to.p != nullptr ? int64_t(p.w_to.rb) * cb : 0;
+  const int64_t job = blockIdx.x;
+  if (job >= n_x + n_w) {
+    __shared__ int32_t sm[kThreads / 64];
+    const int64_t w = job - n_x - n_w;
+    int32_t n = 0;
+    for (int64_t i = threadIdx.x; i < p.worker_rows; i += kThreads) n += counts(p.targets[w * p.worker_rows + i], p.vocab) ? 1 : 0;
+    n = block_sum(n, sm);
+    if (threadIdx.x == 0) p.count[w] = n;
+    return;
+  }
+  const bool of_x = job < n_x;
+  const int64_t block = of_x ? job : job - n_x, rb = block / cb, blocks = of_x ? p.blocks : p.w_to.rb;
+  const int64_t rows = of_x ? p.rows : p.vocab, w = rb / blocks, t0 = (rb % blocks) * kBlk;
+  const int32_t c0 = int32_t(block % cb) * kBlk;
+  const T* src = static_cast<const T*>(of_x ? p.x : p.table);
+  const Mat& to = of_x ? p.x_to : p.w_to;
+  uint16_t* dst = const_cast<uint16_t*>(to.p) + block * kBlkElems;
+  const bool dropped = of_x && d.on;
+  const uint64_t step = dropped ? step_of(d) : 0;
+  int32_t exp2 = 0;
+  if constexpr (sizeof(T) == 4) {
+    exp2 = power_of_two(of_x ? p.peak + kPeakW : p.peak, of_x ? kPeakX : kPeakW);
+    if (threadIdx.x == 0 && block == 0) (of_x ? p.exps->x : p.exps->w) = exp2;
+  }
 #pragma unroll
   for (int it = 0; it < 2; ++it) {
     const int r = it * 32 + int(threadIdx.x) / 8, c = c0 + int(threadIdx.x % 8) * 8;
     const int64_t t = t0 + r, row = w * rows + t;
     bool on = t < rows;
-    float coef = 0.f;
-    if (pr.targets != nullptr) {
-      const int64_t target = on ? pr.targets[row] : -1;
-      on = counts(target, pr.vocab);
-      if (on && pr.count != nullptr) coef = coef_of(pr.scale, pr.count, w);
+    if (of_x) {
+      const int64_t target = on ? p.targets[row] : -1;
+      on = counts(target, p.vocab);
       if (c == 0) {
-        RowInfo ri{on ? int32_t(target) : -1, coef, 0.f, 0.f};
-        if (on && pr.lse != nullptr) {
-          const double l = double(pr.lse[row]) * double(kLog2e);
+        RowInfo ri{on ? int32_t(target) : -1, 0.f, 0.f, 0.f};
+        if (on && p.lse != nullptr) {
+          const double l = double(p.lse[row]) * double(kLog2e);
           ri.hi = float(l);
           ri.lo = fabs(l) < 1e38 ? float(l - double(ri.hi)) : 0.f;
         }
-        pr.info[rb * kBlk + r] = ri;
+        p.info[rb * kBlk + r] = ri;
       }
     }
     float x[8] = {};
-    if (on && c < dim) {
-      const T* p = src + row * dim + c;
-      if (c + 8 <= dim) {
-        load<8>(p, x);
+    if (on && c < p.dim) {
+      const T* from = src + row * p.dim + c;
+      if (c + 8 <= p.dim) {
+        load<8>(from, x);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (c + e < dim) x[e] = widen(p[e]);
+          if (c + e < p.dim) x[e] = widen(from[e]);
       }
-      if (d.on) drop<8>(d, step, uint64_t(row) * uint64_t(dim) + uint64_t(c), x);
+      if (dropped) drop<8>(d, step, uint64_t(row) * uint64_t(p.dim) + uint64_t(c), 1.f, x);
     }
-    const int64_t o = int64_t(blockIdx.x) * kBlkElems + r * kBlk + ((int(threadIdx.x % 8) ^ turn(r)) << 3);
-    uint16_t h[8], l[8];
-    if constexpr (sizeof(T) == 2) {
+    uint16_t* o = dst + r * kBlk + ((int(threadIdx.x % 8) ^ turn(r)) << 3);
+    s8v h, l;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = narrow_bits(x[e]);
-      *reinterpret_cast<s8v*>(to.plain + o) = pack8(h);
-    } else {
-      const int32_t e0 = to.table ? to.exps->w : to.exps->x;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) split16(ldexpf(x[e], e0), h[e], l[e]);
-      *reinterpret_cast<s8v*>(to.plain + o) = pack8(h);
-      *reinterpret_cast<s8v*>(to.plain + to.part + o) = pack8(l);
-      if (to.scaled != nullptr) {
-        const int32_t e1 = to.exps->cx;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) split16(on ? ldexpf(coef * x[e], e1) : 0.f, h[e], l[e]);
-        *reinterpret_cast<s8v*>(to.scaled + o) = pack8(h);
-        *reinterpret_cast<s8v*>(to.scaled + to.part + o) = pack8(l);
-      }
+    for (int e = 0; e < 8; ++e) {
+      uint16_t a = 0, b = 0;
+      if constexpr (sizeof(T) == 2) a = narrow_bits(x[e]);
+      else split16(ldexpf(x[e], exp2), a, b);
+      h[e] = short(a), l[e] = short(b);
     }
+    *reinterpret_cast<s8v*>(o) = h;
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<s8v*>(o + to.part) = l;
   }
 }
 
 // ------------------------------------------------------------------ scores
-// Tile order: every XCD (workgroups are dealt to the eight in turn) gets a contiguous part
-// of the list in which kGroup row tiles take turns on each vocabulary tile, so that both
-// stay in its L2.
-__device__ __forceinline__ bool tile_at(int64_t id, int64_t n_v, int64_t n_t, int& v, int& t) {
-  const int64_t total = n_v * n_t, per = (total + 7) / 8, at = (id % 8) * per + id / 8;
-  if (at >= total || id / 8 >= per) return false;
-  const int64_t group = at / (n_v * kGroup), in = at % (n_v * kGroup);
-  const int64_t width = min(int64_t(kGroup), n_t - group * kGroup);
+// Tile sizes: 256 x 256 by eight waves where that gives at least kFewTiles tiles, and else
+// 64 x 64 by four, so that small problems still spread over the chip: @@TILES@@
+constexpr int64_t kFewTiles = 128;
+
+template <bool SMALL, bool TA, bool TB, bool F16, bool RA, bool RB>
+using Tile = Gemm<2, SMALL ? 2 : 4, SMALL ? 1 : 4, SMALL ? 1 : 2, TA, TB, F16, RA, RB>;
+
+// Workgroups are dealt to the eight XCDs in turn: place `id` of a list of `total` such that
+// every XCD gets a contiguous part of it and neighbours share its L2; -1 past the end.
+__device__ __forceinline__ int64_t place_of(int64_t id, int64_t total) {
+  const int64_t per = (total + 7) / 8, at = (id % 8) * per + id / 8;
+  return at < total && id / 8 < per ? at : -1;
+}
+
+// In that list `group` row tiles take turns on each vocabulary tile.
+__device__ __forceinline__ bool tile_at(int64_t id, int64_t n_v, int64_t n_t, int group, int& v, int& t) {
+  const int64_t at = place_of(id, n_v * n_t);
+  if (at < 0) return false;
+  const int64_t g = at / (n_v * group), in = at % (n_v * group);
+  const int64_t width = min(int64_t(group), n_t - g * group);
   v = int(in / width);
-  t = int(group * kGroup + in % width);
+  t = int(g * group + in % width);
   return true;
 }
 
@@ -648,55 +698,67 @@ struct ScoreArgs {
   int64_t vocab;
   const RowInfo* info;   // from row block 0 on
   const Scales* exps;    // float32 operands
+  float x_scale;         // dropout's
   float2* stat;          // loss: [vocabulary tile][row of the launch] maximum and sum
   float* hit;            // loss: [row] the target's score
   uint16_t* g;           // gradient: blocks [t1 - t0][v1 - v0]
   int64_t g_part;
 };
 
-// What a launch of lm_scores leaves.
+// What a launch of lm_scores leaves.  g lacks its row's factor scale / counted, which is one for
+// all rows of a worker: the products' results are multiplied by it.
 enum ScoreKind {
   kLossBf16, kLossF32,
   kGradBf16,   // g in bf16
   kGradBf16x3,  // g in three bf16 parts
-  kGradF32     // g / coef in two fp16 parts
+  kGradF32     // g in two fp16 parts
 };
 
-// Scores of 256 words x 256 rows: lane l of a wave holds words in its accumulators and row
-// l mod 32 of each of its two pieces, so a row's maximum and sum are taken within a lane, then
+// Scores of a tile of words x rows: lane l of a wave holds words in its accumulators and row
+// l mod 32 of each of its pieces, so a row's maximum and sum are taken within a lane, then
 // over its two lane halves and the two waves that share the row.  Maxima and sums are those of
 // exp2 of s log2(e): m the largest of them, and sum exp2(s log2(e) - m).
-template <int KIND>
-__global__ __launch_bounds__(512) void lm_scores(ScoreArgs p) {
+template <int KIND, bool SMALL, bool R>
+__global__ __launch_bounds__(SMALL ? 256 : 512) void lm_scores(ScoreArgs p) {
   constexpr bool kF16 = KIND == kLossF32 || KIND == kGradF32;
-  typedef Gemm<2, 4, 4, 2, false, false, kF16> G;
+  typedef Tile<SMALL, false, false, kF16, R, false> G;
+  constexpr int kRows = G::kB * kBlk;  // of the tile
   __shared__ __align__(16) uint16_t s0[G::kStage], s1[G::kStage];
   int vt, tt;
-  if (!tile_at(blockIdx.x, (p.v1 - p.v0 + kTile - 1) / kTile, (p.t1 - p.t0 + kTile - 1) / kTile, vt, tt)) return;
-  const int v0 = p.v0 + vt * kTile, t0 = p.t0 + tt * kTile;
+  if (!tile_at(blockIdx.x, (p.v1 - p.v0 + G::kA - 1) / G::kA, (p.t1 - p.t0 + G::kB - 1) / G::kB, kGroup / G::kB, vt, tt)) return;
+  const int v0 = p.v0 + vt * G::kA, t0 = p.t0 + tt * G::kB;
   typename G::Acc acc = {};
   G::run(p.w, v0, p.x, t0, 0, p.w.cb, p.tail, p.parts, (lds_t*)s0, (lds_t*)s1, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / G::kWN, wn = wave % G::kWN;
   const int64_t word0 = int64_t(v0) * kBlk + wm * G::kRowsA;  // of this wave
   const int n_words = int(min(int64_t(G::kRowsA), p.vocab - word0));  // may be negative
-  float unit = 1.f;  // a score is an accumulator times this
-  if constexpr (kF16) unit = ldexpf(1.f, -(p.exps->x + p.exps->w));
-  const float c = kLog2e * unit;
+  float unit = p.x_scale;  // a score is an accumulator times this
+  if constexpr (kF16) unit = ldexpf(unit, -(p.exps->x + p.exps->w));
+  const float c = fmaxf(kLog2e * unit, FLT_MIN);
   if constexpr (KIND == kLossBf16 || KIND == kLossF32) {
-    if (n_words < G::kRowsA) {
-#pragma unroll
-      for (int j = 0; j < G::kFN; ++j)
-#pragma unroll
-        for (int i = 0; i < G::kFM; ++i)
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (i * 32 + acc_row(e, lane) >= n_words) acc[i][j][e] = -INFINITY;
-    }
     float2* joined = reinterpret_cast<float2*>(s0);  // the main loop ends in a barrier: its LDS is free
 #pragma unroll
     for (int j = 0; j < G::kFN; ++j) {
       const int at = wn * G::kRowsB + j * 32 + (lane & 31);  // the row's place in the tile
       const int64_t row = int64_t(t0) * kBlk + at;
+      const int64_t local = t0 + at / kBlk < p.t1 ? p.info[row].target - word0 : -1;
+      const bool here = local >= 0 && local < n_words && (int(local) >> 2 & 1) == lane >> 5;
+      if (__any(here)) {
+        float hit = 0.f;
+#pragma unroll
+        for (int i = 0; i < G::kFM; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (i * 32 + acc_row(e, lane) == int(local)) hit = acc[i][j][e];
+        if (here) p.hit[row] = hit * unit;
+      }
+      if (n_words < G::kRowsA) {
+#pragma unroll
+        for (int i = 0; i < G::kFM; ++i)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (i * 32 + acc_row(e, lane) >= n_words) acc[i][j][e] = -INFINITY;
+      }
       float m = -INFINITY;
 #pragma unroll
       for (int i = 0; i < G::kFM; ++i)
@@ -710,36 +772,26 @@ __global__ __launch_bounds__(512) void lm_scores(ScoreArgs p) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], c, -base));
       s += __shfl_xor(s, 32);
-      const int64_t local = t0 + at / kBlk < p.t1 ? p.info[row].target - word0 : -1;
-      const bool here = local >= 0 && local < n_words && (int(local) >> 2 & 1) == lane >> 5;
-      if (__any(here)) {
-        float hit = 0.f;
-#pragma unroll
-        for (int i = 0; i < G::kFM; ++i)
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (i * 32 + acc_row(e, lane) == int(local)) hit = acc[i][j][e];
-        if (here) p.hit[row] = hit * unit;
-      }
-      if (lane < 32) joined[wm * 256 + at] = make_float2(m, s);
+      if (lane < 32) joined[wm * kRows + at] = make_float2(m, s);
     }
     __syncthreads();
     const int r = threadIdx.x;
-    if (r < 256 && t0 + r / kBlk < p.t1) {
+    if (r < kRows && t0 + r / kBlk < p.t1) {
       float2 a = joined[r];
 #pragma unroll
       for (int k = 1; k < G::kWM; ++k) {
-        const float2 b = joined[k * 256 + r];
+        const float2 b = joined[k * kRows + r];
         const float m = fmaxf(a.x, b.x), base = m == -INFINITY ? 0.f : m;
         a = make_float2(m, a.y * __builtin_amdgcn_exp2f(a.x - base) + b.y * __builtin_amdgcn_exp2f(b.x - base));
       }
-      p.stat[int64_t(vt) * (p.t1 - p.t0) * kBlk + int64_t(tt) * 256 + r] = a;
+      p.stat[int64_t(vt) * (p.t1 - p.t0) * kBlk + int64_t(tt) * kRows + r] = a;
     }
   } else {
     constexpr int kParts = KIND == kGradBf16 ? 1 : KIND == kGradF32 ? 2 : 3;
-    constexpr int kWb = G::kRowsA / kBlk;  // blocks of g per wave: kWb x 1
-    static_assert(G::kRowsB == kBlk, "a wave's rows are one block");
-    uint16_t* own = (wave < 4 ? s0 : s1) + wave % 4 * kWb * kBlkElems;
+    constexpr int kInStage = G::kA + G::kB;  // blocks of a stage
+    static_assert(2 * kInStage >= G::kA * G::kB, "the tile's blocks of g, one part of them, fit the two stages");
+    float g[G::kFM][G::kFN][16];
+    auto place = [&](int block) { return (block < kInStage ? s0 : s1) + block % kInStage * kBlkElems; };
 #pragma unroll
     for (int j = 0; j < G::kFN; ++j) {
       const int at = wn * G::kRowsB + j * 32 + (lane & 31);
@@ -748,29 +800,26 @@ __global__ __launch_bounds__(512) void lm_scores(ScoreArgs p) {
       const bool on = ri.target >= 0;
       const int64_t local = ri.target - word0;
       const bool here = on && local >= 0 && local < n_words;
-      const float mul = kF16 ? float(1 << kGExp) : ri.coef;
+      const float lo = kF16 ? ri.lo - float(kGExp) : ri.lo, one = kF16 ? float(1 << kGExp) : 1.f;
 #pragma unroll
       for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][j][e] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], c, -ri.hi) - ri.lo);
+        for (int e = 0; e < 16; ++e) g[i][j][e] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], c, -ri.hi) - lo);
       if (__any(here)) {
 #pragma unroll
         for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (here && i * 32 + acc_row(e, lane) == int(local)) acc[i][j][e] -= 1.f;
+            if (here && i * 32 + acc_row(e, lane) == int(local)) g[i][j][e] -= one;
       }
-#pragma unroll
-      for (int i = 0; i < G::kFM; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][j][e] *= mul;
       if (n_words < G::kRowsA || __any(!on)) {
 #pragma unroll
         for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (!on || i * 32 + acc_row(e, lane) >= n_words) acc[i][j][e] = 0.f;
+            if (!on || i * 32 + acc_row(e, lane) >= n_words) g[i][j][e] = 0.f;
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int part = 0; part < kParts; ++part) {
@@ -783,63 +832,88 @@ __global__ __launch_bounds__(512) void lm_scores(ScoreArgs p) {
             s4v v;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float x = acc[i][j][e4 * 4 + e];
+              const float x = g[i][j][e4 * 4 + e];
               if constexpr (kF16) {
                 const _Float16 h = _Float16(x);
                 v[e] = __builtin_bit_cast(short, h);
-                if (part == 0) acc[i][j][e4 * 4 + e] = (x - float(h)) * 2048.f;
+                if (part == 0) g[i][j][e4 * 4 + e] = (x - float(h)) * 2048.f;
               } else {
                 const uint16_t h = narrow_bits(x);
                 v[e] = short(h);
-                if (part + 1 < kParts) acc[i][j][e4 * 4 + e] = x - widen(h);
+                if (part + 1 < kParts) g[i][j][e4 * 4 + e] = x - widen(h);
               }
             }
-            const int r = j * 32 + (lane & 31), c8 = (i & 1) * 4 + e4;
-            *reinterpret_cast<s4v*>(own + (i >> 1) * kBlkElems + r * kBlk + ((c8 ^ turn(r)) << 3) + (lane >> 5) * 4) = v;
+            const int row = wn * G::kRowsB + j * 32 + (lane & 31), word = wm * G::kRowsA + i * 32 + e4 * 8;
+            const int r = row % kBlk, c8 = word % kBlk / 8;
+            *reinterpret_cast<s4v*>(place(row / kBlk * G::kA + word / kBlk) + r * kBlk + ((c8 ^ turn(r)) << 3) + (lane >> 5) * 4) = v;
+            __builtin_amdgcn_sched_barrier(0);
           }
       __syncthreads();
-      const int vb = v0 - p.v0 + wm * kWb, n_v = p.v1 - p.v0, tb = t0 + wn;
+      const int n_v = p.v1 - p.v0;
+      constexpr int kPieces = G::kA * G::kB * 8 / G::kWaves;  // 1 KB each, per wave
 #pragma unroll
-      for (int b = 0; b < kWb; ++b) {
-        if (tb >= p.t1 || vb + b >= n_v) continue;
-        uint16_t* o = p.g + part * p.g_part + (int64_t(tb - p.t0) * n_v + vb + b) * kBlkElems;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          *reinterpret_cast<u4v*>(o + (k * 64 + lane) * 8) = *reinterpret_cast<const u4v*>(own + b * kBlkElems + (k * 64 + lane) * 8);
+      for (int k = 0; k < kPieces; ++k) {
+        const int at = wave * kPieces + k, block = at / 8, tb = t0 + block / G::kA, vb = v0 - p.v0 + block % G::kA;
+        if (tb >= p.t1 || vb >= n_v) continue;
+        uint16_t* o = p.g + part * p.g_part + (int64_t(tb - p.t0) * n_v + vb) * kBlkElems + (at % 8 * 64 + lane) * 8;
+        *reinterpret_cast<u4v*>(o) = *reinterpret_cast<const u4v*>(place(block) + (at % 8 * 64 + lane) * 8);
       }
       __syncthreads();
     }
   }
 }
 
-// lse and loss of a row from its `tiles` maxima and sums: 32 rows per workgroup, 8 lanes
-// (64 apart) each.
-__global__ __launch_bounds__(kThreads) void lm_rows(const float2* stat, int32_t tiles, int64_t ld, const RowInfo* info,
-                                                    const float* hit, int64_t rows, float* losses, float* lse) {
+struct RowsArgs {
+  const float2* stat;
+  int32_t tiles;
+  int64_t ld;           // rows per tile in stat
+  const RowInfo* info;
+  const float* hit;
+  int64_t rows;
+  float *losses, *lse;
+  float* mean;          // of each workgroup's rows, or NULL
+};
+
+// lse and loss of rows from their `tiles` maxima and sums: kRowsAt rows at a time per
+// workgroup, the threads kRowsAt apart share a row's tiles.  With `mean`, a workgroup takes
+// all of a worker's `rows` rows and leaves their mean.
+constexpr int kRowsAt = 16;
+
+__global__ __launch_bounds__(kThreads) void lm_rows(RowsArgs p) {
   __shared__ float2 sm[kThreads];
-  const int r = threadIdx.x % 32, part = threadIdx.x / 32;
-  const int64_t row = int64_t(blockIdx.x) * 32 + r;
-  float m = -INFINITY, s = 0.f;
-  if (row < rows)
-    for (int i = part; i < tiles; i += 8) {
-      const float2 a = stat[i * ld + row];
-      const float n = fmaxf(m, a.x), base = n == -INFINITY ? 0.f : n;
+  __shared__ double sums[kThreads / 64];
+  const int r = threadIdx.x % kRowsAt, part = threadIdx.x / kRowsAt;
+  const int64_t first = p.mean != nullptr ? blockIdx.x * p.rows : int64_t(blockIdx.x) * kRowsAt;
+  const int64_t end = p.mean != nullptr ? first + p.rows : min(p.rows, first + kRowsAt);
+  double sum = 0.0, n = 0.0;
+  for (int64_t row0 = first; row0 < end; row0 += kRowsAt) {
+    const int64_t row = row0 + r;
+    float m = -INFINITY, s = 0.f;
+    auto join = [&](const float2& a) {
+      const float top = fmaxf(m, a.x), base = top == -INFINITY ? 0.f : top;
       s = s * __builtin_amdgcn_exp2f(m - base) + a.y * __builtin_amdgcn_exp2f(a.x - base);
-      m = n;
+      m = top;
+    };
+    if (row < end) {
+#pragma unroll 4
+      for (int i = part; i < p.tiles; i += kThreads / kRowsAt) join(p.stat[i * p.ld + row]);
     }
-  sm[threadIdx.x] = make_float2(m, s);
-  __syncthreads();
-  if (part != 0 || row >= rows) return;
-  for (int i = 1; i < 8; ++i) {
-    const float2 a = sm[i * 32 + r];
-    const float n = fmaxf(m, a.x), base = n == -INFINITY ? 0.f : n;
-    s = s * __builtin_amdgcn_exp2f(m - base) + a.y * __builtin_amdgcn_exp2f(a.x - base);
-    m = n;
+    sm[threadIdx.x] = make_float2(m, s);
+    __syncthreads();
+    if (part == 0 && row < end) {
+      for (int i = 1; i < kThreads / kRowsAt; ++i) join(sm[i * kRowsAt + r]);
+      const bool on = p.info[row].target >= 0;
+      const float l = float((double(m) + double(log2f(s))) / double(kLog2e)), loss = on ? l - p.hit[row] : 0.f;
+      p.lse[row] = on ? l : 0.f;
+      p.losses[row] = loss;
+      if (on) sum += double(loss), n += 1.0;
+    }
+    __syncthreads();
   }
-  const bool on = info[row].target >= 0;
-  const float l = float((double(m) + double(log2f(s))) / double(kLog2e));
-  lse[row] = on ? l : 0.f;
-  losses[row] = on ? l - hit[row] : 0.f;
+  if (p.mean == nullptr) return;
+  sum = block_sum(sum, sums);
+  n = block_sum(n, sums);
+  if (threadIdx.x == 0) p.mean[blockIdx.x] = n > 0.0 ? float(sum / n) : 0.f;
 }
 
 __global__ __launch_bounds__(kThreads) void lm_mean(const float* losses, const RowInfo* info, int64_t rows, float* mean) {
@@ -856,54 +930,110 @@ __global__ __launch_bounds__(kThreads) void lm_mean(const float* losses, const R
 }
 
 // ------------------------------------------------------------------ products with g
-struct DxArgs {
-  Mat g, w;  // w from the piece's first block on
-  Parts parts;
-  int32_t kb, tail, splits;
+struct ProductArgs {
+  Mat g, w, x;        // of one piece of the vocabulary, w from its first block on; all rows
+  Parts dx_parts, dw_parts;
   const Scales* exps;
-  float* out;  // [splits][row][ld]
-  int64_t rows, ld;
-  int32_t add;
+  const float* scale;
+  const int32_t* count;
+  const RowInfo* info;
+  int64_t dim;
+  float x_scale;      // dropout's
+  int32_t tw;         // row blocks per worker
+  int32_t workers;
+  int64_t rows;       // per worker
+  // dx = g T
+  int32_t dx_jobs, splits, dx_tail;
+  float* dx_part;     // [splits][packed row][ld], or NULL: straight into dx
+  void* dx;
+  int64_t ld;
+  int32_t dx_add;
+  // table gradient = g^T drop(x)
+  int32_t dw_jobs, dw_tail;
+  int32_t v0;         // first vocabulary block of the piece
+  int64_t vocab, stride;
+  int32_t dw_add;
 };
 
-template <bool F16>
-__global__ __launch_bounds__(512) void lm_dx(DxArgs p) {
-  typedef Gemm<2, 4, 4, 2, false, true, F16> G;
-  __shared__ __align__(16) uint16_t s0[G::kStage], s1[G::kStage];
-  const int n_c = (p.w.cb + kTile - 1) / kTile;
-  const int split = blockIdx.x % p.splits, c0 = int(blockIdx.x / p.splits) % n_c * kTile;
-  const int r0 = int(blockIdx.x / p.splits) / n_c * kTile;
-  const int k0 = int(int64_t(p.kb) * split / p.splits), k1 = int(int64_t(p.kb) * (split + 1) / p.splits);
-  typename G::Acc acc = {};
-  G::run(p.g, r0, p.w, c0, k0, k1, k1 == p.kb ? p.tail : 4, p.parts, (lds_t*)s0, (lds_t*)s1, acc);
-  const float unit = F16 ? ldexpf(1.f, -(kGExp + p.exps->w)) : 1.f;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float* out = p.out + split * p.rows * p.ld;
+// The two products with g.  The first dx_jobs workgroups take the tiles of dx and the splits of
+// their sum over the piece, the others the tiles of every worker's table gradient.
+template <bool F16, typename GT, bool SMALL, bool R>
+__global__ __launch_bounds__(SMALL ? 256 : 512) void lm_products(ProductArgs p, GT* grads) {
+  typedef Tile<SMALL, false, true, F16, false, R> Gx;
+  typedef Tile<SMALL, true, true, F16, false, false> Gw;
+  typedef std::conditional_t<F16, float, uint16_t> T;
+  __shared__ __align__(16) uint16_t s0[Gx::kStage], s1[Gx::kStage];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n_c = (p.x.cb + Gx::kB - 1) / Gx::kB;
+  const int64_t in_r = (wave / Gx::kWN) * Gx::kRowsA, in_c = (wave % Gx::kWN) * Gx::kRowsB + (lane & 31);
+  typename Gx::Acc acc = {};
+  const int dx_grid = (p.dx_jobs + 7) / 8 * 8;
+  if (int(blockIdx.x) < dx_grid) {
+    const int job = int(place_of(blockIdx.x, p.dx_jobs));
+    if (job < 0) return;
+    // tiles side by side share g, those above each other the table
+    const int kb = p.g.cb, n_r = (p.g.rb + Gx::kA - 1) / Gx::kA;
+    const int c0 = job % n_c * Gx::kB, r0 = job / n_c % n_r * Gx::kA, split = job / n_c / n_r;
+    const int k0 = int(int64_t(kb) * split / p.splits), k1 = int(int64_t(kb) * (split + 1) / p.splits);
+    Gx::run(p.g, r0, p.w, c0, k0, k1, k1 == kb ? p.dx_tail : 4, p.dx_parts, (lds_t*)s0, (lds_t*)s1, acc);
+    const float unit = F16 ? ldexpf(1.f, -(kGExp + p.exps->w)) : 1.f;
+    const int64_t packed = int64_t(p.g.rb) * kBlk, per = int64_t(p.tw) * kBlk;
 #pragma unroll
-  for (int i = 0; i < G::kFM; ++i)
+    for (int i = 0; i < Gx::kFM; ++i)
 #pragma unroll
-    for (int j = 0; j < G::kFN; ++j) {
-      const int64_t c = int64_t(c0) * kBlk + (wave % G::kWN) * G::kRowsB + j * 32 + (lane & 31);
-      const int64_t r = int64_t(r0) * kBlk + (wave / G::kWN) * G::kRowsA + i * 32;
-      if (c >= p.ld) continue;
+      for (int j = 0; j < Gx::kFN; ++j) {
+        const int64_t c = int64_t(c0) * kBlk + in_c + j * 32, r = int64_t(r0) * kBlk + in_r + i * 32;
+        if (c >= p.ld) continue;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int64_t row = r + acc_row(e, lane);
+          if (row >= packed) continue;
+          const float x = F16 ? acc[i][j][e] * unit : acc[i][j][e];
+          if (p.dx_part != nullptr) {
+            float* o = p.dx_part + (split * packed + row) * p.ld + c;
+            *o = p.dx_add ? *o + x : x;
+          } else if (c < p.dim && row % per < p.rows) {
+            const int64_t w = row / per;
+            put(static_cast<T*>(p.dx) + (w * p.rows + row % per) * p.dim + c,
+                p.info[row].target >= 0 ? x * coef_of(p.scale, p.count, w) : 0.f);
+          }
+        }
+      }
+    return;
+  }
+  const int job = int(place_of(int(blockIdx.x) - dx_grid, p.dw_jobs));
+  if (job < 0) return;
+  const int per = (p.g.cb + Gw::kA - 1) / Gw::kA * n_c, w = job / per;
+  const int c0 = job % per % n_c * Gw::kB, r0 = job % per / n_c * Gw::kA;
+  Gw::run(p.g, r0, p.x, c0, w * p.tw, (w + 1) * p.tw, p.dw_tail, p.dw_parts, (lds_t*)s0, (lds_t*)s1, acc);
+  const float coef = coef_of(p.scale, p.count, w) * p.x_scale;
+  const float unit = F16 ? ldexpf(1.f, -(kGExp + p.exps->x)) : 1.f;
+  GT* out = grads + w * p.stride;
+#pragma unroll
+  for (int i = 0; i < Gw::kFM; ++i)
+#pragma unroll
+    for (int j = 0; j < Gw::kFN; ++j) {
+      const int64_t c = int64_t(c0) * kBlk + in_c + j * 32, r = int64_t(r0) * kBlk + in_r + i * 32;
+      if (c >= p.dim) continue;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const int64_t row = r + acc_row(e, lane);
-        if (row >= p.rows) continue;
-        float* o = out + row * p.ld + c;
-        const float x = F16 ? acc[i][j][e] * unit : acc[i][j][e];
-        *o = p.add ? *o + x : x;
+        const int64_t in = r + acc_row(e, lane), row = int64_t(p.v0) * kBlk + in;
+        if (in >= int64_t(p.g.cb) * kBlk || row >= p.vocab) continue;
+        const float x = (F16 ? acc[i][j][e] * unit : acc[i][j][e]) * coef;
+        GT* o = out + row * p.dim + c;
+        put(o, p.dw_add ? widen(*o) + x : x);
       }
     }
 }
 
+// dx of every row from its splits, times scale / counted, through dropout.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void lm_dx_out(const float* part, int32_t splits, int64_t packed_rows, int64_t ld,
-                                                      const RowInfo* info, int64_t rows, int64_t packed, int32_t dim,
-                                                      T* out, Drop d) {
+                                                      const RowInfo* info, const float* scale, const int32_t* count,
+                                                      int64_t rows, int64_t packed, int32_t dim, T* out, Drop d) {
   const int64_t row = blockIdx.x, w = row / rows, r = w * packed + row % rows;
   const bool on = info[r].target >= 0;
   const uint64_t step = d.on ? step_of(d) : 0;
+  const float coef = coef_of(scale, count, w);
   for (int32_t c = int32_t(threadIdx.x) * 4; c < dim; c += kThreads * 4) {
     float x[4] = {};
     if (on) {
@@ -913,11 +1043,9 @@ __global__ __launch_bounds__(kThreads) void lm_dx_out(const float* part, int32_t
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] += y[e];
       }
-      if (sizeof(T) == 4) {  // g was held without its row's coef
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] *= info[r].coef;
-      }
-      if (d.on) drop<4>(d, step, uint64_t(row) * uint64_t(dim) + uint64_t(c), x);
+      for (int e = 0; e < 4; ++e) x[e] *= coef;
+      if (d.on) drop<4>(d, step, uint64_t(row) * uint64_t(dim) + uint64_t(c), d.scale, x);
     }
     T* o = out + row * dim + c;
     if (c + 4 <= dim) {
@@ -928,45 +1056,6 @@ __global__ __launch_bounds__(kThreads) void lm_dx_out(const float* part, int32_t
         if (c + e < dim) put(o + e, x[e]);
     }
   }
-}
-
-struct DwArgs {
-  Mat g, x;
-  Parts parts;
-  int32_t tw, tail;   // row blocks per worker
-  const Scales* exps;
-  int32_t v0;         // first vocabulary block of the piece
-  int64_t vocab, dim, stride;
-  int32_t add;
-};
-
-template <bool F16, typename GT>
-__global__ __launch_bounds__(512) void lm_dw(DwArgs p, GT* grads) {
-  typedef Gemm<2, 4, 4, 2, true, true, F16> G;
-  __shared__ __align__(16) uint16_t s0[G::kStage], s1[G::kStage];
-  const int n_c = (p.x.cb + kTile - 1) / kTile;
-  const int w = blockIdx.y, c0 = int(blockIdx.x % n_c) * kTile, r0 = int(blockIdx.x / n_c) * kTile;
-  typename G::Acc acc = {};
-  G::run(p.g, r0, p.x, c0, w * p.tw, (w + 1) * p.tw, p.tail, p.parts, (lds_t*)s0, (lds_t*)s1, acc);
-  const float unit = F16 ? ldexpf(1.f, -(kGExp + p.exps->cx)) : 1.f;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  GT* out = grads + w * p.stride;
-#pragma unroll
-  for (int i = 0; i < G::kFM; ++i)
-#pragma unroll
-    for (int j = 0; j < G::kFN; ++j) {
-      const int64_t c = int64_t(c0) * kBlk + (wave % G::kWN) * G::kRowsB + j * 32 + (lane & 31);
-      const int64_t r = int64_t(r0) * kBlk + (wave / G::kWN) * G::kRowsA + i * 32;
-      if (c >= p.dim) continue;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int64_t in = r + acc_row(e, lane), row = int64_t(p.v0) * kBlk + in;
-        if (in >= int64_t(p.g.cb) * kBlk || row >= p.vocab) continue;
-        GT* o = out + row * p.dim + c;
-        const float x = F16 ? acc[i][j][e] * unit : acc[i][j][e];
-        put(o, p.add ? widen(*o) + x : x);
-      }
-    }
 }
 
 // ------------------------------------------------------------------ embedding
@@ -988,7 +1077,7 @@ __global__ __launch_bounds__(64) void lm_embed(const T* table, int64_t vocab, in
       for (int e = 0; e < 8; ++e)
         if (e < n) x[e] = widen(p[e]);
     }
-    if (d.on) drop<8>(d, step_of(d), uint64_t(row) * uint64_t(dim) + uint64_t(c), x);
+    if (d.on) drop<8>(d, step_of(d), uint64_t(row) * uint64_t(dim) + uint64_t(c), d.scale, x);
   }
   T* o = out + row * dim + c;
   if (n == 8) {
@@ -1110,7 +1199,7 @@ __global__ __launch_bounds__(64) void lm_sum(SumArgs p, const T* dout, GT* table
       for (int e = 0; e < 4; ++e)
         if (e < n) x[e] = widen(s[e]);
     }
-    if (d.on) drop<4>(d, step, uint64_t(row) * uint64_t(p.dim) + uint64_t(c), x);
+    if (d.on) drop<4>(d, step, uint64_t(row) * uint64_t(p.dim) + uint64_t(c), d.scale, x);
 #pragma unroll
     for (int e = 0; e < 4; ++e) sum[e] += x[e];
     const uint64_t next = i + 1 < i1 ? keys[i + 1] >> 32 : after;
@@ -1257,142 +1346,185 @@ constexpr Parts kThreeByOne{3, 0x012, 0x000};  // the smallest part first
 int32_t steps_of_last(int64_t n) { return int32_t(ceil_div((n - 1) % kBlk + 1, 16)); }
 
 struct Views {
-  Mat x, cx, w;
-  uint16_t *xp, *cxp, *wp, *g;
+  Mat x, w;
+  uint16_t* g;
   RowInfo* info;
   int32_t* count;
-  float* peak;
+  uint32_t* peak;
   Scales* exps;
   float2* stat;
   float *hit, *dx;
 };
 
-Views views(const psgd_lm_plan* plan, void* workspace, int32_t tb) {
+Views views(const psgd_lm_plan* plan, const void* params, void* workspace, int32_t tb) {
   char* ws = static_cast<char*>(workspace);
   Views v{};
-  v.xp = reinterpret_cast<uint16_t*>(ws + plan->ws_x);
-  v.cxp = reinterpret_cast<uint16_t*>(ws + plan->ws_cx);
-  v.wp = reinterpret_cast<uint16_t*>(ws + plan->ws_w);
-  v.peak = reinterpret_cast<float*>(ws + plan->ws_peak);
-  v.exps = reinterpret_cast<Scales*>(ws + plan->ws_exps);
   v.g = reinterpret_cast<uint16_t*>(ws + plan->ws_g);
   v.info = reinterpret_cast<RowInfo*>(ws + plan->ws_info);
   v.count = reinterpret_cast<int32_t*>(ws + plan->ws_count);
+  v.peak = reinterpret_cast<uint32_t*>(ws + plan->ws_peak);
+  v.exps = reinterpret_cast<Scales*>(ws + plan->ws_exps);
   v.stat = reinterpret_cast<float2*>(ws + plan->ws_stat);
   v.hit = reinterpret_cast<float*>(ws + plan->ws_hit);
   v.dx = reinterpret_cast<float*>(ws + plan->ws_dx);
-  v.x = Mat{v.xp, int64_t(tb) * plan->db * kBlkElems, tb, plan->db};
-  v.cx = Mat{v.cxp, v.x.part, tb, plan->db};
-  v.w = Mat{v.wp, int64_t(plan->vb) * plan->db * kBlkElems, plan->vb, plan->db};
+  v.x = Mat{reinterpret_cast<uint16_t*>(ws + plan->ws_x), int64_t(tb) * plan->db * kBlkElems, tb, plan->db, 0};
+  v.w = plan->direct ? Mat{static_cast<const uint16_t*>(params) + plan->offset, 0, plan->vb, plan->db, int32_t(plan->vocab - 1)}
+                     : Mat{reinterpret_cast<uint16_t*>(ws + plan->ws_w), int64_t(plan->vb) * plan->db * kBlkElems, plan->vb,
+                           plan->db, 0};
   return v;
 }
 
-// The powers of two of float32 operands, x in groups of `rows` rows, and the table.
-psgd_status enqueue_pack(psgd_lm_plan* plan, const Views& v, const void* x, const void* params, int64_t rows, int32_t blocks,
-                         const PackRows& pr, const Drop& d, hipStream_t st) {
-  const Drop none{0, 0, 0, nullptr, 1.f, 0};
-  const PackRows all{};
-  const dim3 gx(unsigned(int64_t(v.x.rb) * v.x.cb)), gw(unsigned(int64_t(v.w.rb) * v.w.cb));
-  const int32_t dim = int32_t(plan->dim);
-  const bool f32 = plan->act == PSGD_F32, grad = pr.count != nullptr;
-  const float* fx = static_cast<const float*>(x);
-  const float* ft = static_cast<const float*>(params) + plan->offset;
-  const int32_t peaks = f32 ? kPeakW + kPeakX : 0, counts = grad ? plan->n_workers : 0;
-  psgd_status s = PSGD_OK;
-  if (peaks + counts > 0)
-    s = launch(plan, kPrep, lm_prep, dim3(unsigned(peaks + counts)), kThreads, st, peaks, ft, plan->vocab * plan->dim, fx,
-               plan->rows * plan->n_workers * plan->dim, v.peak, pr.targets, plan->rows, plan->vocab, v.count);
-  if (s == PSGD_OK && f32)
-    s = launch(plan, kScale, lm_scale, dim3(1), kThreads, st, static_cast<const float*>(v.peak), pr.scale, pr.count,
-               plan->n_workers, d.on ? d.scale : 1.f, v.exps);
-  if (s != PSGD_OK) return s;
-  const PackTo tx{v.xp, f32 && grad ? v.cxp : nullptr, v.x.part, v.exps, 0}, tw{v.wp, nullptr, v.w.part, v.exps, 1};
-  if (f32) {
-    s = launch(plan, kPack, lm_pack<float>, gx, kThreads, st, fx, rows, dim, blocks, v.x.cb, tx, pr, d);
-    if (s != PSGD_OK) return s;
-    return launch(plan, kPack, lm_pack<float>, gw, kThreads, st, ft, plan->vocab, dim, v.w.rb, v.w.cb, tw, all, none);
-  }
-  s = launch(plan, kPack, lm_pack<uint16_t>, gx, kThreads, st, static_cast<const uint16_t*>(x), rows, dim, blocks, v.x.cb, tx, pr, d);
-  if (s != PSGD_OK) return s;
-  return launch(plan, kPack, lm_pack<uint16_t>, gw, kThreads, st, static_cast<const uint16_t*>(params) + plan->offset,
-                plan->vocab, dim, v.w.rb, v.w.cb, tw, all, none);
+const void* table_of(const psgd_lm_plan* plan, const void* params) {
+  return static_cast<const char*>(params) + plan->offset * (plan->act == PSGD_F32 ? 4 : 2);
 }
 
-unsigned score_grid(const ScoreArgs& a) {
-  return unsigned(ceil_div(ceil_div(a.v1 - a.v0, kTile) * ceil_div(a.t1 - a.t0, kTile), 8) * 8);
+// The packed operands: x in groups of `rows` rows, and the table.  count: NULL for the loss.
+psgd_status enqueue_pack(psgd_lm_plan* plan, const Views& v, const void* x, const void* params, int64_t rows, int32_t blocks,
+                         const int64_t* targets, const float* lse, int32_t* count, const Drop& d, hipStream_t st) {
+  const bool f32 = plan->act == PSGD_F32;
+  const void* table = table_of(plan, params);
+  if (f32) {
+    const psgd_status s = launch(plan, kPeak, lm_peak, dim3(kPeakW + kPeakX), kThreads, st, static_cast<const float*>(table),
+                                 plan->vocab * plan->dim, static_cast<const float*>(x), plan->rows * plan->n_workers * plan->dim,
+                                 v.peak);
+    if (s != PSGD_OK) return s;
+  }
+  PackArgs a{x, table, v.x, v.w, rows, blocks, v.x.rb / blocks, plan->n_workers, plan->rows, plan->vocab, int32_t(plan->dim),
+             targets, lse, v.info, count, v.peak, v.exps};
+  if (plan->direct) a.w_to.p = nullptr;
+  const int64_t jobs = int64_t(v.x.rb) * v.x.cb + (plan->direct ? 0 : int64_t(v.w.rb) * v.w.cb) +
+                       (count != nullptr ? plan->n_workers : 0);
+  return launch(plan, kPack, f32 ? lm_pack<float> : lm_pack<uint16_t>, dim3(unsigned(jobs)), kThreads, st, a, d);
 }
+
+unsigned score_grid(const ScoreArgs& a, int tile) {
+  return unsigned(ceil_div(ceil_div(a.v1 - a.v0, tile) * ceil_div(a.t1 - a.t0, tile), 8) * 8);
+}
+
+// Whether the tiles of a v x t blocks problem are the small ones.
+bool small_tiles(int64_t v, int64_t t) { return ceil_div(v, kTile) * ceil_div(t, kTile) < kFewTiles; }
+
+template <int KIND, bool R>
+psgd_status enqueue_scores(psgd_lm_plan* plan, const ScoreArgs& a, bool small, hipStream_t st) {
+  return small ? launch(plan, kScores, lm_scores<KIND, true, R>, dim3(score_grid(a, 1)), 256, st, a)
+               : launch(plan, kScores, lm_scores<KIND, false, R>, dim3(score_grid(a, kTile)), 512, st, a);
+}
+
+// What the products' results are multiplied by; with p = 1 they are zero.
+float x_scale_of(const Drop& d) { return d.on && d.scale > 0.f ? d.scale : 1.f; }
 
 psgd_status enqueue_loss(psgd_lm_plan* plan, const void* x, const void* params, const int64_t* targets, const Drop& d,
                          float* losses, float* lse, float* mean, void* workspace, hipStream_t st) {
   const int64_t rows = plan->rows * plan->n_workers;
-  const Views v = views(plan, workspace, plan->tb);
-  const PackRows pr{targets, nullptr, nullptr, nullptr, v.info, plan->vocab};
-  psgd_status s = enqueue_pack(plan, v, x, params, rows, plan->tb, pr, d, st);
-  const bool f32 = plan->act == PSGD_F32;
-  for (int32_t t0 = 0; s == PSGD_OK && t0 < plan->tb; t0 += plan->chunk) {
-    const ScoreArgs a{v.w, v.x, f32 ? kF32 : kOne, steps_of_last(plan->dim), 0, plan->vb, t0, std::min(plan->tb, t0 + plan->chunk),
-                      plan->vocab, v.info, v.exps, v.stat, v.hit, nullptr, 0};
-    s = launch(plan, kScores, f32 ? lm_scores<kLossF32> : lm_scores<kLossBf16>, dim3(score_grid(a)), 512, st, a);
-    if (s != PSGD_OK) break;
-    const int64_t r0 = int64_t(t0) * kBlk, n = std::min(rows, int64_t(a.t1) * kBlk) - r0;
-    s = launch(plan, kRows, lm_rows, dim3(unsigned(ceil_div(n, 32))), kThreads, st, static_cast<const float2*>(v.stat),
-               int32_t(ceil_div(plan->vb, kTile)), int64_t(a.t1 - t0) * kBlk, static_cast<const RowInfo*>(v.info + r0),
-               static_cast<const float*>(v.hit + r0), n, losses + r0, lse + r0);
-  }
+  const Views v = views(plan, params, workspace, plan->tb);
+  psgd_status s = enqueue_pack(plan, v, x, params, rows, plan->tb, targets, nullptr, nullptr, d, st);
   if (s != PSGD_OK) return s;
+  const bool f32 = plan->act == PSGD_F32, small = plan->loss_small;
+  const int32_t tiles = int32_t(ceil_div(plan->vb, small ? 1 : kTile));
+  // a workgroup per worker does all its rows where that is little
+  const bool one = plan->chunk >= plan->tb && plan->rows * tiles <= kFewStats;
+  for (int32_t t0 = 0; t0 < plan->tb; t0 += plan->chunk) {
+    const ScoreArgs a{v.w, v.x, f32 ? kF32 : kOne, steps_of_last(plan->dim), 0, plan->vb, t0, std::min(plan->tb, t0 + plan->chunk),
+                      plan->vocab, v.info, v.exps, x_scale_of(d), v.stat, v.hit, nullptr, 0};
+    s = f32 ? enqueue_scores<kLossF32, false>(plan, a, small, st)
+            : plan->direct ? enqueue_scores<kLossBf16, true>(plan, a, small, st) : enqueue_scores<kLossBf16, false>(plan, a, small, st);
+    if (s != PSGD_OK) return s;
+    const int64_t r0 = int64_t(t0) * kBlk, n = one ? plan->rows : std::min(rows, int64_t(a.t1) * kBlk) - r0;
+    const RowsArgs b{v.stat, tiles, int64_t(a.t1 - t0) * kBlk, v.info + r0, v.hit + r0, n, losses + r0, lse + r0,
+                     one ? mean : nullptr};
+    s = launch(plan, kRows, lm_rows, dim3(unsigned(one ? plan->n_workers : ceil_div(n, kRowsAt))), kThreads, st, b);
+    if (s != PSGD_OK) return s;
+  }
+  if (one) return PSGD_OK;
   return launch(plan, kMean, lm_mean, dim3(unsigned(plan->n_workers)), kThreads, st, static_cast<const float*>(losses),
                 static_cast<const RowInfo*>(v.info), plan->rows, mean);
+}
+
+template <bool F16, typename GT, bool R>
+psgd_status enqueue_products(psgd_lm_plan* plan, const ProductArgs& a, bool small, GT* grads, hipStream_t st) {
+  const dim3 grid(unsigned(ceil_div(a.dx_jobs, 8) * 8 + ceil_div(a.dw_jobs, 8) * 8));
+  return small ? launch(plan, kProducts, lm_products<F16, GT, true, R>, grid, 256, st, a, grads)
+               : launch(plan, kProducts, lm_products<F16, GT, false, R>, grid, 512, st, a, grads);
 }
 
 psgd_status enqueue_grad(psgd_lm_plan* plan, const void* x, const void* params, const int64_t* targets, const float* lse,
                          const float* scale, const Drop& d, void* dx, void* grads, bool add, void* workspace, hipStream_t st) {
   const int32_t tb = plan->tw * plan->n_workers;
-  const Views v = views(plan, workspace, tb);
-  const PackRows pr{targets, lse, scale, v.count, v.info, plan->vocab};
-  psgd_status s = enqueue_pack(plan, v, x, params, plan->rows, plan->tw, pr, d, st);
+  const Views v = views(plan, params, workspace, tb);
+  psgd_status s = enqueue_pack(plan, v, x, params, plan->rows, plan->tw, targets, lse, v.count, d, st);
   if (s != PSGD_OK) return s;
-  const bool f32 = plan->act == PSGD_F32, f32g = plan->grad == PSGD_F32;
-  const int64_t packed = int64_t(tb) * kBlk, ld = int64_t(plan->db) * kBlk, n_c = ceil_div(plan->db, kTile);
+  const bool f32 = plan->act == PSGD_F32, f32g = plan->grad == PSGD_F32, direct = plan->direct;
+  const float x_scale = x_scale_of(d);
+  // straight into dx: one piece, one split, and no mask to draw again
+  const bool straight = plan->piece >= plan->vb && plan->splits == 1 && !d.on;
+  const int tile = plan->grad_small ? 1 : kTile;
+  const int64_t n_c = ceil_div(plan->db, tile);
   for (int32_t v0 = 0; v0 < plan->vb; v0 += plan->piece) {
     const int32_t v1 = std::min(plan->vb, v0 + plan->piece), n_v = v1 - v0;
     const int64_t g_part = int64_t(tb) * n_v * kBlkElems;
-    const ScoreArgs a{v.w, v.x, f32 ? kF32 : kOne, steps_of_last(plan->dim), v0, v1, 0, tb, plan->vocab, v.info, v.exps, nullptr,
-                      nullptr, v.g, g_part};
-    s = launch(plan, kScores, f32 ? lm_scores<kGradF32> : f32g ? lm_scores<kGradBf16x3> : lm_scores<kGradBf16>,
-               dim3(score_grid(a)), 512, st, a);
+    const ScoreArgs a{v.w, v.x, f32 ? kF32 : kOne, steps_of_last(plan->dim), v0, v1, 0, tb, plan->vocab, v.info, v.exps, x_scale,
+                      nullptr, nullptr, v.g, g_part};
+    const bool small = plan->scores_small;
+    if (f32)
+      s = enqueue_scores<kGradF32, false>(plan, a, small, st);
+    else if (f32g)
+      s = direct ? enqueue_scores<kGradBf16x3, true>(plan, a, small, st) : enqueue_scores<kGradBf16x3, false>(plan, a, small, st);
+    else
+      s = direct ? enqueue_scores<kGradBf16, true>(plan, a, small, st) : enqueue_scores<kGradBf16, false>(plan, a, small, st);
     if (s != PSGD_OK) return s;
-    const Mat g{v.g, g_part, tb, n_v};
-    if (dx != nullptr) {
-      Mat w = v.w;
-      w.p += int64_t(v0) * w.cb * kBlkElems;
-      w.rb = n_v;
-      const int32_t tail = v1 == plan->vb ? steps_of_last(plan->vocab) : 4;
-      const DxArgs b{g, w, f32 ? kF32 : kOne, n_v, tail, plan->splits, v.exps, v.dx, packed, ld, v0 > 0 ? 1 : 0};
-      s = launch(plan, kDx, f32 ? lm_dx<true> : lm_dx<false>, dim3(unsigned(ceil_div(tb, kTile) * n_c * plan->splits)), 512, st, b);
-      if (s != PSGD_OK) return s;
-    }
-    if (grads != nullptr) {
-      const DwArgs b{g, f32 ? v.cx : v.x, !f32g ? kOne : f32 ? kF32 : kThreeByOne, plan->tw, steps_of_last(plan->rows), v.exps, v0,
-                     plan->vocab, plan->dim, plan->worker_stride, add ? 1 : 0};
-      const dim3 grid(unsigned(ceil_div(n_v, kTile) * n_c), unsigned(plan->n_workers));
-      if (f32g)
-        s = launch(plan, kDw, f32 ? lm_dw<true, float> : lm_dw<false, float>, grid, 512, st, b,
-                   static_cast<float*>(grads) + plan->offset);
-      else
-        s = launch(plan, kDw, f32 ? lm_dw<true, uint16_t> : lm_dw<false, uint16_t>, grid, 512, st, b,
-                   static_cast<uint16_t*>(grads) + plan->offset);
-      if (s != PSGD_OK) return s;
-    }
+    Mat w = v.w;
+    w.p += int64_t(v0) * w.cb * kBlkElems;  // as many elements packed or not
+    w.last -= v0 * kBlk;
+    w.rb = n_v;
+    ProductArgs b{};
+    b.g = Mat{v.g, g_part, tb, n_v, 0};
+    b.w = w;
+    b.x = v.x;
+    b.dx_parts = f32 ? kF32 : kOne;
+    b.dw_parts = !f32g ? kOne : f32 ? kF32 : kThreeByOne;
+    b.exps = v.exps;
+    b.scale = scale;
+    b.count = v.count;
+    b.info = v.info;
+    b.dim = plan->dim;
+    b.x_scale = x_scale;
+    b.tw = plan->tw;
+    b.workers = plan->n_workers;
+    b.rows = plan->rows;
+    b.splits = plan->splits;
+    b.dx_jobs = dx != nullptr ? int32_t(ceil_div(tb, tile) * n_c * plan->splits) : 0;
+    b.dx_tail = v1 == plan->vb ? steps_of_last(plan->vocab) : 4;
+    b.dx_part = straight ? nullptr : v.dx;
+    b.dx = dx;
+    b.ld = int64_t(plan->db) * kBlk;
+    b.dx_add = v0 > 0 ? 1 : 0;
+    b.dw_jobs = grads != nullptr ? int32_t(ceil_div(n_v, tile) * n_c * plan->n_workers) : 0;
+    b.dw_tail = steps_of_last(plan->rows);
+    b.v0 = v0;
+    b.vocab = plan->vocab;
+    b.stride = plan->worker_stride;
+    b.dw_add = add ? 1 : 0;
+    float* gf = static_cast<float*>(grads) + plan->offset;
+    uint16_t* gb = static_cast<uint16_t*>(grads) + plan->offset;
+    const bool few = plan->grad_small;
+    if (f32)
+      s = f32g ? enqueue_products<true, float, false>(plan, b, few, gf, st) : enqueue_products<true, uint16_t, false>(plan, b, few, gb, st);
+    else if (direct)
+      s = f32g ? enqueue_products<false, float, true>(plan, b, few, gf, st) : enqueue_products<false, uint16_t, true>(plan, b, few, gb, st);
+    else
+      s = f32g ? enqueue_products<false, float, false>(plan, b, few, gf, st) : enqueue_products<false, uint16_t, false>(plan, b, few, gb, st);
+    if (s != PSGD_OK) return s;
   }
-  if (dx == nullptr) return PSGD_OK;
+  if (dx == nullptr || straight) return PSGD_OK;
   const dim3 grid(unsigned(plan->rows * plan->n_workers));
   const RowInfo* info = v.info;
   const float* part = v.dx;
-  const int64_t per = int64_t(plan->tw) * kBlk;
-  return plan->act == PSGD_F32 ? launch(plan, kDxOut, lm_dx_out<float>, grid, kThreads, st, part, plan->splits, packed, ld, info,
-                                        plan->rows, per, int32_t(plan->dim), static_cast<float*>(dx), d)
-                               : launch(plan, kDxOut, lm_dx_out<uint16_t>, grid, kThreads, st, part, plan->splits, packed, ld,
-                                        info, plan->rows, per, int32_t(plan->dim), static_cast<uint16_t*>(dx), d);
+  const int32_t* count = v.count;
+  const int64_t packed = int64_t(tb) * kBlk, ld = int64_t(plan->db) * kBlk, per = int64_t(plan->tw) * kBlk;
+  return f32 ? launch(plan, kDxOut, lm_dx_out<float>, grid, kThreads, st, part, plan->splits, packed, ld, info, scale, count,
+                      plan->rows, per, int32_t(plan->dim), static_cast<float*>(dx), d)
+             : launch(plan, kDxOut, lm_dx_out<uint16_t>, grid, kThreads, st, part, plan->splits, packed, ld, info, scale, count,
+                      plan->rows, per, int32_t(plan->dim), static_cast<uint16_t*>(dx), d);
 }
 
 int32_t sort_size(int64_t rows) {
@@ -1490,10 +1622,18 @@ extern "C" psgd_status psgd_lm_plan_create(const psgd_layer* layers, int32_t n_l
     // pieces of about equal size, whole tiles each
     const int64_t most = std::max<int64_t>(1, kPieceBytes / int64_t(gp * blk) / tbp / kTile) * kTile;
     plan->piece = int32_t(ceil_div(ceil_div(plan->vb, ceil_div(plan->vb, most)), kTile) * kTile);
-    const int64_t dx_tiles = ceil_div(tbp, kTile) * ceil_div(plan->db, kTile);
-    plan->splits = int32_t(std::max<int64_t>(1, std::min<int64_t>({256 / dx_tiles, 16, plan->vb - (plan->vb - 1) / plan->piece * plan->piece})));
-    const int64_t v_tiles = ceil_div(plan->vb, kTile);
-    plan->chunk = int32_t(std::max<int64_t>(1, kStatBytes / (v_tiles * kTile * kBlk * 8)) * kTile);
+    const int64_t piece = std::min(plan->piece, plan->vb), last = plan->vb - (plan->vb - 1) / plan->piece * plan->piece;
+    plan->direct = act_dtype == PSGD_BF16 && plan->dim % kBlk == 0;
+    plan->loss_small = small_tiles(plan->vb, plan->tb);
+    plan->scores_small = small_tiles(piece, tbp);
+    // the products' tiles: of dx (rows x dim) and of the table gradients (vocabulary x dim)
+    const int64_t cols = ceil_div(plan->db, kTile);
+    plan->grad_small = cols * (ceil_div(tbp, kTile) + n_workers * ceil_div(piece, kTile)) < kFewTiles;
+    // dx's sum over a piece is split where its tiles leave most of the chip idle, kSplitBlocks at least each
+    const int64_t side = plan->grad_small ? 1 : kTile, dx_tiles = ceil_div(tbp, side) * ceil_div(plan->db, side);
+    plan->splits = int32_t(std::max<int64_t>(1, std::min<int64_t>({256 / dx_tiles, 16, last / kSplitBlocks})));
+    const int64_t v_tiles = ceil_div(plan->vb, plan->loss_small ? 1 : kTile);
+    plan->chunk = plan->loss_small ? plan->tb : int32_t(std::max<int64_t>(1, kStatBytes / (v_tiles * kTile * kBlk * 8)) * kTile);
     uint64_t ws = 0;
     auto take = [&](uint64_t bytes) {
       const uint64_t at = ws;
@@ -1501,10 +1641,9 @@ extern "C" psgd_status psgd_lm_plan_create(const psgd_layer* layers, int32_t n_l
       return at;
     };
     plan->ws_x = take(p * uint64_t(tbp) * uint64_t(plan->db) * blk);
-    plan->ws_cx = take(p > 1 ? p * uint64_t(tbp) * uint64_t(plan->db) * blk : 0);
-    plan->ws_peak = take((kPeakW + kPeakX) * sizeof(float));
+    plan->ws_peak = take((kPeakW + kPeakX) * sizeof(uint32_t));
     plan->ws_exps = take(sizeof(Scales));
-    plan->ws_w = take(p * uint64_t(plan->vb) * uint64_t(plan->db) * blk);
+    plan->ws_w = take(plan->direct ? 0 : p * uint64_t(plan->vb) * uint64_t(plan->db) * blk);
     plan->ws_info = take(uint64_t(tbp) * kBlk * sizeof(RowInfo));
     plan->ws_count = take(uint64_t(n_workers) * 4);
     const uint64_t common = ws;

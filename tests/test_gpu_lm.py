@@ -23,9 +23,10 @@ U = 2.0 ** -24
 HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
 CODE = {"f32": psgd.PSGD_F32, "bf16": psgd.PSGD_BF16}
 TYPES = [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16")]
-# (vocab, dim, workers, rows): single ones, block and tile borders one off, several tiles each way
+# (vocab, dim, workers, rows): single ones, block and tile borders one off, several tiles each way,
+# and sizes for the large tiles, with the table packed and read as it is (dim a multiple of 64)
 SIZES = [(1, 1, 1, 1), (2, 8, 1, 1), (3, 64, 4, 1), (63, 7, 2, 3), (64, 64, 1, 64), (65, 65, 3, 65), (257, 130, 2, 129),
-         (1001, 72, 4, 5), (512, 192, 1, 256), (513, 650, 1, 300), (2049, 33, 1, 700)]
+         (1001, 72, 4, 5), (512, 192, 1, 256), (513, 650, 1, 300), (2049, 33, 1, 700), (12345, 650, 1, 700), (9001, 640, 2, 300)]
 
 
 @pytest.fixture(scope="module")
