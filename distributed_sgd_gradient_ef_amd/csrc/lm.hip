@@ -19,8 +19,8 @@
 //              into the gradient slices
 //   lm_dx_out  the sum of g T's splits, through dropout
 //   lm_embed   rows of the table
-//   lm_sort, lm_merge  every worker's (token, row) pairs in order
-//   lm_zero, lm_sum, lm_join  the table gradient from runs of these pairs
+//   lm_sort, lm_merge  every worker's (token, row) pairs in order; zeroes tables on the side
+//   lm_sum, lm_join  the table gradient from runs of these pairs
 //   lm_dropout
 //
 // No kernel waits for another workgroup, no atomics, no state is kept between calls.
@@ -52,15 +52,17 @@ constexpr int64_t kFewStats = 16384;  // maxima and sums of a worker that one wo
 constexpr int kSplitBlocks = 8;    // vocabulary blocks of a split of lm_products' dx, at least
 constexpr int64_t kPieceBytes = int64_t(512) << 20;  // g of one piece of the vocabulary
 constexpr int64_t kStatBytes = int64_t(64) << 20;    // maxima and sums of one chunk of rows
-constexpr int kSortMax = 4096;     // pairs sorted by one workgroup
+constexpr int kSortMax = 1024;     // pairs sorted by one workgroup
 constexpr int kSortThreads = 512;
-constexpr int kRun = 32;           // sorted pairs summed by one wave
+constexpr int kRun = 16;           // sorted pairs summed by one wave ...
+constexpr int kRunLoads = 8;       // ... whose rows are loaded so many at a time
+constexpr int kZeroUnits = 4;      // 16-byte stores of a thread that zeroes
 
 enum KernelId {
-  kPeak = 0, kPack, kScores, kRows, kMean, kProducts, kDxOut, kEmbed, kSort, kMerge, kZero, kSum, kJoin, kDrop, kNumK
+  kPeak = 0, kPack, kScores, kRows, kMean, kProducts, kDxOut, kEmbed, kSort, kMerge, kSum, kJoin, kNumK
 };
 const char* const kNames[kNumK] = {"lm_peak", "lm_pack", "lm_scores", "lm_rows", "lm_mean", "lm_products", "lm_dx_out", "lm_embed",
-                                   "lm_sort", "lm_merge", "lm_zero", "lm_sum", "lm_join", "lm_dropout"};
+                                   "lm_sort", "lm_merge", "lm_sum", "lm_join"};
 
 }  // namespace lm
 }  // namespace psgd
@@ -205,7 +207,8 @@ typedef __attribute__((address_space(3))) uint16_t lds_t;
 // WM FM x WN FN pieces of 32 x 32, each wave FM x FN of them.  TA, TB: the operand's
 // contraction runs along its blocks' rows instead of along their columns; it is then read
 // from LDS with the transposing load.  RA, RB: the operand is not packed.  Two LDS stages: the
-// next blocks go from memory straight into one while the matrix cores work on the other.
+// blocks of the next step are on their way from memory straight into one while the matrix
+// cores work on the other (three and four stages of small tiles ran alike).
 template <int WM, int WN, int FM, int FN, bool TA, bool TB, bool F16, bool RA, bool RB>
 struct Gemm {
   static_assert((FM == 4 && FN == 2) || (FM == 1 && FN == 1), "what the LDS reads are written out for");
@@ -213,6 +216,7 @@ struct Gemm {
   static constexpr int kA = WM * FM / 2, kB = WN * FN / 2;  // blocks of the tile's sides
   static constexpr int kPer = kBlkElems / 8 / kT;           // 16-byte pieces of a block per thread
   static constexpr int kStage = (kA + kB) * kBlkElems;
+  static constexpr int kLds = 2 * kStage;
   static constexpr int kRowsA = FM * 32, kRowsB = FN * 32;  // of a wave
   typedef f16v Acc[FM][FN];
   static constexpr int kFM = FM, kFN = FN, kWN = WN, kWM = WM;
@@ -389,7 +393,7 @@ struct Gemm {
   }
 
   static __device__ __forceinline__ void sweep(const Mat& a, int a0, const Mat& b, int b0, int k0, int k1, int tail, const Parts& parts,
-                                                 lds_t* s0, lds_t* s1, Acc& acc) {
+                                               lds_t* sm, Acc& acc) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wa = (wave / WN) * FM, wb = (wave % WN) * FN;
     int k = k0;
@@ -428,10 +432,15 @@ struct Gemm {
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
         }
     };
-    int at = k0;  // the block that `cur` holds
+    const int steps = int(parts.n) * (k1 - k0);
+    stage(sm);
+    int at = k0;  // the block of the current step
     auto step = [&](const lds_t* cur, lds_t* next, bool more) {
       __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's part of `cur` is there
-      __syncthreads();                     // everybody's is, and nobody reads `next` any more
+      // everybody's is, and nobody reads `next` any more: reads of LDS end with a wait of their own
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
       if (more) stage(next);
       __builtin_amdgcn_sched_barrier(0);
       const uint32_t base = uint32_t(uintptr_t(cur));
@@ -448,11 +457,10 @@ struct Gemm {
       if (n > 3) multiply(base, ca, cb, std::integral_constant<int, 3>());
       __builtin_amdgcn_sched_barrier(0);
     };
-    stage(s0);
-    for (int left = int(parts.n) * (k1 - k0);;) {
-      step(s0, s1, left > 1);
+    for (int left = steps;;) {
+      step(sm, sm + kStage, left > 1);
       if (--left == 0) break;
-      step(s1, s0, left > 1);
+      step(sm + kStage, sm, left > 1);
       if (--left == 0) break;
     }
     __syncthreads();
@@ -461,12 +469,12 @@ struct Gemm {
   // The whole product.  With fp16 parts the products with a low part come first and are
   // scaled back before the product of the high parts is added.
   static __device__ __forceinline__ void run(const Mat& a, int a0, const Mat& b, int b0, int k0, int k1, int tail,
-                                             const Parts& parts, lds_t* s0, lds_t* s1, Acc& acc) {
+                                             const Parts& parts, lds_t* sm, Acc& acc) {
     if constexpr (!F16) {
-      sweep(a, a0, b, b0, k0, k1, tail, parts, s0, s1, acc);
+      sweep(a, a0, b, b0, k0, k1, tail, parts, sm, acc);
     } else {
       if (parts.n > 1) {
-        sweep(a, a0, b, b0, k0, k1, tail, Parts{parts.n - 1, parts.a, parts.b}, s0, s1, acc);
+        sweep(a, a0, b, b0, k0, k1, tail, Parts{parts.n - 1, parts.a, parts.b}, sm, acc);
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -474,7 +482,7 @@ struct Gemm {
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] *= 1.f / 2048.f;
       }
-      sweep(a, a0, b, b0, k0, k1, tail, Parts{1, 0, 0}, s0, s1, acc);
+      sweep(a, a0, b, b0, k0, k1, tail, Parts{1, 0, 0}, sm, acc);
     }
   }
 };
@@ -723,12 +731,12 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_scores(ScoreArgs p) {
   constexpr bool kF16 = KIND == kLossF32 || KIND == kGradF32;
   typedef Tile<SMALL, false, false, kF16, R, false> G;
   constexpr int kRows = G::kB * kBlk;  // of the tile
-  __shared__ __align__(16) uint16_t s0[G::kStage], s1[G::kStage];
+  __shared__ __align__(16) uint16_t sm[G::kLds];
   int vt, tt;
   if (!tile_at(blockIdx.x, (p.v1 - p.v0 + G::kA - 1) / G::kA, (p.t1 - p.t0 + G::kB - 1) / G::kB, kGroup / G::kB, vt, tt)) return;
   const int v0 = p.v0 + vt * G::kA, t0 = p.t0 + tt * G::kB;
   typename G::Acc acc = {};
-  G::run(p.w, v0, p.x, t0, 0, p.w.cb, p.tail, p.parts, (lds_t*)s0, (lds_t*)s1, acc);
+  G::run(p.w, v0, p.x, t0, 0, p.w.cb, p.tail, p.parts, (lds_t*)sm, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / G::kWN, wn = wave % G::kWN;
   const int64_t word0 = int64_t(v0) * kBlk + wm * G::kRowsA;  // of this wave
   const int n_words = int(min(int64_t(G::kRowsA), p.vocab - word0));  // may be negative
@@ -736,7 +744,7 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_scores(ScoreArgs p) {
   if constexpr (kF16) unit = ldexpf(unit, -(p.exps->x + p.exps->w));
   const float c = fmaxf(kLog2e * unit, FLT_MIN);
   if constexpr (KIND == kLossBf16 || KIND == kLossF32) {
-    float2* joined = reinterpret_cast<float2*>(s0);  // the main loop ends in a barrier: its LDS is free
+    float2* joined = reinterpret_cast<float2*>(sm);  // the main loop ends in a barrier: its LDS is free
 #pragma unroll
     for (int j = 0; j < G::kFN; ++j) {
       const int at = wn * G::kRowsB + j * 32 + (lane & 31);  // the row's place in the tile
@@ -788,10 +796,9 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_scores(ScoreArgs p) {
     }
   } else {
     constexpr int kParts = KIND == kGradBf16 ? 1 : KIND == kGradF32 ? 2 : 3;
-    constexpr int kInStage = G::kA + G::kB;  // blocks of a stage
-    static_assert(2 * kInStage >= G::kA * G::kB, "the tile's blocks of g, one part of them, fit the two stages");
+    static_assert(G::kLds >= G::kA * G::kB * kBlkElems, "the tile's blocks of g, one part of them, fit LDS");
     float g[G::kFM][G::kFN][16];
-    auto place = [&](int block) { return (block < kInStage ? s0 : s1) + block % kInStage * kBlkElems; };
+    auto place = [&](int block) { return sm + block * kBlkElems; };
 #pragma unroll
     for (int j = 0; j < G::kFN; ++j) {
       const int at = wn * G::kRowsB + j * 32 + (lane & 31);
@@ -872,21 +879,21 @@ struct RowsArgs {
   int64_t rows;
   float *losses, *lse;
   float* mean;          // of each workgroup's rows, or NULL
+  int32_t at;           // rows at a time: 256 or less, a power of two
 };
 
-// lse and loss of rows from their `tiles` maxima and sums: kRowsAt rows at a time per
-// workgroup, the threads kRowsAt apart share a row's tiles.  With `mean`, a workgroup takes
-// all of a worker's `rows` rows and leaves their mean.
-constexpr int kRowsAt = 16;
+// lse and loss of rows from their `tiles` maxima and sums: `at` rows at a time per workgroup,
+// the threads `at` apart share a row's tiles.  With `mean`, a workgroup takes all of a
+// worker's `rows` rows and leaves their mean.
 
 __global__ __launch_bounds__(kThreads) void lm_rows(RowsArgs p) {
   __shared__ float2 sm[kThreads];
   __shared__ double sums[kThreads / 64];
-  const int r = threadIdx.x % kRowsAt, part = threadIdx.x / kRowsAt;
-  const int64_t first = p.mean != nullptr ? blockIdx.x * p.rows : int64_t(blockIdx.x) * kRowsAt;
-  const int64_t end = p.mean != nullptr ? first + p.rows : min(p.rows, first + kRowsAt);
+  const int r = threadIdx.x % p.at, part = threadIdx.x / p.at, parts = kThreads / p.at;
+  const int64_t first = p.mean != nullptr ? blockIdx.x * p.rows : int64_t(blockIdx.x) * p.at;
+  const int64_t end = p.mean != nullptr ? first + p.rows : min(p.rows, first + p.at);
   double sum = 0.0, n = 0.0;
-  for (int64_t row0 = first; row0 < end; row0 += kRowsAt) {
+  for (int64_t row0 = first; row0 < end; row0 += p.at) {
     const int64_t row = row0 + r;
     float m = -INFINITY, s = 0.f;
     auto join = [&](const float2& a) {
@@ -896,12 +903,12 @@ __global__ __launch_bounds__(kThreads) void lm_rows(RowsArgs p) {
     };
     if (row < end) {
 #pragma unroll 4
-      for (int i = part; i < p.tiles; i += kThreads / kRowsAt) join(p.stat[i * p.ld + row]);
+      for (int i = part; i < p.tiles; i += parts) join(p.stat[i * p.ld + row]);
     }
     sm[threadIdx.x] = make_float2(m, s);
     __syncthreads();
     if (part == 0 && row < end) {
-      for (int i = 1; i < kThreads / kRowsAt; ++i) join(sm[i * kRowsAt + r]);
+      for (int i = 1; i < parts; ++i) join(sm[i * p.at + r]);
       const bool on = p.info[row].target >= 0;
       const float l = float((double(m) + double(log2f(s))) / double(kLog2e)), loss = on ? l - p.hit[row] : 0.f;
       p.lse[row] = on ? l : 0.f;
@@ -962,7 +969,7 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_products(ProductArgs p, 
   typedef Tile<SMALL, false, true, F16, false, R> Gx;
   typedef Tile<SMALL, true, true, F16, false, false> Gw;
   typedef std::conditional_t<F16, float, uint16_t> T;
-  __shared__ __align__(16) uint16_t s0[Gx::kStage], s1[Gx::kStage];
+  __shared__ __align__(16) uint16_t sm[Gx::kLds];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n_c = (p.x.cb + Gx::kB - 1) / Gx::kB;
   const int64_t in_r = (wave / Gx::kWN) * Gx::kRowsA, in_c = (wave % Gx::kWN) * Gx::kRowsB + (lane & 31);
   typename Gx::Acc acc = {};
@@ -974,7 +981,7 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_products(ProductArgs p, 
     const int kb = p.g.cb, n_r = (p.g.rb + Gx::kA - 1) / Gx::kA;
     const int c0 = job % n_c * Gx::kB, r0 = job / n_c % n_r * Gx::kA, split = job / n_c / n_r;
     const int k0 = int(int64_t(kb) * split / p.splits), k1 = int(int64_t(kb) * (split + 1) / p.splits);
-    Gx::run(p.g, r0, p.w, c0, k0, k1, k1 == kb ? p.dx_tail : 4, p.dx_parts, (lds_t*)s0, (lds_t*)s1, acc);
+    Gx::run(p.g, r0, p.w, c0, k0, k1, k1 == kb ? p.dx_tail : 4, p.dx_parts, (lds_t*)sm, acc);
     const float unit = F16 ? ldexpf(1.f, -(kGExp + p.exps->w)) : 1.f;
     const int64_t packed = int64_t(p.g.rb) * kBlk, per = int64_t(p.tw) * kBlk;
 #pragma unroll
@@ -982,20 +989,24 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_products(ProductArgs p, 
 #pragma unroll
       for (int j = 0; j < Gx::kFN; ++j) {
         const int64_t c = int64_t(c0) * kBlk + in_c + j * 32, r = int64_t(r0) * kBlk + in_r + i * 32;
-        if (c >= p.ld) continue;
+        if (r >= packed || c >= p.ld) continue;  // packed rows and ld are whole pieces
+        if (p.dx_part != nullptr) {
+          float* o = p.dx_part + (split * packed + r) * p.ld + c;
+          float old[16] = {};
+          if (p.dx_add) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) old[e] = o[acc_row(e, lane) * p.ld];
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[acc_row(e, lane) * p.ld] = old[e] + acc[i][j][e] * unit;
+          continue;
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int64_t row = r + acc_row(e, lane);
-          if (row >= packed) continue;
-          const float x = F16 ? acc[i][j][e] * unit : acc[i][j][e];
-          if (p.dx_part != nullptr) {
-            float* o = p.dx_part + (split * packed + row) * p.ld + c;
-            *o = p.dx_add ? *o + x : x;
-          } else if (c < p.dim && row % per < p.rows) {
-            const int64_t w = row / per;
+          const int64_t row = r + acc_row(e, lane), w = row / per;
+          if (c < p.dim && row % per < p.rows)
             put(static_cast<T*>(p.dx) + (w * p.rows + row % per) * p.dim + c,
-                p.info[row].target >= 0 ? x * coef_of(p.scale, p.count, w) : 0.f);
-          }
+                p.info[row].target >= 0 ? acc[i][j][e] * unit * coef_of(p.scale, p.count, w) : 0.f);
         }
       }
     return;
@@ -1004,7 +1015,7 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_products(ProductArgs p, 
   if (job < 0) return;
   const int per = (p.g.cb + Gw::kA - 1) / Gw::kA * n_c, w = job / per;
   const int c0 = job % per % n_c * Gw::kB, r0 = job % per / n_c * Gw::kA;
-  Gw::run(p.g, r0, p.x, c0, w * p.tw, (w + 1) * p.tw, p.dw_tail, p.dw_parts, (lds_t*)s0, (lds_t*)s1, acc);
+  Gw::run(p.g, r0, p.x, c0, w * p.tw, (w + 1) * p.tw, p.dw_tail, p.dw_parts, (lds_t*)sm, acc);
   const float coef = coef_of(p.scale, p.count, w) * p.x_scale;
   const float unit = F16 ? ldexpf(1.f, -(kGExp + p.exps->x)) : 1.f;
   GT* out = grads + w * p.stride;
@@ -1012,15 +1023,29 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_products(ProductArgs p, 
   for (int i = 0; i < Gw::kFM; ++i)
 #pragma unroll
     for (int j = 0; j < Gw::kFN; ++j) {
-      const int64_t c = int64_t(c0) * kBlk + in_c + j * 32, r = int64_t(r0) * kBlk + in_r + i * 32;
-      if (c >= p.dim) continue;
+      const int64_t c = int64_t(c0) * kBlk + in_c + j * 32, in = int64_t(r0) * kBlk + in_r + i * 32;
+      const int64_t row = int64_t(p.v0) * kBlk + in, n = min(p.vocab - row, int64_t(p.g.cb) * kBlk - in);  // words left
+      if (c >= p.dim || n <= 0) continue;
+      GT* o = out + row * p.dim + c;
+      // a whole piece's old values are loaded together
+      float old[16] = {};
+      if (p.dw_add) {
+        if (n >= 32) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int64_t in = r + acc_row(e, lane), row = int64_t(p.v0) * kBlk + in;
-        if (in >= int64_t(p.g.cb) * kBlk || row >= p.vocab) continue;
-        const float x = (F16 ? acc[i][j][e] * unit : acc[i][j][e]) * coef;
-        GT* o = out + row * p.dim + c;
-        put(o, p.dw_add ? widen(*o) + x : x);
+          for (int e = 0; e < 16; ++e) old[e] = widen(o[acc_row(e, lane) * p.dim]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (acc_row(e, lane) < n) old[e] = widen(o[acc_row(e, lane) * p.dim]);
+        }
+      }
+      if (n >= 32) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) put(o + acc_row(e, lane) * p.dim, old[e] + acc[i][j][e] * unit * coef);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (acc_row(e, lane) < n) put(o + acc_row(e, lane) * p.dim, old[e] + acc[i][j][e] * unit * coef);
       }
     }
 }
@@ -1092,11 +1117,30 @@ __global__ __launch_bounds__(64) void lm_embed(const T* table, int64_t vocab, in
 // A pair is token << 32 | row; pairs of tokens outside the vocabulary come last.
 constexpr uint64_t kNoToken = 0xffffffffull;
 
-// One chunk of a worker's pairs, sorted (bitonic: a fixed network on distinct keys).
+// The first workgroups each sort one chunk of a worker's pairs (bitonic: a fixed network on
+// distinct keys); the others zero the tables that are not added to.
+template <typename GT>
 __global__ __launch_bounds__(kSortThreads) void lm_sort(const int64_t* tokens, int64_t rows, int64_t vocab, int32_t size,
-                                                        uint64_t* keys) {
+                                                        uint64_t* keys, int32_t chunks, int32_t workers, GT* table, int64_t n,
+                                                        int64_t stride) {
   __shared__ uint64_t sm[kSortMax];
-  const int64_t at = int64_t(blockIdx.y) * rows, t0 = int64_t(blockIdx.x) * size;
+  if (int(blockIdx.x) >= chunks * workers) {
+    constexpr int kV = 16 / sizeof(GT);
+    const int64_t job = int64_t(blockIdx.x) - chunks * workers;
+    const int64_t per = (n + kSortThreads * kZeroUnits * kV - 1) / (kSortThreads * kZeroUnits * kV);
+    GT* t = table + job / per * stride;
+#pragma unroll
+    for (int u = 0; u < kZeroUnits; ++u) {
+      const int64_t i = ((job % per * kZeroUnits + u) * kSortThreads + threadIdx.x) * kV;
+      if (i + kV <= n) {
+        __builtin_nontemporal_store(u4v{}, reinterpret_cast<u4v*>(t + i));
+      } else {
+        for (int64_t e = i; e < n; ++e) t[e] = GT(0);
+      }
+    }
+    return;
+  }
+  const int64_t at = int64_t(blockIdx.x) / chunks * rows, t0 = int64_t(blockIdx.x) % chunks * size;
   for (int i = threadIdx.x; i < size; i += kSortThreads) {
     uint64_t key = ~0ull;
     if (t0 + i < rows) {
@@ -1138,30 +1182,38 @@ __global__ __launch_bounds__(kThreads) void lm_merge(const uint64_t* src, uint64
   dst[int64_t(blockIdx.y) * rows + (right ? i - mid : i - pair) + pair + (lo - from)] = key;
 }
 
-template <typename GT>
-__global__ __launch_bounds__(kThreads) void lm_zero(GT* table, int64_t n, int64_t stride) {
-  constexpr int kV = 16 / sizeof(GT);
-  const int64_t i = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * kV;
-  GT* p = table + int64_t(blockIdx.y) * stride + i;
-  if (i + kV <= n) {
-    *reinterpret_cast<u4v*>(p) = u4v{};
+// Columns c to c + 3 of a row, without a branch around the load, so that the loads of several
+// rows are under way together.  WIDE (dim >= 4): the last lane's columns come from the row's
+// last four.
+template <bool WIDE, typename T>
+__device__ __forceinline__ void load_row(const T* row, int32_t c, int32_t dim, float (&x)[4]) {
+  if constexpr (WIDE) {
+    const int32_t from = min(c, dim - 4), skip = c - from;
+    float v[4];
+    load<4>(row + from, v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = v[e];
+#pragma unroll
+      for (int k = 1; e + k < 4; ++k) x[e] = skip == k ? v[e + k] : x[e];
+    }
   } else {
-    for (int64_t e = i; e < n; ++e) p[e - i] = GT(0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = widen(row[min(c + e, dim - 1)]);
   }
 }
 
 template <typename GT>
-__device__ __forceinline__ void write_row(GT* o, int n, bool add, float (&x)[4]) {
-  if (n == 4) {
-    float y[4] = {};
-    if (add) load<4>(o, y);
+__device__ __forceinline__ void write_row(GT* o, int n, const float (&old)[4], const float (&x)[4]) {
+  float y[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] += x[e];
+  for (int e = 0; e < 4; ++e) y[e] = old[e] + x[e];
+  if (n == 4) {
     store<4>(o, y);
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (e < n) put(o + e, (add ? widen(o[e]) : 0.f) + x[e]);
+      if (e < n) put(o + e, y[e]);
   }
 }
 
@@ -1173,9 +1225,16 @@ struct SumArgs {
   float* part;  // [worker][run][2][dpad]: a token's sum from its earlier run on, and the start of one that goes on
 };
 
+// A pair that every lane reads, as a scalar.
+__device__ __forceinline__ uint64_t pair_at(const uint64_t* keys, int64_t i) {
+  const uint64_t k = keys[i];
+  return uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(k >> 32)))) << 32 |
+         uint32_t(__builtin_amdgcn_readfirstlane(int(uint32_t(k))));
+}
+
 // kRun sorted pairs x 256 columns per wave, summed in their order.  A token whose pairs lie
 // in one run is written here; the others leave a part per run for lm_join.
-template <typename T, typename GT>
+template <typename T, typename GT, bool WIDE>
 __global__ __launch_bounds__(64) void lm_sum(SumArgs p, const T* dout, GT* table, Drop d) {
   const int64_t w = blockIdx.z, run = blockIdx.x, i0 = run * kRun, i1 = min(p.rows, i0 + kRun);
   const int32_t c = (int32_t(blockIdx.y) * 64 + int32_t(threadIdx.x)) * 4;
@@ -1183,79 +1242,140 @@ __global__ __launch_bounds__(64) void lm_sum(SumArgs p, const T* dout, GT* table
   const int n = min(4, p.dim - c);
   if (n <= 0) return;
   const uint64_t step = d.on ? step_of(d) : 0;
-  const uint64_t before = i0 > 0 ? keys[i0 - 1] >> 32 : ~0ull, after = i1 < p.rows ? keys[i1] >> 32 : ~0ull;
+  const uint64_t before = i0 > 0 ? pair_at(keys, i0 - 1) >> 32 : ~0ull, after = i1 < p.rows ? pair_at(keys, i1) >> 32 : ~0ull;
   float* part = p.part + (w * p.n_runs + run) * 2 * p.dpad + c;
+  table += w * p.stride;
   float sum[4] = {};
-  for (int64_t i = i0; i < i1; ++i) {
-    const uint64_t key = keys[i], token = key >> 32;
-    if (token == kNoToken) break;
-    const int64_t row = w * p.rows + int64_t(key & 0xffffffffu);
-    const T* s = dout + row * p.dim + c;
-    float x[4] = {};
-    if (n == 4) {
-      load<4>(s, x);
-    } else {
+  for (int64_t i = i0; i < i1; i += kRunLoads) {
+    uint64_t key[kRunLoads + 1];
+    float x[kRunLoads][4], old[kRunLoads][4] = {};
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e < n) x[e] = widen(s[e]);
-    }
-    if (d.on) drop<4>(d, step, uint64_t(row) * uint64_t(p.dim) + uint64_t(c), d.scale, x);
+    for (int u = 0; u <= kRunLoads; ++u) key[u] = pair_at(keys, min(i + u, i1 - 1));
+    // a token past the run or the vocabulary is loaded from the first row and left out below
+    auto real = [&](int u) { return i + u < i1 && key[u] >> 32 != kNoToken; };
+    auto row = [&](int u) { return table + (real(u) ? int64_t(key[u] >> 32) : 0) * p.dim; };
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] += x[e];
-    const uint64_t next = i + 1 < i1 ? keys[i + 1] >> 32 : after;
-    if (next == token && i + 1 < i1) continue;
-    // the token's pairs of this run end here
-    const bool from_before = token == before, goes_on = next == token;
-    if (from_before || goes_on) {
-      store<4>(part + (from_before ? 0 : p.dpad), sum);
-    } else {
-      write_row(table + w * p.stride + int64_t(token) * p.dim + c, n, p.add != 0, sum);
+    for (int u = 0; u < kRunLoads; ++u)
+      load_row<WIDE>(dout + (w * p.rows + int64_t(key[u] & 0xffffffffu)) * p.dim, c, p.dim, x[u]);
+    if (p.add) {
+#pragma unroll
+      for (int u = 0; u < kRunLoads; ++u) load_row<WIDE>(row(u), c, p.dim, old[u]);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] = 0.f;
+    for (int u = 0; u < kRunLoads; ++u) {
+      if (!real(u)) continue;
+      const int64_t t = w * p.rows + int64_t(key[u] & 0xffffffffu);
+      if (d.on) drop<4>(d, step, uint64_t(t) * uint64_t(p.dim) + uint64_t(c), d.scale, x[u]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += x[u][e];
+      const uint64_t token = key[u] >> 32, next = i + u + 1 < i1 ? key[u + 1] >> 32 : ~0ull;
+      if (token == next) continue;
+      // the token's pairs of this run end here
+      if (token == before || (i + u + 1 == i1 && token == after)) {
+        store<4>(part + (token == before ? 0 : p.dpad), sum);
+      } else {
+        write_row(row(u) + c, n, old[u], sum);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] = 0.f;
+    }
   }
 }
 
-// The tokens whose pairs start in this run and go on after it.
-template <typename GT>
+// The tokens whose pairs start in this run and go on after it: as far as the runs begin with
+// them; kRunLoads runs are looked at together.
+template <typename GT, bool WIDE>
 __global__ __launch_bounds__(64) void lm_join(SumArgs p, GT* table) {
   const int64_t w = blockIdx.z, run = blockIdx.x, i0 = run * kRun, i1 = i0 + kRun;
   const uint64_t* keys = p.keys + w * p.rows;
   if (i1 >= p.rows) return;
-  const uint64_t token = keys[i1 - 1] >> 32;
-  if (token == kNoToken || keys[i1] >> 32 != token || (i0 > 0 && keys[i0 - 1] >> 32 == token)) return;
+  const uint64_t token = pair_at(keys, i1 - 1) >> 32;
+  if (token == kNoToken || pair_at(keys, i1) >> 32 != token || (i0 > 0 && pair_at(keys, i0 - 1) >> 32 == token)) return;
   const int32_t c = (int32_t(blockIdx.y) * 64 + int32_t(threadIdx.x)) * 4;
   const int n = min(4, p.dim - c);
   if (n <= 0) return;
-  const float* part = p.part + (w * p.n_runs + run) * 2 * p.dpad + c;
-  float sum[4];
-  load<4>(part + p.dpad, sum);
-  for (int64_t i = i1; i < p.rows && keys[i] >> 32 == token; i += kRun) {
-    part += 2 * p.dpad;
-    float x[4];
-    load<4>(part, x);
+  const float* part = p.part + w * p.n_runs * 2 * p.dpad + c;
+  table += w * p.stride + int64_t(token) * p.dim;
+  float sum[4], old[4] = {};
+  load<4>(part + (run * 2 + 1) * p.dpad, sum);
+  if (p.add) load_row<WIDE>(table, c, p.dim, old);
+  bool goes_on = true;
+  for (int64_t r = run + 1; goes_on; r += kRunLoads) {
+    uint64_t key[kRunLoads];
+    float x[kRunLoads][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] += x[e];
+    for (int u = 0; u < kRunLoads; ++u) {
+      const int64_t at = min(r + u, int64_t(p.n_runs) - 1);
+      key[u] = pair_at(keys, at * kRun);
+      load<4>(part + at * 2 * p.dpad, x[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kRunLoads; ++u) {
+      goes_on = goes_on && r + u < p.n_runs && key[u] >> 32 == token;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += goes_on ? x[u][e] : 0.f;
+    }
   }
-  write_row(table + w * p.stride + int64_t(token) * p.dim + c, n, p.add != 0, sum);
+  write_row(table + c, n, old, sum);
 }
 
 // ------------------------------------------------------------------ dropout
-template <typename T>
-__global__ __launch_bounds__(kThreads) void lm_dropout(const T* x, int64_t xs, const T* residual, int64_t rs, T* out,
-                                                       int64_t os, int64_t n, int64_t cols, Drop d) {
-  const int64_t group = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-  if (group * 4 >= n) return;
-  uint32_t w[4];
-  philox(uint64_t(group), step_of(d), d.key0, d.key1, w);
-  int64_t r = group * 4 / cols, c = group * 4 % cols;
+// n / d for 32-bit n: the multiplier and shifts of Granlund and Montgomery ("Division by
+// invariant integers using multiplication", 1994).
+struct Div {
+  uint64_t d;
+  uint32_t mul, s1, s2;
+};
+
+__device__ __forceinline__ uint64_t divide(uint64_t n, const Div& v) {
+  if ((n | v.d) >> 32) return n / v.d;
+  const uint32_t x = uint32_t(n), t = __umulhi(v.mul, x);
+  return (t + ((x - t) >> v.s1)) >> v.s2;
+}
+
+struct DropArgs {
+  const void *x, *residual;
+  void* out;
+  int64_t xs, rs, os;  // strides
+  int64_t n, cols;
+  Div groups;  // VEC: groups of N entries per row; otherwise cols
+};
+
+// N consecutive entries per thread.  VEC: they lie in one row (cols is a multiple of N).
+template <typename T, int N, bool VEC>
+__global__ __launch_bounds__(kThreads) void lm_dropout(DropArgs p, Drop d) {
+  const int64_t group = int64_t(blockIdx.x) * kThreads + threadIdx.x, i = group * N;
+  if (i >= p.n) return;
+  const T* x = static_cast<const T*>(p.x);
+  const T* residual = static_cast<const T*>(p.residual);
+  T* out = static_cast<T*>(p.out);
+  const uint64_t step = step_of(d);
+  if constexpr (VEC) {
+    const int64_t r = int64_t(divide(uint64_t(group), p.groups)), c = i - r * p.cols;
+    float v[N], y[N] = {};
+    load<N>(x + r * p.xs + c, v);
+    if (residual != nullptr) load<N>(residual + r * p.rs + c, y);
+    drop<N>(d, step, uint64_t(i), d.scale, v);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (group * 4 + e >= n) break;
-    float y = uint64_t(w[e]) >= d.keep_from ? widen(x[r * xs + c]) * d.scale : 0.f;
-    if (residual != nullptr) y += widen(residual[r * rs + c]);
-    put(out + r * os + c, y);
-    if (++c == cols) c = 0, ++r;
+    for (int e = 0; e < N; ++e) v[e] += y[e];
+    store<N>(out + r * p.os + c, v);
+  } else {
+    int64_t r = int64_t(divide(uint64_t(i), p.groups)), c = i - r * p.cols;
+    int64_t rows[N], at[N];
+    float v[N] = {}, y[N] = {};
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      rows[e] = r, at[e] = c;
+      if (i + e < p.n) {
+        v[e] = widen(x[r * p.xs + c]);
+        if (residual != nullptr) y[e] = widen(residual[r * p.rs + c]);
+      }
+      if (++c == p.cols) c = 0, ++r;
+    }
+    drop<N>(d, step, uint64_t(i), d.scale, v);
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (i + e < p.n) put(out + rows[e] * p.os + at[e], v[e] + y[e]);
   }
 }
 
@@ -1423,6 +1543,8 @@ psgd_status enqueue_loss(psgd_lm_plan* plan, const void* x, const void* params, 
   const int32_t tiles = int32_t(ceil_div(plan->vb, small ? 1 : kTile));
   // a workgroup per worker does all its rows where that is little
   const bool one = plan->chunk >= plan->tb && plan->rows * tiles <= kFewStats;
+  int32_t at = kThreads;  // 16 threads for a row's tiles, or as many as there are tiles
+  while (at > 16 && kThreads / at < tiles) at /= 2;
   for (int32_t t0 = 0; t0 < plan->tb; t0 += plan->chunk) {
     const ScoreArgs a{v.w, v.x, f32 ? kF32 : kOne, steps_of_last(plan->dim), 0, plan->vb, t0, std::min(plan->tb, t0 + plan->chunk),
                       plan->vocab, v.info, v.exps, x_scale_of(d), v.stat, v.hit, nullptr, 0};
@@ -1431,8 +1553,8 @@ psgd_status enqueue_loss(psgd_lm_plan* plan, const void* x, const void* params, 
     if (s != PSGD_OK) return s;
     const int64_t r0 = int64_t(t0) * kBlk, n = one ? plan->rows : std::min(rows, int64_t(a.t1) * kBlk) - r0;
     const RowsArgs b{v.stat, tiles, int64_t(a.t1 - t0) * kBlk, v.info + r0, v.hit + r0, n, losses + r0, lse + r0,
-                     one ? mean : nullptr};
-    s = launch(plan, kRows, lm_rows, dim3(unsigned(one ? plan->n_workers : ceil_div(n, kRowsAt))), kThreads, st, b);
+                     one ? mean : nullptr, at};
+    s = launch(plan, kRows, lm_rows, dim3(unsigned(one ? plan->n_workers : ceil_div(n, at))), kThreads, st, b);
     if (s != PSGD_OK) return s;
   }
   if (one) return PSGD_OK;
@@ -1527,6 +1649,23 @@ psgd_status enqueue_grad(psgd_lm_plan* plan, const void* x, const void* params, 
                       plan->rows, per, int32_t(plan->dim), static_cast<uint16_t*>(dx), d);
 }
 
+Div divide_by(uint64_t d) {
+  Div v{d, 0, 0, 0};
+  if (d >> 32) return v;
+  uint32_t l = 0;
+  while ((uint64_t(1) << l) < d) ++l;
+  v.mul = uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << l) - d)) / d + 1);
+  v.s1 = std::min<uint32_t>(l, 1);
+  v.s2 = l > 1 ? l - 1 : 0;
+  return v;
+}
+
+template <typename T, int N, bool VEC>
+void enqueue_dropout(DropArgs a, const Drop& d, hipStream_t st) {
+  a.groups = divide_by(uint64_t(VEC ? a.cols / N : a.cols));
+  hipLaunchKernelGGL((lm_dropout<T, N, VEC>), dim3(unsigned(ceil_div(a.n, kThreads * N))), dim3(kThreads), 0, st, a, d);
+}
+
 int32_t sort_size(int64_t rows) {
   int32_t n = 2;
   while (n < kSortMax && n < rows) n <<= 1;
@@ -1541,27 +1680,24 @@ psgd_status enqueue_embed_grad(psgd_lm_plan* plan, const int64_t* tokens, const 
   uint64_t* other = reinterpret_cast<uint64_t*>(ws + plan->ws_key2);
   const unsigned W = unsigned(plan->n_workers);
   const int32_t size = sort_size(plan->rows);
-  psgd_status s = launch(plan, kSort, lm_sort, dim3(unsigned(ceil_div(plan->rows, size)), W), kSortThreads, st, tokens, plan->rows,
-                         plan->vocab, size, keys);
+  const int64_t n = plan->vocab * plan->dim, chunks = ceil_div(plan->rows, size);
+  const int64_t zeros = add ? 0 : ceil_div(n, kSortThreads * kZeroUnits * (16 / int64_t(sizeof(GT)))) * plan->n_workers;
+  psgd_status s = launch(plan, kSort, lm_sort<GT>, dim3(unsigned(chunks * plan->n_workers + zeros)), kSortThreads, st, tokens,
+                         plan->rows, plan->vocab, size, keys, int32_t(chunks), plan->n_workers, table, n, plan->worker_stride);
   for (int64_t run = size; s == PSGD_OK && run < plan->rows; run *= 2) {
     s = launch(plan, kMerge, lm_merge, dim3(unsigned(ceil_div(plan->rows, kThreads)), W), kThreads, st,
                static_cast<const uint64_t*>(keys), other, plan->rows, run);
     std::swap(keys, other);
   }
   if (s != PSGD_OK) return s;
-  const int64_t n = plan->vocab * plan->dim;
-  if (!add) {
-    s = launch(plan, kZero, lm_zero<GT>, dim3(unsigned(ceil_div(n, kThreads * (16 / int64_t(sizeof(GT))))), W), kThreads, st, table,
-               n, plan->worker_stride);
-    if (s != PSGD_OK) return s;
-  }
   const int32_t runs = int32_t(ceil_div(plan->rows, kRun)), dpad = int32_t(ceil_div(plan->dim, 4) * 4);
   const SumArgs a{keys, plan->rows, int32_t(plan->dim), dpad, runs, add ? 1 : 0, plan->worker_stride,
                   reinterpret_cast<float*>(ws + plan->ws_part)};
   const dim3 grid(unsigned(runs), unsigned(ceil_div(plan->dim, 256)), W);
-  s = launch(plan, kSum, lm_sum<T, GT>, grid, 64, st, a, dout, table, d);
+  const bool wide = plan->dim >= 4;
+  s = launch(plan, kSum, wide ? lm_sum<T, GT, true> : lm_sum<T, GT, false>, grid, 64, st, a, dout, table, d);
   if (s != PSGD_OK || runs == 1) return s;
-  return launch(plan, kJoin, lm_join<GT>, grid, 64, st, a, table);
+  return launch(plan, kJoin, wide ? lm_join<GT, true> : lm_join<GT, false>, grid, 64, st, a, table);
 }
 
 }  // namespace
@@ -1891,15 +2027,11 @@ extern "C" psgd_status psgd_dropout(const void* x, int64_t x_stride, const void*
       if ((s = check_spans(fn, three, 3, same ? 0 : -1, same ? 1 : -1)) != PSGD_OK) return s;
     }
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    const int64_t n = rows * cols;
-    const dim3 grid(unsigned(ceil_div(n, kThreads * 4)));
+    DropArgs a{x, residual, out, x_stride, residual_stride, out_stride, rows * cols, cols, Div{}};
     if (dtype == PSGD_F32)
-      hipLaunchKernelGGL(lm_dropout<float>, grid, dim3(kThreads), 0, st, static_cast<const float*>(x), x_stride,
-                         static_cast<const float*>(residual), residual_stride, static_cast<float*>(out), out_stride, n, cols, d);
+      cols % 4 == 0 ? enqueue_dropout<float, 4, true>(a, d, st) : enqueue_dropout<float, 4, false>(a, d, st);
     else
-      hipLaunchKernelGGL(lm_dropout<uint16_t>, grid, dim3(kThreads), 0, st, static_cast<const uint16_t*>(x), x_stride,
-                         static_cast<const uint16_t*>(residual), residual_stride, static_cast<uint16_t*>(out), out_stride, n, cols,
-                         d);
+      cols % 8 == 0 ? enqueue_dropout<uint16_t, 8, true>(a, d, st) : enqueue_dropout<uint16_t, 4, false>(a, d, st);
     const hipError_t err = hipGetLastError();
     return err == hipSuccess ? PSGD_OK : hip_fail("launch lm_dropout", err);
   } catch (...) {
