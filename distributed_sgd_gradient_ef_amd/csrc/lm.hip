@@ -45,6 +45,7 @@ namespace lm {
 constexpr int kBlk = 64;           // rows and columns of a packed block
 constexpr int kBlkElems = kBlk * kBlk;
 constexpr int64_t kMaxBlocks = int64_t(1) << 23;  // of x or the table: launches of 256 threads each stay below 2^32
+constexpr int64_t kMaxDim = int64_t(1) << 23;     // strips of columns are a launch's second dimension
 constexpr int kTile = 4;           // blocks per side of a workgroup's tile
 constexpr int kThreads = 256;      // of the kernels around the products
 constexpr int kGroup = 16;         // row blocks that take turns on one vocabulary tile (lm_scores)
@@ -523,21 +524,14 @@ __device__ __forceinline__ F block_sum(F x, F* sm) {
 
 __device__ __forceinline__ bool counts(int64_t target, int64_t vocab) { return uint64_t(target) < uint64_t(vocab); }
 
-// Largest finite magnitude (as its bits) of every part of the table and of x.
-__global__ __launch_bounds__(kThreads) void lm_peak(const float* table, int64_t n_table, const float* x, int64_t n_x,
-                                                    uint32_t* peak) {
-  __shared__ uint32_t sm[kThreads / 64];
-  const int job = blockIdx.x;
-  const bool t = job < kPeakW;
-  const float* p = t ? table : x;
-  const int64_t n = t ? n_table : n_x, part = t ? job : job - kPeakW, of = t ? kPeakW : kPeakX;
-  const int64_t per = (n + of * 4 - 1) / (of * 4) * 4, end = min(n, (part + 1) * per);
+// Largest finite magnitude (as its bits) of p[begin, end), by threads `id` of `of`.
+__device__ __forceinline__ uint32_t peak_of(const float* p, int64_t begin, int64_t end, int id, int of) {
   uint32_t m = 0;
-  for (int64_t i = part * per + threadIdx.x * 4; i < end; i += kThreads * 16) {
+  for (int64_t i = begin + id * 4; i < end; i += of * 16) {
     float v[4][4] = {};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int64_t at = i + k * kThreads * 4;
+      const int64_t at = i + k * of * 4;
       if (at + 4 <= end) {
         load<4>(p + at, v[k]);
       } else {
@@ -553,6 +547,23 @@ __global__ __launch_bounds__(kThreads) void lm_peak(const float* table, int64_t 
         const uint32_t u = __float_as_uint(v[k][e]) & 0x7fffffffu;
         m = max(m, u < 0x7f800000u ? u : 0u);
       }
+  }
+  return m;
+}
+
+// The largest magnitude of every part of the table (a workgroup each), and of x's rows that count
+// (a wave takes a row at a time): what the others hold must not matter.
+__global__ __launch_bounds__(kThreads) void lm_peak(const float* table, int64_t n_table, const float* x, int64_t rows,
+                                                    int64_t dim, const int64_t* targets, int64_t vocab, uint32_t* peak) {
+  __shared__ uint32_t sm[kThreads / 64];
+  const int job = blockIdx.x, wave = threadIdx.x >> 6;
+  uint32_t m = 0;
+  if (job < kPeakW) {
+    const int64_t per = (n_table + kPeakW * 4 - 1) / (kPeakW * 4) * 4;
+    m = peak_of(table, job * per, min(n_table, (job + 1) * per), threadIdx.x, kThreads);
+  } else {
+    for (int64_t r = (job - kPeakW) * (kThreads / 64) + wave; r < rows; r += kPeakX * (kThreads / 64))
+      if (counts(targets[r], vocab)) m = max(m, peak_of(x, r * dim, (r + 1) * dim, threadIdx.x & 63, 64));
   }
   for (int o = 32; o > 0; o >>= 1) m = max(m, uint32_t(__shfl_xor(int(m), o)));
   if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
@@ -1505,8 +1516,8 @@ psgd_status enqueue_pack(psgd_lm_plan* plan, const Views& v, const void* x, cons
   const void* table = table_of(plan, params);
   if (f32) {
     const psgd_status s = launch(plan, kPeak, lm_peak, dim3(kPeakW + kPeakX), kThreads, st, static_cast<const float*>(table),
-                                 plan->vocab * plan->dim, static_cast<const float*>(x), plan->rows * plan->n_workers * plan->dim,
-                                 v.peak);
+                                 plan->vocab * plan->dim, static_cast<const float*>(x), plan->rows * plan->n_workers,
+                                 plan->dim, targets, plan->vocab, v.peak);
     if (s != PSGD_OK) return s;
   }
   PackArgs a{x, table, v.x, v.w, rows, blocks, v.x.rb / blocks, plan->n_workers, plan->rows, plan->vocab, int32_t(plan->dim),
@@ -1749,10 +1760,11 @@ extern "C" psgd_status psgd_lm_plan_create(const psgd_layer* layers, int32_t n_l
     plan->tb = int32_t(ceil_div(n, kBlk));
     plan->tw = int32_t(ceil_div(rows, kBlk));
     const int64_t tbp = int64_t(plan->tw) * n_workers;  // >= tb
-    if (std::max<int64_t>(tbp, plan->vb) * plan->db > kMaxBlocks) {
+    if (plan->dim > kMaxDim || std::max<int64_t>(tbp, plan->vb) * plan->db > kMaxBlocks) {
       delete plan;
       plan = nullptr;
-      return fail(PSGD_ERR_INVALID_ARG, "psgd_lm_plan_create: the table or the workers' rows have over 2^23 blocks of 64 x 64");
+      return fail(PSGD_ERR_INVALID_ARG,
+                  "psgd_lm_plan_create: dim is over 2^23, or the table or the workers' rows have over 2^23 blocks of 64 x 64");
     }
     const uint64_t blk = kBlkElems * 2, p = uint64_t(parts_of(act_dtype)), gp = uint64_t(g_parts(plan));
     // pieces of about equal size, whole tiles each

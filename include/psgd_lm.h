@@ -34,12 +34,16 @@
  * graph draw new masks; layers are told apart by their seeds.
  *
  * Precision.  Activations (x, out, dout, dx) and params have one type, gradients another or
- * the same, float32 or bfloat16 each.  Products are summed in float32.  float32 factors
- * enter the matrix cores as three bfloat16 parts (24 bits); g is rounded to bfloat16 where
- * the other factor and the result are bfloat16 both.  Everything else is float32, means and
- * counts are taken in float64, results are rounded once.  Sums have a fixed order: equal
- * calls give equal bits.  Non-finite entries are not errors: one in the table, or in x's
- * row, makes what depends on it infinite or NaN (that row's loss, or every row's).
+ * the same, float32 or bfloat16 each.  Products are summed in float32.  float32 matrices enter
+ * the matrix cores as two scaled fp16 parts: 22 bits of an entry down to 2^-28 of the largest
+ * finite entry of its matrix (x's counted rows, the table), fewer below that and none below
+ * 2^-49; g likewise, against 1.  With bfloat16 activations x and the table are taken as they
+ * are and g is rounded to bfloat16, but not for a float32 table gradient.  With float32
+ * activations and bfloat16 gradients the table gradient's factors have 11 bits.  Everything
+ * else is float32, means are taken in float64, results are rounded once.  Sums have a fixed
+ * order: equal calls give equal bits.  Non-finite entries are not errors: one in the table, or
+ * in a counted row of x, makes what depends on it infinite or NaN (that row's loss, or every
+ * counted row's).
  *
  * No logits are kept: psgd_lm_loss reduces each tile of them where it is computed, and
  * psgd_lm_loss_grad holds g for one piece of the vocabulary at a time in the workspace.
@@ -82,8 +86,8 @@ typedef struct psgd_lm_sizes {
 
 /* Build a plan for a model of `n_layers` tensors (1 <= rows*cols < 2^31 each) of which
  * tensor `table` is the vocab x dim table, n_workers in 1..65535 workers and `rows` tokens
- * per worker, n_workers * rows in 1..2^23.  The table, and the workers' rows (every
- * worker's rounded up to 64), have at most 2^23 blocks of 64 x 64.  act_dtype: type of
+ * per worker, n_workers * rows in 1..2^23.  dim is at most 2^23, and the table and
+ * the workers' rows (every worker's rounded up to 64) have at most 2^23 blocks of 64 x 64.  act_dtype: type of
  * params and activations; grad_dtype: type of grads.  flags must be 0 (PSGD_ERR_UNSUPPORTED otherwise, as for an
  * unknown dtype).  Host only. */
 psgd_status psgd_lm_plan_create(const psgd_layer* layers, int32_t n_layers, int32_t table, int32_t n_workers,
@@ -125,7 +129,8 @@ psgd_status psgd_lm_loss(psgd_lm_plan* plan, const void* x, const void* params, 
                          void* stream);
 
 /* Gradients of every worker's scale * mean:
- *   lse     [n_workers][rows] float32, of psgd_lm_loss on the same x, params and dropout
+ *   lse     [n_workers][rows] float32, of psgd_lm_loss on the same x, params and dropout (for
+ *           one that is smaller g is larger than 1, and past 4 no number)
  *   scale   [n_workers] float32, or NULL for 1
  *   dx      [n_workers][rows][dim] act_dtype out, or NULL
  *   grads   [n_workers][worker_stride] grad_dtype, the table's part set or added to, or NULL

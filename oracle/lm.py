@@ -19,10 +19,11 @@ def philox4x32(counter, key):
     return np.stack(c, 1)
 
 
-def kept(shape, p, seed, step):
-    """Which entries of an array of this shape (row-major) dropout keeps."""
+def kept(shape, p, seed, step, first=0):
+    """Which entries of an array of this shape (row-major) dropout keeps; the array may be the
+    part of a larger one that starts at entry `first`, a multiple of 4."""
     n = int(np.prod(shape, dtype=np.int64))
-    i = np.arange((n + 3) // 4, dtype=np.uint64)
+    i = np.arange((n + 3) // 4, dtype=np.uint64) + np.uint64(first // 4)
     step = int(step) & 0xFFFFFFFFFFFFFFFF
     counter = np.stack([i & np.uint64(0xFFFFFFFF), i >> np.uint64(32), np.full_like(i, step & 0xFFFFFFFF),
                         np.full_like(i, step >> 32)], 1)
