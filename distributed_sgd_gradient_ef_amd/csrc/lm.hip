@@ -51,7 +51,10 @@ constexpr int kThreads = 256;      // of the kernels around the products
 constexpr int kGroup = 16;         // row blocks that take turns on one vocabulary tile (lm_scores)
 constexpr int64_t kFewStats = 16384;  // maxima and sums of a worker that one workgroup takes in
 constexpr int kSplitBlocks = 8;    // vocabulary blocks of a split of lm_products' dx, at least
-constexpr int64_t kPieceBytes = int64_t(512) << 20;  // g of one piece of the vocabulary
+// g of one piece of the vocabulary.  64, 128, 256, 512, 1024 MB: gradients of 33,278 x 650, 8 x 700
+// rows float32 3.57, 3.24, 2.79, 2.65, 2.63 ms; of 65,536 x 2048, 2 x 2048 rows bfloat16 3.65, 3.49,
+// 3.19, 3.12, 3.12 (each piece adds to all of dx, and the last tiles of a launch run alone).
+constexpr int64_t kPieceBytes = int64_t(512) << 20;
 constexpr int64_t kStatBytes = int64_t(64) << 20;    // maxima and sums of one chunk of rows
 constexpr int kSortMax = 1024;     // pairs sorted by one workgroup
 constexpr int kSortThreads = 512;
@@ -186,7 +189,8 @@ __device__ __forceinline__ void drop(const Drop& d, uint64_t step, uint64_t i, f
 //
 // A bfloat16 table whose rows are whole blocks (dim a multiple of 64) needs no packing: its
 // blocks are gathered, 16 bytes a lane, as they go into LDS.  Against packing it first,
-// 131,072 x 2048 for 4096 rows: @@DIRECT@@.
+// 131,072 x 2048 for 4096 rows: packing it took 228 of
+// the loss's 2081 us.
 struct Mat {
   const uint16_t* p;
   int64_t part;  // elements between parts
@@ -552,7 +556,8 @@ __device__ __forceinline__ uint32_t peak_of(const float* p, int64_t begin, int64
 }
 
 // The largest magnitude of every part of the table (a workgroup each), and of x's rows that count
-// (a wave takes a row at a time): what the others hold must not matter.
+// (a wave takes a row at a time): what the others hold must not matter.  Bound by memory: 87 MB
+// of table and 15 MB of x in 15 to 18 us (256 workgroups without loads in flight: 34).
 __global__ __launch_bounds__(kThreads) void lm_peak(const float* table, int64_t n_table, const float* x, int64_t rows,
                                                     int64_t dim, const int64_t* targets, int64_t vocab, uint32_t* peak) {
   __shared__ uint32_t sm[kThreads / 64];
@@ -609,7 +614,8 @@ struct PackArgs {
 
 // One block per workgroup: those of x (through dropout, but not scaled: the products' results
 // are; zero where a row does not count), those of the table, and after them one workgroup per
-// worker that counts its rows.
+// worker that counts its rows.  Bound by memory: 33,278 x 650 and 5600 rows in float32, 102 MB
+// read and 108 MB written, in 41 us.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void lm_pack(PackArgs p, Drop d) {
   const int32_t cb = p.x_to.cb;
@@ -684,7 +690,10 @@ __global__ __launch_bounds__(kThreads) void lm_pack(PackArgs p, Drop d) {
 
 // ------------------------------------------------------------------ scores
 // Tile sizes: 256 x 256 by eight waves where that gives at least kFewTiles tiles, and else
-// 64 x 64 by four, so that small problems still spread over the chip: @@TILES@@
+// 64 x 64 by four, so that small problems still spread over the chip.  us a call for bounds of
+// 64, 128, 256 and 512 tiles: loss of 8000 x 512, 512 rows 83, 21, 21, 21; of 16,000 x 300, 1024
+// rows 31, 31, 40, 40; of 32,000 x 1024, 1024 rows 77, 76, 76, 113; gradients of 4000 x 300, 1000
+// rows float32 90, 66, 65, 65; of 32,000 x 1024, 512 rows 129, 130, 144, 194.
 constexpr int64_t kFewTiles = 128;
 
 template <bool SMALL, bool TA, bool TB, bool F16, bool RA, bool RB>
@@ -737,6 +746,13 @@ enum ScoreKind {
 // l mod 32 of each of its pieces, so a row's maximum and sum are taken within a lane, then
 // over its two lane halves and the two waves that share the row.  Maxima and sums are those of
 // exp2 of s log2(e): m the largest of them, and sum exp2(s log2(e) - m).
+//
+// Bound by the matrix cores and the card's power: 131,072 x 2048 for 4096 rows in bfloat16
+// takes 1.83 to 1.95 ms (box to box), 1.2 PFLOP/s with the exponentials; the library's product
+// alone, which keeps its scores, 1.65 (1.33 PFLOP/s).  The matrix cores are busy for 56% of
+// the cycles at 1.7 GHz, there 75% at 1.5 GHz.  What got it here, in us: operands through
+// registers 2113, straight into LDS 1907, LDS reads with one wait per 16 contraction steps
+// 1798, one fused multiply-add per exponential.  Four waves of 128 x 128: 2856.
 template <int KIND, bool SMALL, bool R>
 __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_scores(ScoreArgs p) {
   constexpr bool kF16 = KIND == kLossF32 || KIND == kGradF32;
@@ -974,7 +990,14 @@ struct ProductArgs {
 };
 
 // The two products with g.  The first dx_jobs workgroups take the tiles of dx and the splits of
-// their sum over the piece, the others the tiles of every worker's table gradient.
+// their sum over the piece, the others the tiles of every worker's table gradient; one launch, so
+// that the chip does not run empty between them.
+//
+// Bound by the matrix cores as lm_scores where rows and dim are long: 65,536 x 2048 for 2 x 2048
+// rows in bfloat16 2.0 ms, 1.1 PFLOP/s for both.  Tiles side by side on one XCD: 2.85 -> 2.79 ms
+// for a call on 33,278 x 650, 8 x 700 rows.  By memory where a worker has few rows: for 16 x
+// 148 rows 55,650 x 292, 1.04 GB of float32 added to in 1.26 ms (a piece's old values loaded
+// one after the other: 2.35).
 template <bool F16, typename GT, bool SMALL, bool R>
 __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_products(ProductArgs p, GT* grads) {
   typedef Tile<SMALL, false, true, F16, false, R> Gx;
@@ -1061,7 +1084,8 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_products(ProductArgs p, 
     }
 }
 
-// dx of every row from its splits, times scale / counted, through dropout.
+// dx of every row from its splits, times scale / counted, through dropout: 5600 x 650
+// float32 from three splits, 62 MB, in 16 us.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void lm_dx_out(const float* part, int32_t splits, int64_t packed_rows, int64_t ld,
                                                       const RowInfo* info, const float* scale, const int32_t* count,
@@ -1095,6 +1119,8 @@ __global__ __launch_bounds__(kThreads) void lm_dx_out(const float* part, int32_t
 }
 
 // ------------------------------------------------------------------ embedding
+// A wave takes 512 columns of a row.  8 x 700 rows of 650 in float32, dropped out: 9.2 us for
+// 29 MB (one row: 2.8).
 template <typename T>
 __global__ __launch_bounds__(64) void lm_embed(const T* table, int64_t vocab, int32_t dim, const int64_t* tokens, T* out,
                                                Drop d) {
@@ -1129,7 +1155,8 @@ __global__ __launch_bounds__(64) void lm_embed(const T* table, int64_t vocab, in
 constexpr uint64_t kNoToken = 0xffffffffull;
 
 // The first workgroups each sort one chunk of a worker's pairs (bitonic: a fixed network on
-// distinct keys); the others zero the tables that are not added to.
+// distinct keys, 55 steps of a barrier each: 14 us for 1024 pairs, 50 for 4096); the others zero
+// the tables that are not added to (537 MB in 98 us), which hides the sort.
 template <typename GT>
 __global__ __launch_bounds__(kSortThreads) void lm_sort(const int64_t* tokens, int64_t rows, int64_t vocab, int32_t size,
                                                         uint64_t* keys, int32_t chunks, int32_t workers, GT* table, int64_t n,
@@ -1244,7 +1271,9 @@ __device__ __forceinline__ uint64_t pair_at(const uint64_t* keys, int64_t i) {
 }
 
 // kRun sorted pairs x 256 columns per wave, summed in their order.  A token whose pairs lie
-// in one run is written here; the others leave a part per run for lm_join.
+// in one run is written here; the others leave a part per run for lm_join.  Bound by the
+// latency of the loads, hence kRunLoads rows at once and no branch around them: 8 x 700 rows
+// of 650 in float32, dropped out and added, 20 us (one row after the other, 32 per wave: 51).
 template <typename T, typename GT, bool WIDE>
 __global__ __launch_bounds__(64) void lm_sum(SumArgs p, const T* dout, GT* table, Drop d) {
   const int64_t w = blockIdx.z, run = blockIdx.x, i0 = run * kRun, i1 = min(p.rows, i0 + kRun);
@@ -1352,7 +1381,9 @@ struct DropArgs {
   Div groups;  // VEC: groups of N entries per row; otherwise cols
 };
 
-// N consecutive entries per thread.  VEC: they lie in one row (cols is a multiple of N).
+// N consecutive entries per thread.  VEC: they lie in one row (cols is a multiple of N); 16-byte
+// loads at any alignment.  16,384 x 4096 bfloat16 with a residual: 71 us, 5.7 TB/s; element by
+// element, with a 64-bit division per thread, 155.
 template <typename T, int N, bool VEC>
 __global__ __launch_bounds__(kThreads) void lm_dropout(DropArgs p, Drop d) {
   const int64_t group = int64_t(blockIdx.x) * kThreads + threadIdx.x, i = group * N;
