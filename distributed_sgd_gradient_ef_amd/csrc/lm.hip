@@ -222,6 +222,12 @@ struct Gemm {
   static constexpr int kPer = kBlkElems / 8 / kT;           // 16-byte pieces of a block per thread
   static constexpr int kStage = (kA + kB) * kBlkElems;
   static constexpr int kLds = 2 * kStage;
+  // The small score tiles have registers for a sum of its own for each quarter of a block's
+  // steps: shorter sums round less, and an error of a score of 40 reaches exp(s - lse) whole.
+  // Distance of table gradients from float64, 1, 2 and 4 sums: 2 x 19 rows of 21,396 x 1532 1.0,
+  // 0.39, 0.21e-5; 3 x 127 rows of 1429 x 1323 8.0, 4.2, 2.4e-6; 403 rows' loss over 14,070 x
+  // 259 takes 27, 27, 30 us.
+  static constexpr int kSums = FM == 1 && !TA && !TB ? 4 : 1;
   static constexpr int kRowsA = FM * 32, kRowsB = FN * 32;  // of a wave
   typedef f16v Acc[FM][FN];
   static constexpr int kFM = FM, kFN = FN, kWN = WN, kWM = WM;
@@ -416,6 +422,7 @@ struct Gemm {
     uint32_t at_ra[4], at_rb[4];
     rows_at(wa, lane, at_ra);
     rows_at(wb, lane, at_rb);
+    Acc sums[kSums] = {};
     auto multiply = [&](uint32_t base, const uint32_t (&ca)[2][2], const uint32_t (&cb)[2][2], auto kk) {
       constexpr int K = decltype(kk)::value;
       bf8 x[FM], y[FN];
@@ -431,10 +438,11 @@ struct Gemm {
       for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
+          f16v& a = kSums > 1 ? sums[K][i][j] : acc[i][j];
           if constexpr (F16)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, x[i]), __builtin_bit_cast(h8, y[j]), acc[i][j], 0, 0, 0);
+            a = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, x[i]), __builtin_bit_cast(h8, y[j]), a, 0, 0, 0);
           else
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
+            a = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], y[j], a, 0, 0, 0);
         }
     };
     const int steps = int(parts.n) * (k1 - k0);
@@ -469,6 +477,12 @@ struct Gemm {
       if (--left == 0) break;
     }
     __syncthreads();
+    if constexpr (kSums > 1) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] += (sums[0][i][j] + sums[1][i][j]) + (sums[2][i][j] + sums[3][i][j]);
+    }
   }
 
   // The whole product.  With fp16 parts the products with a low part come first and are
