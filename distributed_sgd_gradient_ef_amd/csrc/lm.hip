@@ -438,7 +438,7 @@ struct Gemm {
       for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-          f16v& a = kSums > 1 ? sums[K][i][j] : acc[i][j];
+          f16v& a = kSums > 1 ? sums[K % kSums][i][j] : acc[i][j];
           if constexpr (F16)
             a = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, x[i]), __builtin_bit_cast(h8, y[j]), a, 0, 0, 0);
           else
@@ -614,8 +614,8 @@ struct PackArgs {
   const void *x, *table;
   Mat x_to, w_to;        // packed (p is written); w_to.p NULL: the table is read as it is
   int64_t rows;          // of x in each group, which starts at a block of its own ...
-  int32_t blocks, groups;  // ... of `blocks`
-  int64_t workers, worker_rows;  // how the targets are counted
+  int32_t blocks;        // ... of `blocks`
+  int64_t worker_rows;   // how the targets are counted
   int64_t vocab;
   int32_t dim;
   const int64_t* targets;
@@ -988,7 +988,6 @@ struct ProductArgs {
   int64_t dim;
   float x_scale;      // dropout's
   int32_t tw;         // row blocks per worker
-  int32_t workers;
   int64_t rows;       // per worker
   // dx = g T
   int32_t dx_jobs, splits, dx_tail;
@@ -1565,7 +1564,7 @@ psgd_status enqueue_pack(psgd_lm_plan* plan, const Views& v, const void* x, cons
                                  plan->dim, targets, plan->vocab, v.peak);
     if (s != PSGD_OK) return s;
   }
-  PackArgs a{x, table, v.x, v.w, rows, blocks, v.x.rb / blocks, plan->n_workers, plan->rows, plan->vocab, int32_t(plan->dim),
+  PackArgs a{x, table, v.x, v.w, rows, blocks, plan->rows, plan->vocab, int32_t(plan->dim),
              targets, lse, v.info, count, v.peak, v.exps};
   if (plan->direct) a.w_to.p = nullptr;
   const int64_t jobs = int64_t(v.x.rb) * v.x.cb + (plan->direct ? 0 : int64_t(v.w.rb) * v.w.cb) +
@@ -1667,7 +1666,6 @@ psgd_status enqueue_grad(psgd_lm_plan* plan, const void* x, const void* params, 
     b.dim = plan->dim;
     b.x_scale = x_scale;
     b.tw = plan->tw;
-    b.workers = plan->n_workers;
     b.rows = plan->rows;
     b.splits = plan->splits;
     b.dx_jobs = dx != nullptr ? int32_t(ceil_div(tb, tile) * n_c * plan->splits) : 0;
