@@ -1,12 +1,16 @@
 // Embedding, softmax cross entropy and dropout around a language model's table: the gfx950
 // kernels and the host side of psgd_lm.h.
 //
-// Products run on bf16 matrix cores from packed operands: 64 x 64 blocks of bf16, 8 KB each
-// and one after the other, so that a tile is a few contiguous runs of 16-byte loads, zero
-// past a matrix's edges, so that no product loop has an edge of its own.  A float32 operand
-// is scaled by a power of two and held as two fp16 parts, x = h + l / 2048, which carry 22
-// bits; a product of two of them is h l' + l h' (divided by 2048) + h h': the loop over the
-// contraction simply runs three times.
+// Products run on 16-bit matrix cores from packed operands: 64 x 64 blocks of bf16 or fp16,
+// 8 KB each and one after the other, so that a tile is a few contiguous runs of 16-byte loads,
+// zero past a matrix's edges, so that no product loop has an edge of its own.  Operands in
+// float32 are held in parts, and the loop over the contraction runs once per product of two
+// parts:
+// - for the scores they are scaled by a power of two and held as two fp16 parts, x = h + l /
+//   2048; a product of two of them is h l' + l h' (divided by 2048) + h h';
+// - for the products with g, whose entries and whose partners' rows range over any powers of
+//   two, they and g are three bf16 parts, x = h + m + l: every entry has its 24 bits, whatever
+//   the others are.  The six products above 2^-24 take part.
 //
 //   lm_peak    the largest entries of float32 operands
 //   lm_pack    x (through dropout, zero where a row does not count) and the table, packed; the
@@ -81,7 +85,7 @@ struct psgd_lm_plan {
   int32_t chunk = 0;             // row blocks per chunk in psgd_lm_loss
   bool direct = false;           // the table is read as it is
   bool loss_small = false, scores_small = false, grad_small = false;  // which tiles are the small ones
-  uint64_t ws_x = 0, ws_w = 0, ws_peak = 0, ws_exps = 0, ws_info = 0, ws_count = 0, ws_stat = 0, ws_hit = 0, ws_g = 0, ws_dx = 0;
+  uint64_t ws_x = 0, ws_w = 0, ws_x3 = 0, ws_w3 = 0, ws_peak = 0, ws_exps = 0, ws_info = 0, ws_count = 0, ws_stat = 0, ws_hit = 0, ws_g = 0, ws_dx = 0;
   uint64_t ws_key = 0, ws_key2 = 0, ws_part = 0, workspace_bytes = 0;
   bool timing = false;
   std::vector<psgd::PendingTiming> pending;
@@ -125,6 +129,18 @@ __device__ __forceinline__ void store(uint16_t* p, const float (&x)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = narrow_bits(x[i]);
   __builtin_memcpy(p, v, sizeof(v));
+}
+
+// x = h + m + l, bf16 each, every one the nearest to what is left.  A number past the largest
+// bf16 takes that as its first part; infinities and NaN have one part.
+__device__ __forceinline__ void split3(float x, uint16_t (&part)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    uint16_t b = narrow_bits(x);
+    if ((b & 0x7fff) == 0x7f80 && (__float_as_uint(x) & 0x7fffffffu) < 0x7f800000u) b -= 1;
+    part[i] = b;
+    x = (b & 0x7f80) == 0x7f80 ? 0.f : x - widen(b);
+  }
 }
 
 // The two fp16 parts of x, |x| < 2^15 or not finite: x = h + l / 2048.
@@ -519,7 +535,6 @@ struct RowInfo {
 };
 
 constexpr float kLog2e = 1.44269504f;
-constexpr int kGExp = 14;  // g is held in fp16 as g 2^14: it is below 1 but for rounding
 
 // float32 operands: their powers of two.  An operand is scaled so that its largest finite
 // entry lies in [2^14, 2^15): its fp16 parts hold 22 bits of entries down to 2^-28 of it.
@@ -613,6 +628,7 @@ __device__ __forceinline__ float coef_of(const float* scale, const int32_t* coun
 struct PackArgs {
   const void *x, *table;
   Mat x_to, w_to;        // packed (p is written); w_to.p NULL: the table is read as it is
+  Mat x3_to, w3_to;      // float32: their three bf16 parts; p NULL: not wanted
   int64_t rows;          // of x in each group, which starts at a block of its own ...
   int32_t blocks;        // ... of `blocks`
   int64_t worker_rows;   // how the targets are counted
@@ -629,7 +645,7 @@ struct PackArgs {
 // One block per workgroup: those of x (through dropout, but not scaled: the products' results
 // are; zero where a row does not count), those of the table, and after them one workgroup per
 // worker that counts its rows.  Bound by memory: 33,278 x 650 and 5600 rows in float32, 102 MB
-// read and 108 MB written, in 41 us.
+// read and 108 MB written, in 41 us (for the loss).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void lm_pack(PackArgs p, Drop d) {
   const int32_t cb = p.x_to.cb;
@@ -649,8 +665,7 @@ __global__ __launch_bounds__(kThreads) void lm_pack(PackArgs p, Drop d) {
   const int64_t rows = of_x ? p.rows : p.vocab, w = rb / blocks, t0 = (rb % blocks) * kBlk;
   const int32_t c0 = int32_t(block % cb) * kBlk;
   const T* src = static_cast<const T*>(of_x ? p.x : p.table);
-  const Mat& to = of_x ? p.x_to : p.w_to;
-  uint16_t* dst = const_cast<uint16_t*>(to.p) + block * kBlkElems;
+  const Mat &to = of_x ? p.x_to : p.w_to, &to3 = of_x ? p.x3_to : p.w3_to;
   const bool dropped = of_x && d.on;
   const uint64_t step = dropped ? step_of(d) : 0;
   int32_t exp2 = 0;
@@ -688,7 +703,8 @@ __global__ __launch_bounds__(kThreads) void lm_pack(PackArgs p, Drop d) {
       }
       if (dropped) drop<8>(d, step, uint64_t(row) * uint64_t(p.dim) + uint64_t(c), 1.f, x);
     }
-    uint16_t* o = dst + r * kBlk + ((int(threadIdx.x % 8) ^ turn(r)) << 3);
+    const int64_t at = block * kBlkElems + r * kBlk + ((int(threadIdx.x % 8) ^ turn(r)) << 3);
+    uint16_t* o = const_cast<uint16_t*>(to.p) + at;
     s8v h, l;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -698,7 +714,20 @@ __global__ __launch_bounds__(kThreads) void lm_pack(PackArgs p, Drop d) {
       h[e] = short(a), l[e] = short(b);
     }
     *reinterpret_cast<s8v*>(o) = h;
-    if constexpr (sizeof(T) == 4) *reinterpret_cast<s8v*>(o + to.part) = l;
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<s8v*>(o + to.part) = l;
+      if (to3.p == nullptr) continue;
+      s8v v[3];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        uint16_t part[3];
+        split3(x[e], part);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) v[i][e] = short(part[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) *reinterpret_cast<s8v*>(const_cast<uint16_t*>(to3.p) + i * to3.part + at) = v[i];
+    }
   }
 }
 
@@ -753,7 +782,7 @@ enum ScoreKind {
   kLossBf16, kLossF32,
   kGradBf16,   // g in bf16
   kGradBf16x3,  // g in three bf16 parts
-  kGradF32     // g in two fp16 parts
+  kGradF32     // the same, of float32 operands
 };
 
 // Scores of a tile of words x rows: lane l of a wave holds words in its accumulators and row
@@ -836,7 +865,7 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_scores(ScoreArgs p) {
       p.stat[int64_t(vt) * (p.t1 - p.t0) * kBlk + int64_t(tt) * kRows + r] = a;
     }
   } else {
-    constexpr int kParts = KIND == kGradBf16 ? 1 : KIND == kGradF32 ? 2 : 3;
+    constexpr int kParts = KIND == kGradBf16 ? 1 : 3;
     static_assert(G::kLds >= G::kA * G::kB * kBlkElems, "the tile's blocks of g, one part of them, fit LDS");
     float g[G::kFM][G::kFN][16];
     auto place = [&](int block) { return sm + block * kBlkElems; };
@@ -848,17 +877,16 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_scores(ScoreArgs p) {
       const bool on = ri.target >= 0;
       const int64_t local = ri.target - word0;
       const bool here = on && local >= 0 && local < n_words;
-      const float lo = kF16 ? ri.lo - float(kGExp) : ri.lo, one = kF16 ? float(1 << kGExp) : 1.f;
 #pragma unroll
       for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) g[i][j][e] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], c, -ri.hi) - lo);
+        for (int e = 0; e < 16; ++e) g[i][j][e] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], c, -ri.hi) - ri.lo);
       if (__any(here)) {
 #pragma unroll
         for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (here && i * 32 + acc_row(e, lane) == int(local)) g[i][j][e] -= one;
+            if (here && i * 32 + acc_row(e, lane) == int(local)) g[i][j][e] -= 1.f;
       }
       if (n_words < G::kRowsA || __any(!on)) {
 #pragma unroll
@@ -881,15 +909,9 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_scores(ScoreArgs p) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float x = g[i][j][e4 * 4 + e];
-              if constexpr (kF16) {
-                const _Float16 h = _Float16(x);
-                v[e] = __builtin_bit_cast(short, h);
-                if (part == 0) g[i][j][e4 * 4 + e] = (x - float(h)) * 2048.f;
-              } else {
-                const uint16_t h = narrow_bits(x);
-                v[e] = short(h);
-                if (part + 1 < kParts) g[i][j][e4 * 4 + e] = x - widen(h);
-              }
+              const uint16_t h = narrow_bits(x);
+              v[e] = short(h);
+              if (part + 1 < kParts) g[i][j][e4 * 4 + e] = x - widen(h);
             }
             const int row = wn * G::kRowsB + j * 32 + (lane & 31), word = wm * G::kRowsA + i * 32 + e4 * 8;
             const int r = row % kBlk, c8 = word % kBlk / 8;
@@ -981,7 +1003,6 @@ __global__ __launch_bounds__(kThreads) void lm_mean(const float* losses, const R
 struct ProductArgs {
   Mat g, w, x;        // of one piece of the vocabulary, w from its first block on; all rows
   Parts dx_parts, dw_parts;
-  const Scales* exps;
   const float* scale;
   const int32_t* count;
   const RowInfo* info;
@@ -1011,11 +1032,10 @@ struct ProductArgs {
 // for a call on 33,278 x 650, 8 x 700 rows.  By memory where a worker has few rows: for 16 x
 // 148 rows 55,650 x 292, 1.04 GB of float32 added to in 1.26 ms (a piece's old values loaded
 // one after the other: 2.35).
-template <bool F16, typename GT, bool SMALL, bool R>
+template <typename T, typename GT, bool SMALL, bool R>
 __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_products(ProductArgs p, GT* grads) {
-  typedef Tile<SMALL, false, true, F16, false, R> Gx;
-  typedef Tile<SMALL, true, true, F16, false, false> Gw;
-  typedef std::conditional_t<F16, float, uint16_t> T;
+  typedef Tile<SMALL, false, true, false, false, R> Gx;
+  typedef Tile<SMALL, true, true, false, false, false> Gw;
   __shared__ __align__(16) uint16_t sm[Gx::kLds];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n_c = (p.x.cb + Gx::kB - 1) / Gx::kB;
   const int64_t in_r = (wave / Gx::kWN) * Gx::kRowsA, in_c = (wave % Gx::kWN) * Gx::kRowsB + (lane & 31);
@@ -1029,7 +1049,6 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_products(ProductArgs p, 
     const int c0 = job % n_c * Gx::kB, r0 = job / n_c % n_r * Gx::kA, split = job / n_c / n_r;
     const int k0 = int(int64_t(kb) * split / p.splits), k1 = int(int64_t(kb) * (split + 1) / p.splits);
     Gx::run(p.g, r0, p.w, c0, k0, k1, k1 == kb ? p.dx_tail : 4, p.dx_parts, (lds_t*)sm, acc);
-    const float unit = F16 ? ldexpf(1.f, -(kGExp + p.exps->w)) : 1.f;
     const int64_t packed = int64_t(p.g.rb) * kBlk, per = int64_t(p.tw) * kBlk;
 #pragma unroll
     for (int i = 0; i < Gx::kFM; ++i)
@@ -1045,7 +1064,7 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_products(ProductArgs p, 
             for (int e = 0; e < 16; ++e) old[e] = o[acc_row(e, lane) * p.ld];
           }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[acc_row(e, lane) * p.ld] = old[e] + acc[i][j][e] * unit;
+          for (int e = 0; e < 16; ++e) o[acc_row(e, lane) * p.ld] = old[e] + acc[i][j][e];
           continue;
         }
 #pragma unroll
@@ -1053,7 +1072,7 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_products(ProductArgs p, 
           const int64_t row = r + acc_row(e, lane), w = row / per;
           if (c < p.dim && row % per < p.rows)
             put(static_cast<T*>(p.dx) + (w * p.rows + row % per) * p.dim + c,
-                p.info[row].target >= 0 ? acc[i][j][e] * unit * coef_of(p.scale, p.count, w) : 0.f);
+                p.info[row].target >= 0 ? acc[i][j][e] * coef_of(p.scale, p.count, w) : 0.f);
         }
       }
     return;
@@ -1064,7 +1083,6 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_products(ProductArgs p, 
   const int c0 = job % per % n_c * Gw::kB, r0 = job % per / n_c * Gw::kA;
   Gw::run(p.g, r0, p.x, c0, w * p.tw, (w + 1) * p.tw, p.dw_tail, p.dw_parts, (lds_t*)sm, acc);
   const float coef = coef_of(p.scale, p.count, w) * p.x_scale;
-  const float unit = F16 ? ldexpf(1.f, -(kGExp + p.exps->x)) : 1.f;
   GT* out = grads + w * p.stride;
 #pragma unroll
   for (int i = 0; i < Gw::kFM; ++i)
@@ -1088,11 +1106,11 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_products(ProductArgs p, 
       }
       if (n >= 32) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) put(o + acc_row(e, lane) * p.dim, old[e] + acc[i][j][e] * unit * coef);
+        for (int e = 0; e < 16; ++e) put(o + acc_row(e, lane) * p.dim, old[e] + acc[i][j][e] * coef);
       } else {
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (acc_row(e, lane) < n) put(o + acc_row(e, lane) * p.dim, old[e] + acc[i][j][e] * unit * coef);
+          if (acc_row(e, lane) < n) put(o + acc_row(e, lane) * p.dim, old[e] + acc[i][j][e] * coef);
       }
     }
 }
@@ -1512,16 +1530,19 @@ psgd_status make_drop(const char* fn, const psgd_dropout_config* c, Drop* out) {
 }
 
 int parts_of(psgd_dtype t) { return t == PSGD_F32 ? 2 : 1; }
-int g_parts(const psgd_lm_plan* plan) { return plan->act == PSGD_F32 ? 2 : plan->grad == PSGD_F32 ? 3 : 1; }
+int g_parts(const psgd_lm_plan* plan) { return plan->act == PSGD_F32 || plan->grad == PSGD_F32 ? 3 : 1; }
 
 constexpr Parts kOne{1, 0, 0};
-constexpr Parts kF32{3, 0x001, 0x010};        // high x low, low x high, high x high
-constexpr Parts kThreeByOne{3, 0x012, 0x000};  // the smallest part first
+constexpr Parts kF32{3, 0x001, 0x010};        // two fp16 parts each: high x low, low x high, high x high
+// bf16 parts, the smallest products first
+constexpr Parts kThreeByOne{3, 0x012, 0x000};
+constexpr Parts kTwoByTwo{3, 0x010, 0x001};           // for a bf16 result: what is left out is 2^-16 of it
+constexpr Parts kThreeByThree{6, 0x010120, 0x001102};  // all above 2^-24
 
 int32_t steps_of_last(int64_t n) { return int32_t(ceil_div((n - 1) % kBlk + 1, 16)); }
 
 struct Views {
-  Mat x, w;
+  Mat x, w, x3, w3;
   uint16_t* g;
   RowInfo* info;
   int32_t* count;
@@ -1546,6 +1567,11 @@ Views views(const psgd_lm_plan* plan, const void* params, void* workspace, int32
   v.w = plan->direct ? Mat{static_cast<const uint16_t*>(params) + plan->offset, 0, plan->vb, plan->db, int32_t(plan->vocab - 1)}
                      : Mat{reinterpret_cast<uint16_t*>(ws + plan->ws_w), int64_t(plan->vb) * plan->db * kBlkElems, plan->vb,
                            plan->db, 0};
+  v.x3 = v.x, v.w3 = v.w;
+  if (plan->act == PSGD_F32) {
+    v.x3.p = reinterpret_cast<uint16_t*>(ws + plan->ws_x3);
+    v.w3.p = reinterpret_cast<uint16_t*>(ws + plan->ws_w3);
+  }
   return v;
 }
 
@@ -1554,8 +1580,10 @@ const void* table_of(const psgd_lm_plan* plan, const void* params) {
 }
 
 // The packed operands: x in groups of `rows` rows, and the table.  count: NULL for the loss.
+// x3, w3: whether the products with g will read them.
 psgd_status enqueue_pack(psgd_lm_plan* plan, const Views& v, const void* x, const void* params, int64_t rows, int32_t blocks,
-                         const int64_t* targets, const float* lse, int32_t* count, const Drop& d, hipStream_t st) {
+                         const int64_t* targets, const float* lse, int32_t* count, bool x3, bool w3, const Drop& d,
+                         hipStream_t st) {
   const bool f32 = plan->act == PSGD_F32;
   const void* table = table_of(plan, params);
   if (f32) {
@@ -1564,9 +1592,11 @@ psgd_status enqueue_pack(psgd_lm_plan* plan, const Views& v, const void* x, cons
                                  plan->dim, targets, plan->vocab, v.peak);
     if (s != PSGD_OK) return s;
   }
-  PackArgs a{x, table, v.x, v.w, rows, blocks, plan->rows, plan->vocab, int32_t(plan->dim),
+  PackArgs a{x, table, v.x, v.w, v.x3, v.w3, rows, blocks, plan->rows, plan->vocab, int32_t(plan->dim),
              targets, lse, v.info, count, v.peak, v.exps};
   if (plan->direct) a.w_to.p = nullptr;
+  if (!x3) a.x3_to.p = nullptr;
+  if (!w3) a.w3_to.p = nullptr;
   const int64_t jobs = int64_t(v.x.rb) * v.x.cb + (plan->direct ? 0 : int64_t(v.w.rb) * v.w.cb) +
                        (count != nullptr ? plan->n_workers : 0);
   return launch(plan, kPack, f32 ? lm_pack<float> : lm_pack<uint16_t>, dim3(unsigned(jobs)), kThreads, st, a, d);
@@ -1592,7 +1622,7 @@ psgd_status enqueue_loss(psgd_lm_plan* plan, const void* x, const void* params, 
                          float* losses, float* lse, float* mean, void* workspace, hipStream_t st) {
   const int64_t rows = plan->rows * plan->n_workers;
   const Views v = views(plan, params, workspace, plan->tb);
-  psgd_status s = enqueue_pack(plan, v, x, params, rows, plan->tb, targets, nullptr, nullptr, d, st);
+  psgd_status s = enqueue_pack(plan, v, x, params, rows, plan->tb, targets, nullptr, nullptr, false, false, d, st);
   if (s != PSGD_OK) return s;
   const bool f32 = plan->act == PSGD_F32, small = plan->loss_small;
   const int32_t tiles = int32_t(ceil_div(plan->vb, small ? 1 : kTile));
@@ -1617,18 +1647,19 @@ psgd_status enqueue_loss(psgd_lm_plan* plan, const void* x, const void* params, 
                 static_cast<const RowInfo*>(v.info), plan->rows, mean);
 }
 
-template <bool F16, typename GT, bool R>
+template <typename T, typename GT, bool R>
 psgd_status enqueue_products(psgd_lm_plan* plan, const ProductArgs& a, bool small, GT* grads, hipStream_t st) {
   const dim3 grid(unsigned(ceil_div(a.dx_jobs, 8) * 8 + ceil_div(a.dw_jobs, 8) * 8));
-  return small ? launch(plan, kProducts, lm_products<F16, GT, true, R>, grid, 256, st, a, grads)
-               : launch(plan, kProducts, lm_products<F16, GT, false, R>, grid, 512, st, a, grads);
+  return small ? launch(plan, kProducts, lm_products<T, GT, true, R>, grid, 256, st, a, grads)
+               : launch(plan, kProducts, lm_products<T, GT, false, R>, grid, 512, st, a, grads);
 }
 
 psgd_status enqueue_grad(psgd_lm_plan* plan, const void* x, const void* params, const int64_t* targets, const float* lse,
                          const float* scale, const Drop& d, void* dx, void* grads, bool add, void* workspace, hipStream_t st) {
   const int32_t tb = plan->tw * plan->n_workers;
   const Views v = views(plan, params, workspace, tb);
-  psgd_status s = enqueue_pack(plan, v, x, params, plan->rows, plan->tw, targets, lse, v.count, d, st);
+  psgd_status s = enqueue_pack(plan, v, x, params, plan->rows, plan->tw, targets, lse, v.count, grads != nullptr, dx != nullptr,
+                               d, st);
   if (s != PSGD_OK) return s;
   const bool f32 = plan->act == PSGD_F32, f32g = plan->grad == PSGD_F32, direct = plan->direct;
   const float x_scale = x_scale_of(d);
@@ -1649,17 +1680,16 @@ psgd_status enqueue_grad(psgd_lm_plan* plan, const void* x, const void* params, 
     else
       s = direct ? enqueue_scores<kGradBf16, true>(plan, a, small, st) : enqueue_scores<kGradBf16, false>(plan, a, small, st);
     if (s != PSGD_OK) return s;
-    Mat w = v.w;
+    Mat w = v.w3;
     w.p += int64_t(v0) * w.cb * kBlkElems;  // as many elements packed or not
     w.last -= v0 * kBlk;
     w.rb = n_v;
     ProductArgs b{};
     b.g = Mat{v.g, g_part, tb, n_v, 0};
     b.w = w;
-    b.x = v.x;
-    b.dx_parts = f32 ? kF32 : kOne;
-    b.dw_parts = !f32g ? kOne : f32 ? kF32 : kThreeByOne;
-    b.exps = v.exps;
+    b.x = v.x3;
+    b.dx_parts = f32 ? kThreeByThree : kOne;
+    b.dw_parts = f32 ? (f32g ? kThreeByThree : kTwoByTwo) : f32g ? kThreeByOne : kOne;
     b.scale = scale;
     b.count = v.count;
     b.info = v.info;
@@ -1684,11 +1714,11 @@ psgd_status enqueue_grad(psgd_lm_plan* plan, const void* x, const void* params, 
     uint16_t* gb = static_cast<uint16_t*>(grads) + plan->offset;
     const bool few = plan->grad_small;
     if (f32)
-      s = f32g ? enqueue_products<true, float, false>(plan, b, few, gf, st) : enqueue_products<true, uint16_t, false>(plan, b, few, gb, st);
+      s = f32g ? enqueue_products<float, float, false>(plan, b, few, gf, st) : enqueue_products<float, uint16_t, false>(plan, b, few, gb, st);
     else if (direct)
-      s = f32g ? enqueue_products<false, float, true>(plan, b, few, gf, st) : enqueue_products<false, uint16_t, true>(plan, b, few, gb, st);
+      s = f32g ? enqueue_products<uint16_t, float, true>(plan, b, few, gf, st) : enqueue_products<uint16_t, uint16_t, true>(plan, b, few, gb, st);
     else
-      s = f32g ? enqueue_products<false, float, false>(plan, b, few, gf, st) : enqueue_products<false, uint16_t, false>(plan, b, few, gb, st);
+      s = f32g ? enqueue_products<uint16_t, float, false>(plan, b, few, gf, st) : enqueue_products<uint16_t, uint16_t, false>(plan, b, few, gb, st);
     if (s != PSGD_OK) return s;
   }
   if (dx == nullptr || straight) return PSGD_OK;
@@ -1842,6 +1872,10 @@ extern "C" psgd_status psgd_lm_plan_create(const psgd_layer* layers, int32_t n_l
     plan->ws_hit = take(uint64_t(plan->tb) * kBlk * 4);
     const uint64_t loss_end = ws;
     ws = common;
+    if (act_dtype == PSGD_F32) {
+      plan->ws_x3 = take(3 * uint64_t(tbp) * uint64_t(plan->db) * blk);
+      plan->ws_w3 = take(3 * uint64_t(plan->vb) * uint64_t(plan->db) * blk);
+    }
     plan->ws_g = take(gp * uint64_t(tbp) * uint64_t(std::min(plan->piece, plan->vb)) * blk);
     plan->ws_dx = take(uint64_t(plan->splits) * uint64_t(tbp) * kBlk * uint64_t(plan->db) * kBlk * 4);
     const uint64_t grad_end = ws;

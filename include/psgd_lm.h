@@ -34,12 +34,12 @@
  * graph draw new masks; layers are told apart by their seeds.
  *
  * Precision.  Activations (x, out, dout, dx) and params have one type, gradients another or
- * the same, float32 or bfloat16 each.  Products are summed in float32.  float32 matrices enter
- * the matrix cores as two scaled fp16 parts: 22 bits of an entry down to 2^-28 of the largest
- * finite entry of its matrix (x's counted rows, the table), fewer below that and none below
- * 2^-49; g likewise, against 1.  With bfloat16 activations x and the table are taken as they
- * are and g is rounded to bfloat16, but not for a float32 table gradient.  With float32
- * activations and bfloat16 gradients the table gradient's factors have 11 bits.  Everything
+ * the same, float32 or bfloat16 each.  Products are summed in float32.  For the scores float32
+ * matrices enter the matrix cores as two scaled fp16 parts: 22 bits of an entry down to 2^-28 of
+ * the largest finite entry of its matrix (x's counted rows, the table), fewer below that and
+ * none below 2^-49.  For the gradients they and g have all their 24 bits, whatever the other
+ * entries are (16 for a bfloat16 table gradient).  With bfloat16 activations x and the table
+ * are taken as they are and g is rounded to bfloat16, but not for a float32 table gradient.  Everything
  * else is float32, means are taken in float64, results are rounded once.  Sums have a fixed
  * order: equal calls give equal bits.  Non-finite entries are not errors: one in the table, or
  * in a counted row of x, makes what depends on it infinite or NaN (that row's loss, or every
@@ -129,8 +129,7 @@ psgd_status psgd_lm_loss(psgd_lm_plan* plan, const void* x, const void* params, 
                          void* stream);
 
 /* Gradients of every worker's scale * mean:
- *   lse     [n_workers][rows] float32, of psgd_lm_loss on the same x, params and dropout (for
- *           one that is smaller g is larger than 1, and past 4 no number)
+ *   lse     [n_workers][rows] float32, of psgd_lm_loss on the same x, params and dropout
  *   scale   [n_workers] float32, or NULL for 1
  *   dx      [n_workers][rows][dim] act_dtype out, or NULL
  *   grads   [n_workers][worker_stride] grad_dtype, the table's part set or added to, or NULL

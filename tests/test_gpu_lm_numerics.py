@@ -1,0 +1,132 @@
+"""Language-model ends on the GPU: numbers at the ends of their ranges, against the float64 oracle.
+
+Bounds are formed entry by entry as in test_gpu_lm.py, but with no term that grows with entries an
+output does not depend on.  u = 2^-24.  A float32 entry is three bf16 parts, each the nearest to
+what is left: |m| <= 2^-8 |x|, |l| <= 2^-16 |x|, and nothing remains.  The six products that are
+taken leave out m l' + l m' + l l', at most 2.01 u |x x'|; the three that a bfloat16 result takes
+leave out m m' + h l' + l h' and smaller ones, at most 3.1 2^-16 |x x'|."""
+
+import numpy as np
+import pytest
+
+from distributed_sgd_gradient_ef_amd import psgd
+from oracle import lm as O
+from tests.gpu_harness import log
+from tests.test_gpu_lm import HALF, TYPES, U, Case, close
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def torch_gpu():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no ROCm GPU visible")
+    psgd.load_library()
+    return torch
+
+
+def set_case(c, x, table, words):
+    """Other inputs for a case."""
+    t = c.torch
+    c.x.copy_(t.from_numpy(np.ascontiguousarray(x)))
+    c.params[c.span].view(table.shape).copy_(t.from_numpy(np.ascontiguousarray(table)))
+    c.table = c.np(c.params[c.span]).reshape(table.shape)
+    c.words_np = np.asarray(words, dtype=np.int64)
+    c.words.copy_(t.from_numpy(c.words_np))
+
+
+def bounds(c, lse):
+    """(dx, table gradient) of the oracle and their bounds, without dropout and scale."""
+    h, s, ok = O.scores(c.np(c.x), c.table, c.words_np)
+    g, _ = O.score_grad(c.np(c.x), c.table, c.words_np, lse)
+    a, T = np.abs(h), np.abs(c.table)
+    f32 = c.act == "f32"
+    es = (2 * c.n_adds(c.s["dim"]) + (20 if f32 else 8)) * U * (a @ T.T)
+    if f32:  # fp16 parts end 2^-50 below the largest entry of a row
+        es += 2.0 ** -49 * (a.max(-1, keepdims=True) * T.sum(1) + T.max(1) * a.sum(-1, keepdims=True))
+    cc = (ok / np.maximum(1, ok.sum(1, keepdims=True)))[..., None]
+    away = np.where(ok[..., None], s - lse[..., None], 0)
+    eg = cc * np.exp(away) * (np.expm1(es) + 2 * U * (np.abs(away) + 3)) + 4 * U * np.abs(g)
+    eg, gt = np.where(ok[..., None], eg, 0), np.swapaxes(np.abs(g), 1, 2)
+    n_x, n_w = c.n_adds(c.s["vocab"]) + 20, 3 * (-(-c.s["rows"] // 16) + 4)
+    rest_x = 2.1 * U if f32 else HALF["bf16"]
+    rest_w = 2.1 * U if c.grad == "f32" else 3.1 * 2.0 ** -16 if f32 else HALF["bf16"]
+    e_dx = eg @ T + ((2 * n_x + 8) * U + rest_x) * (np.abs(g) @ T)
+    e_gw = np.swapaxes(eg, 1, 2) @ a + ((2 * n_w + 8) * U + rest_w) * (gt @ a)
+    return O.loss_grad(c.np(c.x), c.table, c.words_np, lse), (e_dx, e_gw)
+
+
+def check(c, lse):
+    dx, grads = c.loss_grad(lse)
+    (want_dx, want_g), (e_dx, e_g) = bounds(c, c.np(lse))
+    close("dx", c.np(dx), want_dx, e_dx, c.act)
+    close("grads", c.table_part(grads), want_g, e_g, c.grad)
+
+
+@pytest.mark.parametrize("act,grad", TYPES)
+def test_gradients_of_improbable_words(torch_gpu, act, grad):
+    """Words' probabilities fall from 1 to e^-57; the rows of all of them are relatively exact."""
+    log(f"[case] improbable words, {act} {grad}")
+    V, D, T = 96, 16, 40
+    c = Case(torch_gpu, V, D, 2, T, act, grad, seed=1)
+    rng = np.random.default_rng(11)
+    table = rng.standard_normal((V, D)) * 0.25
+    table[:, 0] = -0.6 * np.arange(V)
+    x = rng.standard_normal((2, T, D))
+    x[..., 0] = 1
+    set_case(c, x, table, rng.integers(0, 8, (2, T)))
+    check(c, c.loss()[1])
+
+
+@pytest.mark.parametrize("act,grad", TYPES)
+def test_gradients_of_columns_of_any_size(torch_gpu, act, grad):
+    """Columns of x and of the table down to 2^-70 of the others keep all their bits in the gradients."""
+    log(f"[case] small columns, {act} {grad}")
+    V, D, T = 70, 36, 50
+    c = Case(torch_gpu, V, D, 2, T, act, grad, seed=2)
+    rng = np.random.default_rng(12)
+    x, table = rng.standard_normal((2, T, D)), rng.standard_normal((V, D)) * 0.5
+    x[..., :14] *= 2.0 ** (-5 * np.arange(1, 15))
+    table[:, 14:28] *= 2.0 ** (-5 * np.arange(1, 15))
+    set_case(c, x, table, rng.integers(0, V, (2, T)))
+    check(c, c.loss()[1])
+
+
+@pytest.mark.parametrize("act,grad", TYPES)
+@pytest.mark.parametrize("less", [1.0, 3.0, 60.0])
+def test_lse_below_the_scores(torch_gpu, act, grad, less):
+    """An lse of other origin that makes g larger than 1."""
+    log(f"[case] lse less by {less}, {act} {grad}")
+    c = Case(torch_gpu, 301, 24, 2, 33, act, grad, seed=3)
+    lse = c.loss()[1]
+    check(c, lse - less)
+
+
+def test_probabilities_next_to_one(torch_gpu):
+    """g of confident rows is p - 1, so p's own error counts.  Scores are exact here (few bits
+    each); the exponent s - lse is small, and so are its two roundings, u |s - lse| log2(e) each,
+    or 3 u p |s - lse| of p; exp2 gives the nearest float32 but one, u for p in 1/2..1.  g's parts
+    and its product with x: (2.1 + 8) u |g x|."""
+    torch = torch_gpu
+    W, V, D = 400, 4, 2
+    log("[case] confident rows")
+    c = Case(torch, V, D, W, 1, seed=4)
+    rng = np.random.default_rng(13)
+    x = rng.integers(24, 33, (W, 1, D)) / 16.0
+    table = np.array([[3.25, 2.5], [1.5, 0.75], [0.25, 1.125], [-1.0, 0.5]])
+    set_case(c, x, table, np.zeros((W, 1)))
+    lse = c.loss()[1]
+    s = (c.np(c.x) @ c.table.T)[:, 0]
+    away = s - c.np(lse)
+    p = np.exp(away)
+    assert (p[:, 0] > 0.9).all() and (p[:, 0] < 1).all()
+    _, grads = c.loss_grad(lse)
+    got = c.table_part(grads)[:, 0, :]  # the target's row of each worker's gradient: (p - 1) x
+    want = (p[:, :1] - 1) * x[:, 0]
+    err = (3 * U * np.abs(away[:, :1]) + U) * np.abs(x[:, 0]) + 10.1 * U * np.abs(want)
+    worst = (np.abs(got - want) / err).max()
+    log(f"   {worst:.3f} of the bound")
+    assert worst <= 1
