@@ -6,13 +6,13 @@
 // zero past a matrix's edges, so that no product loop has an edge of its own.  Operands in
 // float32 are held in parts, and the loop over the contraction runs once per product of two
 // parts:
-// - for the scores they are scaled by a power of two and held as two fp16 parts, x = h + l /
-//   2048; a product of two of them is h l' + l h' (divided by 2048) + h h';
-// - for the products with g, whose entries and whose partners' rows range over any powers of
-//   two, they and g are three bf16 parts, x = h + m + l: every entry has its 24 bits, whatever
+// - for the scores every row, of x and of the table, is scaled by a power of two of its own,
+//   which leaves the contraction, and held as two fp16 parts, x = h + l / 2048; a product of
+//   two of them is h l' + l h' (divided by 2048) + h h';
+// - for the products with g, whose contraction runs over rows, of any sizes, they and g are three bf16 parts, x = h + m + l: every entry has its 24 bits, whatever
 //   the others are.  The six products above 2^-24 take part.
 //
-//   lm_peak    the largest entries of float32 operands
+//   lm_peak    the powers of two of float32 operands' rows
 //   lm_pack    x (through dropout, zero where a row does not count) and the table, packed; the
 //              counted rows of every worker
 //   lm_scores  tiles of T drop(x)^T: their rows' maximum and sum (loss), or g of their entries,
@@ -33,7 +33,6 @@
 #include <hip/hip_ext.h>
 
 #include <algorithm>
-#include <cfloat>
 #include <cmath>
 #include <cstdio>
 #include <string>
@@ -85,7 +84,7 @@ struct psgd_lm_plan {
   int32_t chunk = 0;             // row blocks per chunk in psgd_lm_loss
   bool direct = false;           // the table is read as it is
   bool loss_small = false, scores_small = false, grad_small = false;  // which tiles are the small ones
-  uint64_t ws_x = 0, ws_w = 0, ws_x3 = 0, ws_w3 = 0, ws_peak = 0, ws_exps = 0, ws_info = 0, ws_count = 0, ws_stat = 0, ws_hit = 0, ws_g = 0, ws_dx = 0;
+  uint64_t ws_x = 0, ws_w = 0, ws_x3 = 0, ws_w3 = 0, ws_x_exps = 0, ws_w_exps = 0, ws_info = 0, ws_count = 0, ws_stat = 0, ws_hit = 0, ws_g = 0, ws_dx = 0;
   uint64_t ws_key = 0, ws_key2 = 0, ws_part = 0, workspace_bytes = 0;
   bool timing = false;
   std::vector<psgd::PendingTiming> pending;
@@ -103,6 +102,7 @@ typedef short s4v __attribute__((ext_vector_type(4)));
 typedef short s8v __attribute__((ext_vector_type(8)));
 typedef float f16v __attribute__((ext_vector_type(16)));
 typedef uint32_t u4v __attribute__((ext_vector_type(4)));
+typedef int32_t i4v __attribute__((ext_vector_type(4)));
 
 // ------------------------------------------------------------------ numbers
 __device__ __forceinline__ float widen(uint16_t b) { return __uint_as_float(uint32_t(b) << 16); }
@@ -531,18 +531,12 @@ __device__ __forceinline__ int acc_row(int i, int lane) { return 8 * (i >> 2) + 
 struct RowInfo {
   int32_t target;  // -1: the row does not count
   float hi, lo;    // lse * kLog2e
-  float pad;
+  int32_t exp;     // float32: the row's power of two
 };
 
 constexpr float kLog2e = 1.44269504f;
 
-// float32 operands: their powers of two.  An operand is scaled so that its largest finite
-// entry lies in [2^14, 2^15): its fp16 parts hold 22 bits of entries down to 2^-28 of it.
-struct Scales {
-  int32_t w, x;  // of the table, of x
-};
-
-constexpr int kPeakW = 768, kPeakX = 256;  // workgroups that look for the largest entry
+constexpr int kPeakGroups = 2048;  // workgroups of lm_peak: all that fit the chip at once
 
 template <typename F>
 __device__ __forceinline__ F block_sum(F x, F* sm) {
@@ -557,67 +551,57 @@ __device__ __forceinline__ F block_sum(F x, F* sm) {
 
 __device__ __forceinline__ bool counts(int64_t target, int64_t vocab) { return uint64_t(target) < uint64_t(vocab); }
 
-// Largest finite magnitude (as its bits) of p[begin, end), by threads `id` of `of`.
-__device__ __forceinline__ uint32_t peak_of(const float* p, int64_t begin, int64_t end, int id, int of) {
+// Largest finite magnitude (as its bits) that dropout leaves of the n entries at p, the first of
+// them entry `first`, by threads `id` of `of`.
+__device__ __forceinline__ uint32_t peak_of(const float* p, int64_t n, int id, int of, bool dropped, const Drop& d,
+                                            uint64_t step, uint64_t first) {
   uint32_t m = 0;
-  for (int64_t i = begin + id * 4; i < end; i += of * 16) {
+  for (int64_t i = id * 4; i < n; i += of * 16) {
     float v[4][4] = {};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int64_t at = i + k * of * 4;
-      if (at + 4 <= end) {
+      if (at + 4 <= n) {
         load<4>(p + at, v[k]);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (at + e < end) v[k][e] = p[at + e];
+          if (at + e < n) v[k][e] = p[at + e];
       }
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 4; ++k) {
+      if (dropped && i + k * of * 4 < n) drop<4>(d, step, first + uint64_t(i + k * of * 4), 1.f, v[k]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint32_t u = __float_as_uint(v[k][e]) & 0x7fffffffu;
         m = max(m, u < 0x7f800000u ? u : 0u);
       }
+    }
   }
   return m;
 }
 
-// The largest magnitude of every part of the table (a workgroup each), and of x's rows that count
-// (a wave takes a row at a time): what the others hold must not matter.  Bound by memory: 87 MB
-// of table and 15 MB of x in 15 to 18 us (256 workgroups without loads in flight: 34).
-__global__ __launch_bounds__(kThreads) void lm_peak(const float* table, int64_t n_table, const float* x, int64_t rows,
-                                                    int64_t dim, const int64_t* targets, int64_t vocab, uint32_t* peak) {
-  __shared__ uint32_t sm[kThreads / 64];
-  const int job = blockIdx.x, wave = threadIdx.x >> 6;
-  uint32_t m = 0;
-  if (job < kPeakW) {
-    const int64_t per = (n_table + kPeakW * 4 - 1) / (kPeakW * 4) * 4;
-    m = peak_of(table, job * per, min(n_table, (job + 1) * per), threadIdx.x, kThreads);
-  } else {
-    for (int64_t r = (job - kPeakW) * (kThreads / 64) + wave; r < rows; r += kPeakX * (kThreads / 64))
-      if (counts(targets[r], vocab)) m = max(m, peak_of(x, r * dim, (r + 1) * dim, threadIdx.x & 63, 64));
+// The power of two of every row of the table (0 past the vocabulary, up to `padded` words) and
+// of every row of x that counts: it brings the largest finite entry that dropout leaves into
+// [2^14, 2^15), so the row's fp16 parts hold 22 bits of entries down to 2^-28 of that one.  One
+// power for a whole matrix would let the largest entry of one row, or one that is dropped, take
+// bits from every other worker's rows.  `lanes` lanes (a power of two up to 64) take a row.
+// Bound by memory.
+__global__ __launch_bounds__(kThreads) void lm_peak(const float* table, int64_t vocab, int64_t padded, const float* x,
+                                                    int64_t rows, int64_t dim, const int64_t* targets, int32_t lanes,
+                                                    int32_t* w_exps, int32_t* x_exps, Drop d) {
+  const int id = threadIdx.x & (lanes - 1), per = kThreads / lanes;
+  const uint64_t step = d.on ? step_of(d) : 0;
+  for (int64_t job = int64_t(blockIdx.x) * per + threadIdx.x / lanes; job < padded + rows; job += int64_t(gridDim.x) * per) {
+    const bool of_x = job >= padded;
+    const int64_t r = of_x ? job - padded : job;
+    uint32_t m = 0;
+    if (of_x ? counts(targets[r], vocab) : r < vocab)
+      m = peak_of((of_x ? x : table) + r * dim, dim, id, lanes, of_x && d.on, d, step, uint64_t(r) * uint64_t(dim));
+    for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, uint32_t(__shfl_xor(int(m), o)));
+    if (id == 0) (of_x ? x_exps : w_exps)[r] = m != 0 ? 14 - ilogbf(__uint_as_float(m)) : 0;
   }
-  for (int o = 32; o > 0; o >>= 1) m = max(m, uint32_t(__shfl_xor(int(m), o)));
-  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
-  __syncthreads();
-  if (threadIdx.x != 0) return;
-  for (int i = 1; i < kThreads / 64; ++i) m = max(m, sm[i]);
-  peak[job] = m;
-}
-
-// The power of two that brings the largest of `n` peaks into [2^14, 2^15).
-__device__ __forceinline__ int32_t power_of_two(const uint32_t* peak, int n) {
-  __shared__ uint32_t sm[kThreads / 64];
-  uint32_t m = 0;
-  for (int i = threadIdx.x; i < n; i += kThreads) m = max(m, peak[i]);
-  for (int o = 32; o > 0; o >>= 1) m = max(m, uint32_t(__shfl_xor(int(m), o)));
-  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = m;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kThreads / 64; ++i) m = max(m, sm[i]);
-  return m != 0 ? 14 - ilogbf(__uint_as_float(m)) : 0;
 }
 
 // What every row of a worker's g is multiplied by.
@@ -638,8 +622,7 @@ struct PackArgs {
   const float* lse;      // NULL for the loss
   RowInfo* info;
   int32_t* count;        // counted rows of every worker, or NULL
-  const uint32_t* peak;  // float32 operands
-  Scales* exps;
+  const int32_t *x_exps, *w_exps;  // float32 operands
 };
 
 // One block per workgroup: those of x (through dropout, but not scaled: the products' results
@@ -668,21 +651,18 @@ __global__ __launch_bounds__(kThreads) void lm_pack(PackArgs p, Drop d) {
   const Mat &to = of_x ? p.x_to : p.w_to, &to3 = of_x ? p.x3_to : p.w3_to;
   const bool dropped = of_x && d.on;
   const uint64_t step = dropped ? step_of(d) : 0;
-  int32_t exp2 = 0;
-  if constexpr (sizeof(T) == 4) {
-    exp2 = power_of_two(of_x ? p.peak + kPeakW : p.peak, of_x ? kPeakX : kPeakW);
-    if (threadIdx.x == 0 && block == 0) (of_x ? p.exps->x : p.exps->w) = exp2;
-  }
 #pragma unroll
   for (int it = 0; it < 2; ++it) {
     const int r = it * 32 + int(threadIdx.x) / 8, c = c0 + int(threadIdx.x % 8) * 8;
     const int64_t t = t0 + r, row = w * rows + t;
     bool on = t < rows;
+    int32_t exp = 0;
     if (of_x) {
       const int64_t target = on ? p.targets[row] : -1;
       on = counts(target, p.vocab);
+      if (sizeof(T) == 4 && on) exp = p.x_exps[row];
       if (c == 0) {
-        RowInfo ri{on ? int32_t(target) : -1, 0.f, 0.f, 0.f};
+        RowInfo ri{on ? int32_t(target) : -1, 0.f, 0.f, exp};
         if (on && p.lse != nullptr) {
           const double l = double(p.lse[row]) * double(kLog2e);
           ri.hi = float(l);
@@ -690,6 +670,8 @@ __global__ __launch_bounds__(kThreads) void lm_pack(PackArgs p, Drop d) {
         }
         p.info[rb * kBlk + r] = ri;
       }
+    } else if (sizeof(T) == 4 && on) {
+      exp = p.w_exps[t];
     }
     float x[8] = {};
     if (on && c < p.dim) {
@@ -710,7 +692,7 @@ __global__ __launch_bounds__(kThreads) void lm_pack(PackArgs p, Drop d) {
     for (int e = 0; e < 8; ++e) {
       uint16_t a = 0, b = 0;
       if constexpr (sizeof(T) == 2) a = narrow_bits(x[e]);
-      else split16(ldexpf(x[e], exp2), a, b);
+      else split16(ldexpf(x[e], exp), a, b);
       h[e] = short(a), l[e] = short(b);
     }
     *reinterpret_cast<s8v*>(o) = h;
@@ -768,7 +750,7 @@ struct ScoreArgs {
   int32_t t0, t1;        // row blocks
   int64_t vocab;
   const RowInfo* info;   // from row block 0 on
-  const Scales* exps;    // float32 operands
+  const int32_t* w_exps;  // float32 operands
   float x_scale;         // dropout's
   float2* stat;          // loss: [vocabulary tile][row of the launch] maximum and sum
   float* hit;            // loss: [row] the target's score
@@ -810,9 +792,25 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_scores(ScoreArgs p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave / G::kWN, wn = wave % G::kWN;
   const int64_t word0 = int64_t(v0) * kBlk + wm * G::kRowsA;  // of this wave
   const int n_words = int(min(int64_t(G::kRowsA), p.vocab - word0));  // may be negative
-  float unit = p.x_scale;  // a score is an accumulator times this
-  if constexpr (kF16) unit = ldexpf(unit, -(p.exps->x + p.exps->w));
-  const float c = fmaxf(kLog2e * unit, FLT_MIN);
+  const float unit = p.x_scale, c = kLog2e * unit;  // a score is an accumulator times this
+  if constexpr (kF16) {  // after the powers of two of its row and its word, whose sum is taken first: neither overflows alone
+    int32_t of_row[G::kFN];
+#pragma unroll
+    for (int j = 0; j < G::kFN; ++j) {
+      const int at = wn * G::kRowsB + j * 32 + (lane & 31);
+      of_row[j] = t0 + at / kBlk < p.t1 ? p.info[int64_t(t0) * kBlk + at].exp : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < G::kFM; ++i)
+#pragma unroll
+      for (int e4 = 0; e4 < 4; ++e4) {
+        const i4v of_word = *reinterpret_cast<const i4v*>(p.w_exps + word0 + i * 32 + e4 * 8 + (lane >> 5) * 4);
+#pragma unroll
+        for (int j = 0; j < G::kFN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e4 * 4 + e] = ldexpf(acc[i][j][e4 * 4 + e], -(of_word[e] + of_row[j]));
+      }
+  }
   if constexpr (KIND == kLossBf16 || KIND == kLossF32) {
     float2* joined = reinterpret_cast<float2*>(sm);  // the main loop ends in a barrier: its LDS is free
 #pragma unroll
@@ -872,7 +870,7 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_scores(ScoreArgs p) {
 #pragma unroll
     for (int j = 0; j < G::kFN; ++j) {
       const int at = wn * G::kRowsB + j * 32 + (lane & 31);
-      RowInfo ri{-1, 0.f, 0.f, 0.f};
+      RowInfo ri{-1, 0.f, 0.f, 0};
       if (t0 + at / kBlk < p.t1) ri = p.info[int64_t(t0) * kBlk + at];
       const bool on = ri.target >= 0;
       const int64_t local = ri.target - word0;
@@ -1546,8 +1544,7 @@ struct Views {
   uint16_t* g;
   RowInfo* info;
   int32_t* count;
-  uint32_t* peak;
-  Scales* exps;
+  int32_t *x_exps, *w_exps;
   float2* stat;
   float *hit, *dx;
 };
@@ -1558,8 +1555,8 @@ Views views(const psgd_lm_plan* plan, const void* params, void* workspace, int32
   v.g = reinterpret_cast<uint16_t*>(ws + plan->ws_g);
   v.info = reinterpret_cast<RowInfo*>(ws + plan->ws_info);
   v.count = reinterpret_cast<int32_t*>(ws + plan->ws_count);
-  v.peak = reinterpret_cast<uint32_t*>(ws + plan->ws_peak);
-  v.exps = reinterpret_cast<Scales*>(ws + plan->ws_exps);
+  v.x_exps = reinterpret_cast<int32_t*>(ws + plan->ws_x_exps);
+  v.w_exps = reinterpret_cast<int32_t*>(ws + plan->ws_w_exps);
   v.stat = reinterpret_cast<float2*>(ws + plan->ws_stat);
   v.hit = reinterpret_cast<float*>(ws + plan->ws_hit);
   v.dx = reinterpret_cast<float*>(ws + plan->ws_dx);
@@ -1575,6 +1572,9 @@ Views views(const psgd_lm_plan* plan, const void* params, void* workspace, int32
   return v;
 }
 
+// Words of whole large tiles, as lm_scores reads their powers of two.
+int64_t padded_words(int64_t vb) { return ceil_div(vb, kTile) * kTile * kBlk; }
+
 const void* table_of(const psgd_lm_plan* plan, const void* params) {
   return static_cast<const char*>(params) + plan->offset * (plan->act == PSGD_F32 ? 4 : 2);
 }
@@ -1587,13 +1587,17 @@ psgd_status enqueue_pack(psgd_lm_plan* plan, const Views& v, const void* x, cons
   const bool f32 = plan->act == PSGD_F32;
   const void* table = table_of(plan, params);
   if (f32) {
-    const psgd_status s = launch(plan, kPeak, lm_peak, dim3(kPeakW + kPeakX), kThreads, st, static_cast<const float*>(table),
-                                 plan->vocab * plan->dim, static_cast<const float*>(x), plan->rows * plan->n_workers,
-                                 plan->dim, targets, plan->vocab, v.peak);
+    int32_t lanes = 1;
+    while (lanes < 64 && lanes * 4 < plan->dim) lanes *= 2;
+    const int64_t padded = padded_words(plan->vb), n = plan->rows * plan->n_workers;
+    const int64_t groups = std::min<int64_t>(kPeakGroups, ceil_div((padded + n) * lanes, kThreads));
+    const psgd_status s = launch(plan, kPeak, lm_peak, dim3(unsigned(groups)), kThreads, st, static_cast<const float*>(table),
+                                 plan->vocab, padded, static_cast<const float*>(x), n, plan->dim, targets, lanes, v.w_exps,
+                                 v.x_exps, d);
     if (s != PSGD_OK) return s;
   }
   PackArgs a{x, table, v.x, v.w, v.x3, v.w3, rows, blocks, plan->rows, plan->vocab, int32_t(plan->dim),
-             targets, lse, v.info, count, v.peak, v.exps};
+             targets, lse, v.info, count, v.x_exps, v.w_exps};
   if (plan->direct) a.w_to.p = nullptr;
   if (!x3) a.x3_to.p = nullptr;
   if (!w3) a.w3_to.p = nullptr;
@@ -1632,7 +1636,7 @@ psgd_status enqueue_loss(psgd_lm_plan* plan, const void* x, const void* params, 
   while (at > 16 && kThreads / at < tiles) at /= 2;
   for (int32_t t0 = 0; t0 < plan->tb; t0 += plan->chunk) {
     const ScoreArgs a{v.w, v.x, f32 ? kF32 : kOne, steps_of_last(plan->dim), 0, plan->vb, t0, std::min(plan->tb, t0 + plan->chunk),
-                      plan->vocab, v.info, v.exps, x_scale_of(d), v.stat, v.hit, nullptr, 0};
+                      plan->vocab, v.info, v.w_exps, x_scale_of(d), v.stat, v.hit, nullptr, 0};
     s = f32 ? enqueue_scores<kLossF32, false>(plan, a, small, st)
             : plan->direct ? enqueue_scores<kLossBf16, true>(plan, a, small, st) : enqueue_scores<kLossBf16, false>(plan, a, small, st);
     if (s != PSGD_OK) return s;
@@ -1670,7 +1674,7 @@ psgd_status enqueue_grad(psgd_lm_plan* plan, const void* x, const void* params, 
   for (int32_t v0 = 0; v0 < plan->vb; v0 += plan->piece) {
     const int32_t v1 = std::min(plan->vb, v0 + plan->piece), n_v = v1 - v0;
     const int64_t g_part = int64_t(tb) * n_v * kBlkElems;
-    const ScoreArgs a{v.w, v.x, f32 ? kF32 : kOne, steps_of_last(plan->dim), v0, v1, 0, tb, plan->vocab, v.info, v.exps, x_scale,
+    const ScoreArgs a{v.w, v.x, f32 ? kF32 : kOne, steps_of_last(plan->dim), v0, v1, 0, tb, plan->vocab, v.info, v.w_exps, x_scale,
                       nullptr, nullptr, v.g, g_part};
     const bool small = plan->scores_small;
     if (f32)
@@ -1862,8 +1866,10 @@ extern "C" psgd_status psgd_lm_plan_create(const psgd_layer* layers, int32_t n_l
       return at;
     };
     plan->ws_x = take(p * uint64_t(tbp) * uint64_t(plan->db) * blk);
-    plan->ws_peak = take((kPeakW + kPeakX) * sizeof(uint32_t));
-    plan->ws_exps = take(sizeof(Scales));
+    if (act_dtype == PSGD_F32) {
+      plan->ws_x_exps = take(uint64_t(n) * 4);
+      plan->ws_w_exps = take(uint64_t(padded_words(plan->vb)) * 4);
+    }
     plan->ws_w = take(plan->direct ? 0 : p * uint64_t(plan->vb) * uint64_t(plan->db) * blk);
     plan->ws_info = take(uint64_t(tbp) * kBlk * sizeof(RowInfo));
     plan->ws_count = take(uint64_t(n_workers) * 4);

@@ -35,9 +35,9 @@
  *
  * Precision.  Activations (x, out, dout, dx) and params have one type, gradients another or
  * the same, float32 or bfloat16 each.  Products are summed in float32.  For the scores float32
- * matrices enter the matrix cores as two scaled fp16 parts: 22 bits of an entry down to 2^-28 of
- * the largest finite entry of its matrix (x's counted rows, the table), fewer below that and
- * none below 2^-49.  For the gradients they and g have all their 24 bits, whatever the other
+ * matrices enter the matrix cores as two fp16 parts of rows scaled by their own powers of two: 22
+ * bits of an entry down to 2^-28 of the largest finite entry of its row (of those that dropout
+ * keeps), fewer below that and none below 2^-49; what other rows hold does not matter.  For the gradients they and g have all their 24 bits, whatever the other
  * entries are (16 for a bfloat16 table gradient).  With bfloat16 activations x and the table
  * are taken as they are and g is rounded to bfloat16, but not for a float32 table gradient.  Everything
  * else is float32, means are taken in float64, results are rounded once.  Sums have a fixed

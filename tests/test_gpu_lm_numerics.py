@@ -130,3 +130,40 @@ def test_probabilities_next_to_one(torch_gpu):
     worst = (np.abs(got - want) / err).max()
     log(f"   {worst:.3f} of the bound")
     assert worst <= 1
+
+
+def everything(c):
+    out = list(c.loss())
+    return out + list(c.loss_grad(out[1]))
+
+
+@pytest.mark.parametrize("act,grad", TYPES)
+@pytest.mark.parametrize("junk", [1e30, -3e38, float("inf"), float("nan")])
+def test_dropped_entries_may_hold_anything(torch_gpu, act, grad, junk):
+    torch = torch_gpu
+    drop = (0.3, 17, 5)
+    log(f"[case] {junk} where x is dropped, {act} {grad}")
+    c = Case(torch, 500, 37, 2, 70, act, grad, drop=drop, seed=6)
+    off = torch.from_numpy(~O.kept(tuple(c.x.shape), *drop)).to(DEV)
+    c.x[off] = 0
+    want = everything(c)
+    c.x[off] = junk
+    for a, b in zip(want, everything(c)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("act,grad", TYPES)
+def test_a_huge_entry_of_one_word_costs_no_other(torch_gpu, act, grad):
+    """A table entry of 2^60 that only meets zeros: every score stays as it was."""
+    torch = torch_gpu
+    log(f"[case] a huge table entry, {act} {grad}")
+    c = Case(torch, 400, 33, 2, 50, act, grad, seed=7)
+    c.x[..., 0] = 0
+    table = c.params[c.span].view(400, 33)
+    table[5] = 0
+    want = everything(c)
+    table[5, 0] = 2.0 ** 60
+    got = everything(c)
+    for i in (0, 1, 2, 4):
+        assert torch.equal(want[i], got[i])
+    assert torch.equal(want[3][..., 1:], got[3][..., 1:])
