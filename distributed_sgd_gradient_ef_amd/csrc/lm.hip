@@ -526,11 +526,10 @@ struct Gemm {
 __device__ __forceinline__ int acc_row(int i, int lane) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
 
 // ------------------------------------------------------------------ rows and packing
-// What the score tiles need of a packed row.  exp(s - lse) is taken as
-// exp2(s log2(e) - (hi + lo)), with the float32 next to log2(e) in both places.
+// What the score tiles need of a packed row.
 struct RowInfo {
   int32_t target;  // -1: the row does not count
-  float hi, lo;    // lse * kLog2e
+  float lse;
   int32_t exp;     // float32: the row's power of two
 };
 
@@ -662,13 +661,7 @@ __global__ __launch_bounds__(kThreads) void lm_pack(PackArgs p, Drop d) {
       on = counts(target, p.vocab);
       if (sizeof(T) == 4 && on) exp = p.x_exps[row];
       if (c == 0) {
-        RowInfo ri{on ? int32_t(target) : -1, 0.f, 0.f, exp};
-        if (on && p.lse != nullptr) {
-          const double l = double(p.lse[row]) * double(kLog2e);
-          ri.hi = float(l);
-          ri.lo = fabs(l) < 1e38 ? float(l - double(ri.hi)) : 0.f;
-        }
-        p.info[rb * kBlk + r] = ri;
+        p.info[rb * kBlk + r] = RowInfo{on ? int32_t(target) : -1, on && p.lse != nullptr ? p.lse[row] : 0.f, exp};
       }
     } else if (sizeof(T) == 4 && on) {
       exp = p.w_exps[t];
@@ -753,10 +746,17 @@ struct ScoreArgs {
   const int32_t* w_exps;  // float32 operands
   float x_scale;         // dropout's
   float2* stat;          // loss: [vocabulary tile][row of the launch] maximum and sum
-  float* hit;            // loss: [row] the target's score
+  float* hit;            // loss: [row] the target's score; as the maxima without x_scale
   uint16_t* g;           // gradient: blocks [t1 - t0][v1 - v0]
   int64_t g_part;
 };
+
+// A score as a float32 of its own: lse is one too, and where a row has one score that matters
+// their difference has to be 0, however large they are.
+__device__ __forceinline__ float score_of(float acc, float unit) {
+#pragma clang fp contract(off)
+  return acc * unit;
+}
 
 // What a launch of lm_scores leaves.  g lacks its row's factor scale / counted, which is one for
 // all rows of a worker: the products' results are multiplied by it.
@@ -769,15 +769,17 @@ enum ScoreKind {
 
 // Scores of a tile of words x rows: lane l of a wave holds words in its accumulators and row
 // l mod 32 of each of its pieces, so a row's maximum and sum are taken within a lane, then
-// over its two lane halves and the two waves that share the row.  Maxima and sums are those of
-// exp2 of s log2(e): m the largest of them, and sum exp2(s log2(e) - m).
+// over its two lane halves and the two waves that share the row: m the largest, and the sum of
+// exp(s - m).  An exponent is always the difference of two scores, rounded once, times log2(e):
+// multiplied first (one fused multiply-add an exponential), the rounding of m log2(e) reaches
+// the sum whole, 2^-24 |m| of it, and past 2^31 a finite score gives an infinite one.
 //
 // Bound by the matrix cores and the card's power: 131,072 x 2048 for 4096 rows in bfloat16
 // takes 1.83 to 1.95 ms (box to box), 1.2 PFLOP/s with the exponentials; the library's product
 // alone, which keeps its scores, 1.65 (1.33 PFLOP/s).  The matrix cores are busy for 56% of
 // the cycles at 1.7 GHz, there 75% at 1.5 GHz.  What got it here, in us: operands through
 // registers 2113, straight into LDS 1907, LDS reads with one wait per 16 contraction steps
-// 1798, one fused multiply-add per exponential.  Four waves of 128 x 128: 2856.
+// 1798.  Four waves of 128 x 128: 2856.
 template <int KIND, bool SMALL, bool R>
 __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_scores(ScoreArgs p) {
   constexpr bool kF16 = KIND == kLossF32 || KIND == kGradF32;
@@ -826,7 +828,7 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_scores(ScoreArgs p) {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             if (i * 32 + acc_row(e, lane) == int(local)) hit = acc[i][j][e];
-        if (here) p.hit[row] = hit * unit;
+        if (here) p.hit[row] = hit;
       }
       if (n_words < G::kRowsA) {
 #pragma unroll
@@ -840,13 +842,13 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_scores(ScoreArgs p) {
       for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e) m = fmaxf(m, acc[i][j][e]);
-      m = fmaxf(m, __shfl_xor(m, 32)) * c;
+      m = fmaxf(m, __shfl_xor(m, 32));
       const float base = m == -INFINITY ? 0.f : m;
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], c, -base));
+        for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f((acc[i][j][e] - base) * c);
       s += __shfl_xor(s, 32);
       if (lane < 32) joined[wm * kRows + at] = make_float2(m, s);
     }
@@ -858,7 +860,7 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_scores(ScoreArgs p) {
       for (int k = 1; k < G::kWM; ++k) {
         const float2 b = joined[k * kRows + r];
         const float m = fmaxf(a.x, b.x), base = m == -INFINITY ? 0.f : m;
-        a = make_float2(m, a.y * __builtin_amdgcn_exp2f(a.x - base) + b.y * __builtin_amdgcn_exp2f(b.x - base));
+        a = make_float2(m, a.y * __builtin_amdgcn_exp2f((a.x - base) * c) + b.y * __builtin_amdgcn_exp2f((b.x - base) * c));
       }
       p.stat[int64_t(vt) * (p.t1 - p.t0) * kBlk + int64_t(tt) * kRows + r] = a;
     }
@@ -870,7 +872,7 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_scores(ScoreArgs p) {
 #pragma unroll
     for (int j = 0; j < G::kFN; ++j) {
       const int at = wn * G::kRowsB + j * 32 + (lane & 31);
-      RowInfo ri{-1, 0.f, 0.f, 0};
+      RowInfo ri{-1, 0.f, 0};
       if (t0 + at / kBlk < p.t1) ri = p.info[int64_t(t0) * kBlk + at];
       const bool on = ri.target >= 0;
       const int64_t local = ri.target - word0;
@@ -878,7 +880,7 @@ __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_scores(ScoreArgs p) {
 #pragma unroll
       for (int i = 0; i < G::kFM; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) g[i][j][e] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], c, -ri.hi) - ri.lo);
+        for (int e = 0; e < 16; ++e) g[i][j][e] = __builtin_amdgcn_exp2f((score_of(acc[i][j][e], unit) - ri.lse) * kLog2e);
       if (__any(here)) {
 #pragma unroll
         for (int i = 0; i < G::kFM; ++i)
@@ -937,6 +939,7 @@ struct RowsArgs {
   int64_t ld;           // rows per tile in stat
   const RowInfo* info;
   const float* hit;
+  float x_scale;
   int64_t rows;
   float *losses, *lse;
   float* mean;          // of each workgroup's rows, or NULL
@@ -953,13 +956,14 @@ __global__ __launch_bounds__(kThreads) void lm_rows(RowsArgs p) {
   const int r = threadIdx.x % p.at, part = threadIdx.x / p.at, parts = kThreads / p.at;
   const int64_t first = p.mean != nullptr ? blockIdx.x * p.rows : int64_t(blockIdx.x) * p.at;
   const int64_t end = p.mean != nullptr ? first + p.rows : min(p.rows, first + p.at);
+  const float c = kLog2e * p.x_scale;
   double sum = 0.0, n = 0.0;
   for (int64_t row0 = first; row0 < end; row0 += p.at) {
     const int64_t row = row0 + r;
     float m = -INFINITY, s = 0.f;
     auto join = [&](const float2& a) {
       const float top = fmaxf(m, a.x), base = top == -INFINITY ? 0.f : top;
-      s = s * __builtin_amdgcn_exp2f(m - base) + a.y * __builtin_amdgcn_exp2f(a.x - base);
+      s = s * __builtin_amdgcn_exp2f((m - base) * c) + a.y * __builtin_amdgcn_exp2f((a.x - base) * c);
       m = top;
     };
     if (row < end) {
@@ -971,8 +975,9 @@ __global__ __launch_bounds__(kThreads) void lm_rows(RowsArgs p) {
     if (part == 0 && row < end) {
       for (int i = 1; i < parts; ++i) join(sm[i * p.at + r]);
       const bool on = p.info[row].target >= 0;
-      const float l = float((double(m) + double(log2f(s))) / double(kLog2e)), loss = on ? l - p.hit[row] : 0.f;
-      p.lse[row] = on ? l : 0.f;
+      const double ln = double(logf(s));
+      const float loss = on ? float((double(m) - double(p.hit[row])) * double(p.x_scale) + ln) : 0.f;  // not less than 0
+      p.lse[row] = on ? float(double(m) * double(p.x_scale) + ln) : 0.f;
       p.losses[row] = loss;
       if (on) sum += double(loss), n += 1.0;
     }
@@ -1641,7 +1646,7 @@ psgd_status enqueue_loss(psgd_lm_plan* plan, const void* x, const void* params, 
             : plan->direct ? enqueue_scores<kLossBf16, true>(plan, a, small, st) : enqueue_scores<kLossBf16, false>(plan, a, small, st);
     if (s != PSGD_OK) return s;
     const int64_t r0 = int64_t(t0) * kBlk, n = one ? plan->rows : std::min(rows, int64_t(a.t1) * kBlk) - r0;
-    const RowsArgs b{v.stat, tiles, int64_t(a.t1 - t0) * kBlk, v.info + r0, v.hit + r0, n, losses + r0, lse + r0,
+    const RowsArgs b{v.stat, tiles, int64_t(a.t1 - t0) * kBlk, v.info + r0, v.hit + r0, a.x_scale, n, losses + r0, lse + r0,
                      one ? mean : nullptr, at};
     s = launch(plan, kRows, lm_rows, dim3(unsigned(one ? plan->n_workers : ceil_div(n, at))), kThreads, st, b);
     if (s != PSGD_OK) return s;

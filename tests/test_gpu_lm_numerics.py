@@ -167,3 +167,66 @@ def test_a_huge_entry_of_one_word_costs_no_other(torch_gpu, act, grad):
     for i in (0, 1, 2, 4):
         assert torch.equal(want[i], got[i])
     assert torch.equal(want[3][..., 1:], got[3][..., 1:])
+
+
+@pytest.mark.parametrize("act,grad", TYPES)
+@pytest.mark.parametrize("vocab,dim,rows,p", [(300, 40, 50, 0.0), (300, 40, 50, 0.3), (9001, 130, 700, 0.0)])
+def test_a_worker_with_huge_entries_changes_no_other(torch_gpu, act, grad, vocab, dim, rows, p):
+    """One worker's activations grow by 2^40: the others' results keep their bits."""
+    torch = torch_gpu
+    log(f"[case] a huge worker, {vocab} x {dim}, {rows} rows, p {p}, {act} {grad}")
+    c = Case(torch, vocab, dim, 3, rows, act, grad, drop=(p, 3, 4), seed=5)
+    before = everything(c)
+    c.x[1] *= 2.0 ** 40
+    after = everything(c)
+    for a, b in zip(before, after):
+        assert torch.isfinite(b).all()
+        for w in (0, 2):
+            assert torch.equal(a[w], b[w])
+    assert not torch.equal(before[0][1], after[0][1])
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("p", [0.0, 0.1, 0.2, 0.3, 0.5])
+def test_losses_of_confident_rows(torch_gpu, act, p):
+    """Scores of up to 45 whose target leads by 5 to 15.  The products are exact here (few bits), so
+    differences of two scores are too, up to their factor: the float32 next to 1 / (1 - p), u / 2,
+    and that next to log2(e), u / 4, their product's rounding u and the difference's times it, u:
+    below 3 u |s - top| of an exponential; its own rounding is 2 u.  The sum of 5 is off by 5 u of
+    itself, its logarithm by 2 u (1 + loss)."""
+    torch = torch_gpu
+    drop = (p, 21, 7)
+    log(f"[case] confident rows, p {p}, {act}")
+    W, T, V, D = 2, 300, 5, 4
+    c = Case(torch, V, D, W, T, act, act, drop=drop, seed=9)
+    rng = np.random.default_rng(19)
+    x = rng.integers(40, 64, (W, T, D)) / 16.0
+    table = np.array([[3.0, 2.5, 3.0, 2.75], [1.5, 0.75, 2.0, 0.25], [0.25, 1.125, 0.5, 0.0], [-1.0, 0.5, 1.0, 1.0],
+                      [1.0, 1.5, 0.25, 0.5]])
+    set_case(c, x, table, np.where(rng.random((W, T)) < 0.9, 0, 1))
+    losses, lse, mean = (c.np(t) for t in c.loss())
+    h, s, _ = O.scores(c.np(c.x), c.table, c.words_np, drop)
+    want, want_lse, want_mean = O.loss(c.np(c.x), c.table, c.words_np, drop)
+    away = s.max(-1, keepdims=True) - s
+    hit = np.take_along_axis(away, c.words_np[..., None], -1)[..., 0]
+    err = (np.exp(s - want_lse[..., None]) * (3 * U * away + 2 * U)).sum(-1) + 5 * U + 3 * U * (1 + want) + U * hit
+    worst = (np.abs(losses - want) / err).max()
+    log(f"   losses {worst:.3f} of the bound, the smallest {want.min():.2g}")
+    assert worst <= 1 and (losses >= 0).all() and want.min() < 1e-4
+    assert (np.abs(mean - want_mean) <= err.mean(1) + U * want_mean).all()
+    assert (np.abs(lse - want_lse) <= err + 2 * U * np.abs(want_lse)).all()
+
+
+@pytest.mark.parametrize("act,grad", TYPES)
+def test_losses_are_not_negative(torch_gpu, act, grad):
+    """Rows that lean far towards their targets: the loss is 0 or more, and finite."""
+    torch = torch_gpu
+    log(f"[case] certain rows, {act}")
+    c = Case(torch, 700, 130, 2, 90, act, grad, seed=10, bad=0.0, drop=(0.1, 2, 3))
+    table = c.params[c.span].view(700, 130)
+    for lean in (10.0, 100.0, 1e6, 1e12):
+        c.x.copy_(lean * table[c.words].float())
+        losses, lse, mean = c.loss()
+        assert (losses >= 0).all() and torch.isfinite(losses).all() and torch.isfinite(lse).all() and (mean >= 0).all()
+        dx, grads = c.loss_grad(lse)
+        assert torch.isfinite(dx).all() and torch.isfinite(grads).all()
