@@ -64,6 +64,8 @@ constexpr int kSortThreads = 512;
 constexpr int kRun = 16;           // sorted pairs summed by one wave ...
 constexpr int kRunLoads = 8;       // ... whose rows are loaded so many at a time
 constexpr int kZeroUnits = 4;      // 16-byte stores of a thread that zeroes
+constexpr int64_t kMostGroups = int64_t(1) << 23;  // workgroups of a launch of psgd_dropout: HIP takes below 2^32 threads
+constexpr int64_t kMostEntries = int64_t(1) << 41;  // of psgd_dropout, below it: 1024 launches at most
 
 enum KernelId {
   kPeak = 0, kPack, kScores, kRows, kMean, kProducts, kDxOut, kEmbed, kSort, kMerge, kSum, kJoin, kNumK
@@ -1412,7 +1414,8 @@ struct DropArgs {
   void* out;
   int64_t xs, rs, os;  // strides
   int64_t n, cols;
-  Div groups;  // VEC: groups of N entries per row; otherwise cols
+  int64_t first;  // the launch's first group of N entries
+  Div groups;     // VEC: groups of N entries per row; otherwise cols
 };
 
 // N consecutive entries per thread.  VEC: they lie in one row (cols is a multiple of N); 16-byte
@@ -1420,7 +1423,7 @@ struct DropArgs {
 // element, with a 64-bit division per thread, 155.
 template <typename T, int N, bool VEC>
 __global__ __launch_bounds__(kThreads) void lm_dropout(DropArgs p, Drop d) {
-  const int64_t group = int64_t(blockIdx.x) * kThreads + threadIdx.x, i = group * N;
+  const int64_t group = p.first + int64_t(blockIdx.x) * kThreads + threadIdx.x, i = group * N;
   if (i >= p.n) return;
   const T* x = static_cast<const T*>(p.x);
   const T* residual = static_cast<const T*>(p.residual);
@@ -1754,9 +1757,16 @@ Div divide_by(uint64_t d) {
 }
 
 template <typename T, int N, bool VEC>
-void enqueue_dropout(DropArgs a, const Drop& d, hipStream_t st) {
+psgd_status enqueue_dropout(DropArgs a, const Drop& d, hipStream_t st) {
   a.groups = divide_by(uint64_t(VEC ? a.cols / N : a.cols));
-  hipLaunchKernelGGL((lm_dropout<T, N, VEC>), dim3(unsigned(ceil_div(a.n, kThreads * N))), dim3(kThreads), 0, st, a, d);
+  const int64_t all = ceil_div(a.n, kThreads * N);
+  for (int64_t at = 0; at < all; at += kMostGroups) {
+    a.first = at * kThreads;
+    hipLaunchKernelGGL((lm_dropout<T, N, VEC>), dim3(unsigned(std::min(kMostGroups, all - at))), dim3(kThreads), 0, st, a, d);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return hip_fail("launch lm_dropout", e);
+  }
+  return PSGD_OK;
 }
 
 int32_t sort_size(int64_t rows) {
@@ -2111,8 +2121,7 @@ extern "C" psgd_status psgd_dropout(const void* x, int64_t x_stride, const void*
     const int64_t far = std::max({x_stride, residual_stride, out_stride});
     if (std::min({x_stride, residual_stride, out_stride}) < cols || far > (int64_t(1) << 60) / rows)
       return fail(PSGD_ERR_INVALID_ARG, "psgd_dropout: a stride is less than cols, or its rows span over 2^60 elements");
-    if (rows * cols > int64_t(0x7fffffff) * kThreads * 4)
-      return fail(PSGD_ERR_INVALID_ARG, "psgd_dropout: rows * cols is too large for one launch");
+    if (rows * cols >= kMostEntries) return fail(PSGD_ERR_INVALID_ARG, "psgd_dropout: rows * cols must be below 2^41");
     const unsigned e = unsigned(size_of(dtype));
     auto span = [&](const char* name, const void* p, int64_t stride, bool nullable) {
       return ArgSpan{name, p, (uint64_t(rows - 1) * uint64_t(stride) + uint64_t(cols)) * e, e, nullable};
@@ -2127,13 +2136,9 @@ extern "C" psgd_status psgd_dropout(const void* x, int64_t x_stride, const void*
       if ((s = check_spans(fn, three, 3, same ? 0 : -1, same ? 1 : -1)) != PSGD_OK) return s;
     }
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    DropArgs a{x, residual, out, x_stride, residual_stride, out_stride, rows * cols, cols, Div{}};
-    if (dtype == PSGD_F32)
-      cols % 4 == 0 ? enqueue_dropout<float, 4, true>(a, d, st) : enqueue_dropout<float, 4, false>(a, d, st);
-    else
-      cols % 8 == 0 ? enqueue_dropout<uint16_t, 8, true>(a, d, st) : enqueue_dropout<uint16_t, 4, false>(a, d, st);
-    const hipError_t err = hipGetLastError();
-    return err == hipSuccess ? PSGD_OK : hip_fail("launch lm_dropout", err);
+    DropArgs a{x, residual, out, x_stride, residual_stride, out_stride, rows * cols, cols, 0, Div{}};
+    if (dtype == PSGD_F32) return cols % 4 == 0 ? enqueue_dropout<float, 4, true>(a, d, st) : enqueue_dropout<float, 4, false>(a, d, st);
+    return cols % 8 == 0 ? enqueue_dropout<uint16_t, 8, true>(a, d, st) : enqueue_dropout<uint16_t, 4, false>(a, d, st);
   } catch (...) {
     return no_memory();
   }

@@ -230,3 +230,22 @@ def test_losses_are_not_negative(torch_gpu, act, grad):
         assert (losses >= 0).all() and torch.isfinite(losses).all() and torch.isfinite(lse).all() and (mean >= 0).all()
         dx, grads = c.loss_grad(lse)
         assert torch.isfinite(dx).all() and torch.isfinite(grads).all()
+
+
+@pytest.mark.parametrize("rows,cols,act,per", [
+    (262147, 65537, "bf16", 4), (524291, 65536, "bf16", 8), (262147, 65536, "f32", 4)])
+def test_dropout_past_one_launch(torch_gpu, rows, cols, act, per):
+    """Past 2^32 threads' entries, in place: both sides of every border between launches, and the end."""
+    torch = torch_gpu
+    n = rows * cols
+    log(f"[case] dropout of {n} {act} entries, in place")
+    assert n > per << 32
+    x = torch.ones((rows, cols), dtype=torch.bfloat16 if act == "bf16" else torch.float32, device=DEV)
+    psgd.psgd_dropout(x, None, x, psgd.DropoutConfig(0.5, 99))
+    flat = x.view(-1)
+    for first in (0, per * 2 ** 31 - 4096, per * 2 ** 31, per * 2 ** 32 - 4096, per * 2 ** 32, n // 4 * 4 - 8192):
+        m = min(8192, n - first)
+        want = O.kept((m,), 0.5, 99, 0, first) * 2.0
+        assert np.array_equal(flat[first:first + m].float().cpu().numpy(), want), first
+    del x, flat
+    torch.cuda.empty_cache()
