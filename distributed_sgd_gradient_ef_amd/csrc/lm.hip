@@ -64,6 +64,7 @@ constexpr int kSortThreads = 512;
 constexpr int kRun = 16;           // sorted pairs summed by one wave ...
 constexpr int kRunLoads = 8;       // ... whose rows are loaded so many at a time
 constexpr int kZeroUnits = 4;      // 16-byte stores of a thread that zeroes
+constexpr int64_t kZeroGroups = 65536;  // workgroups that zero, at most: HIP takes below 2^32 threads a launch
 constexpr int64_t kMostGroups = int64_t(1) << 23;  // workgroups of a launch of psgd_dropout: HIP takes below 2^32 threads
 constexpr int64_t kMostEntries = int64_t(1) << 41;  // of psgd_dropout, below it: 1024 launches at most
 
@@ -1192,24 +1193,25 @@ constexpr uint64_t kNoToken = 0xffffffffull;
 
 // The first workgroups each sort one chunk of a worker's pairs (bitonic: a fixed network on
 // distinct keys, 55 steps of a barrier each: 14 us for 1024 pairs, 50 for 4096); the others zero
-// the tables that are not added to (537 MB in 98 us), which hides the sort.
+// the tables that are not added to (537 MB in 98 us), 32 KB at a time in turn, which hides the sort.
 template <typename GT>
 __global__ __launch_bounds__(kSortThreads) void lm_sort(const int64_t* tokens, int64_t rows, int64_t vocab, int32_t size,
                                                         uint64_t* keys, int32_t chunks, int32_t workers, GT* table, int64_t n,
-                                                        int64_t stride) {
+                                                        int64_t stride, int64_t zeros) {
   __shared__ uint64_t sm[kSortMax];
   if (int(blockIdx.x) >= chunks * workers) {
     constexpr int kV = 16 / sizeof(GT);
-    const int64_t job = int64_t(blockIdx.x) - chunks * workers;
     const int64_t per = (n + kSortThreads * kZeroUnits * kV - 1) / (kSortThreads * kZeroUnits * kV);
-    GT* t = table + job / per * stride;
+    for (int64_t job = int64_t(blockIdx.x) - chunks * workers; job < zeros; job += int64_t(gridDim.x) - chunks * workers) {
+      GT* t = table + job / per * stride;
 #pragma unroll
-    for (int u = 0; u < kZeroUnits; ++u) {
-      const int64_t i = ((job % per * kZeroUnits + u) * kSortThreads + threadIdx.x) * kV;
-      if (i + kV <= n) {
-        __builtin_nontemporal_store(u4v{}, reinterpret_cast<u4v*>(t + i));
-      } else {
-        for (int64_t e = i; e < n; ++e) t[e] = GT(0);
+      for (int u = 0; u < kZeroUnits; ++u) {
+        const int64_t i = ((job % per * kZeroUnits + u) * kSortThreads + threadIdx.x) * kV;
+        if (i + kV <= n) {
+          __builtin_nontemporal_store(u4v{}, reinterpret_cast<u4v*>(t + i));
+        } else {
+          for (int64_t e = i; e < n; ++e) t[e] = GT(0);
+        }
       }
     }
     return;
@@ -1785,8 +1787,9 @@ psgd_status enqueue_embed_grad(psgd_lm_plan* plan, const int64_t* tokens, const 
   const int32_t size = sort_size(plan->rows);
   const int64_t n = plan->vocab * plan->dim, chunks = ceil_div(plan->rows, size);
   const int64_t zeros = add ? 0 : ceil_div(n, kSortThreads * kZeroUnits * (16 / int64_t(sizeof(GT)))) * plan->n_workers;
-  psgd_status s = launch(plan, kSort, lm_sort<GT>, dim3(unsigned(chunks * plan->n_workers + zeros)), kSortThreads, st, tokens,
-                         plan->rows, plan->vocab, size, keys, int32_t(chunks), plan->n_workers, table, n, plan->worker_stride);
+  psgd_status s = launch(plan, kSort, lm_sort<GT>, dim3(unsigned(chunks * plan->n_workers + std::min(zeros, kZeroGroups))),
+                         kSortThreads, st, tokens, plan->rows, plan->vocab, size, keys, int32_t(chunks), plan->n_workers, table, n,
+                         plan->worker_stride, zeros);
   for (int64_t run = size; s == PSGD_OK && run < plan->rows; run *= 2) {
     s = launch(plan, kMerge, lm_merge, dim3(unsigned(ceil_div(plan->rows, kThreads)), W), kThreads, st,
                static_cast<const uint64_t*>(keys), other, plan->rows, run);
