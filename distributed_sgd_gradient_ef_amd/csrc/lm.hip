@@ -1361,7 +1361,8 @@ __global__ __launch_bounds__(64) void lm_sum(SumArgs p, const T* dout, GT* table
 }
 
 // The tokens whose pairs start in this run and go on after it: as far as the runs begin with
-// them; kRunLoads runs are looked at together.
+// them; kRunLoads runs are looked at together.  The runs' parts are added up in float64: a token
+// can fill 2^19 of them, and as many roundings to float32 of a sum that grows would be seen.
 template <typename GT, bool WIDE>
 __global__ __launch_bounds__(64) void lm_join(SumArgs p, GT* table) {
   const int64_t w = blockIdx.z, run = blockIdx.x, i0 = run * kRun, i1 = i0 + kRun;
@@ -1374,9 +1375,10 @@ __global__ __launch_bounds__(64) void lm_join(SumArgs p, GT* table) {
   if (n <= 0) return;
   const float* part = p.part + w * p.n_runs * 2 * p.dpad + c;
   table += w * p.stride + int64_t(token) * p.dim;
-  float sum[4], old[4] = {};
-  load<4>(part + (run * 2 + 1) * p.dpad, sum);
+  float first[4], old[4] = {};
+  load<4>(part + (run * 2 + 1) * p.dpad, first);
   if (p.add) load_row<WIDE>(table, c, p.dim, old);
+  double sum[4] = {first[0], first[1], first[2], first[3]};
   bool goes_on = true;
   for (int64_t r = run + 1; goes_on; r += kRunLoads) {
     uint64_t key[kRunLoads];
@@ -1391,10 +1393,11 @@ __global__ __launch_bounds__(64) void lm_join(SumArgs p, GT* table) {
     for (int u = 0; u < kRunLoads; ++u) {
       goes_on = goes_on && r + u < p.n_runs && key[u] >> 32 == token;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum[e] += goes_on ? x[u][e] : 0.f;
+      for (int e = 0; e < 4; ++e) sum[e] += goes_on ? double(x[u][e]) : 0.0;
     }
   }
-  write_row(table + c, n, old, sum);
+  const float all[4] = {float(sum[0]), float(sum[1]), float(sum[2]), float(sum[3])};
+  write_row(table + c, n, old, all);
 }
 
 // ------------------------------------------------------------------ dropout

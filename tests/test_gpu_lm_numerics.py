@@ -249,3 +249,31 @@ def test_dropout_past_one_launch(torch_gpu, rows, cols, act, per):
         assert np.array_equal(flat[first:first + m].float().cpu().numpy(), want), first
     del x, flat
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("same", [True, False])
+@pytest.mark.parametrize("act,grad,dim", [("f32", "f32", 7), ("bf16", "f32", 3), ("bf16", "bf16", 9)])
+def test_one_word_in_a_million_rows(torch_gpu, act, grad, dim, same):
+    """A padding word's gradient: a float32 sum of at most 16 rows at a time (15 roundings, u each),
+    those in float64, one more rounding, and its type's."""
+    torch = torch_gpu
+    log(f"[case] one word in 2^20 rows, equal rows {same}, {act} {grad}")
+    V, T = 5, 1 << 20
+    plan = psgd.psgd_lm_plan_create([(V, dim)], 0, 1, T, psgd.PSGD_BF16 if act == "bf16" else psgd.PSGD_F32,
+                                    psgd.PSGD_BF16 if grad == "bf16" else psgd.PSGD_F32)
+    dout = torch.rand((T, dim), device=DEV, generator=torch.Generator(DEV).manual_seed(1)) + 0.5
+    if same:
+        dout[:] = dout[0].clone()
+    dout = dout.to(torch.bfloat16 if act == "bf16" else torch.float32)
+    tokens = torch.full((1, T), 3, dtype=torch.int64, device=DEV)
+    tokens[0, :5] = torch.tensor([0, 1, -1, 4, 0], device=DEV)
+    grads = torch.full((1, plan.sizes["worker_stride"]), float("nan"), dtype=torch.bfloat16 if grad == "bf16" else torch.float32,
+                       device=DEV)
+    ws = torch.empty(plan.sizes["workspace_bytes"], dtype=torch.uint8, device=DEV)
+    psgd.psgd_lm_embed_grad(plan, tokens, dout, None, grads, 0, ws)
+    d = dout.double()
+    got, want = grads[0, 3 * dim:4 * dim].double(), d[5:].sum(0)
+    worst = float(((got - want).abs() / ((17 * U + HALF[grad]) * want)).max())
+    log(f"   {worst:.3f} of the bound")
+    assert worst <= 1
+    assert torch.equal(grads[0, 4 * dim:5 * dim].float(), dout[3].to(grads.dtype).float()) and not grads[0, 2 * dim:3 * dim].any()
