@@ -1601,7 +1601,7 @@ psgd_status enqueue_pack(psgd_lm_plan* plan, const Views& v, const void* x, cons
   const void* table = table_of(plan, params);
   if (f32) {
     int32_t lanes = 1;
-    while (lanes < 64 && lanes * 4 < plan->dim) lanes *= 2;
+    while (lanes < 64 && lanes * 16 < plan->dim) lanes *= 2;
     const int64_t padded = padded_words(plan->vb), n = plan->rows * plan->n_workers;
     const int64_t groups = std::min<int64_t>(kPeakGroups, ceil_div((padded + n) * lanes, kThreads));
     const psgd_status s = launch(plan, kPeak, lm_peak, dim3(unsigned(groups)), kThreads, st, static_cast<const float*>(table),
