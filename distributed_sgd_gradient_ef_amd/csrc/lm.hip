@@ -63,6 +63,7 @@ constexpr int kSortMax = 1024;     // pairs sorted by one workgroup
 constexpr int kSortThreads = 512;
 constexpr int kRun = 16;           // sorted pairs summed by one wave ...
 constexpr int kRunLoads = 8;       // ... whose rows are loaded so many at a time
+constexpr int kJoinWaves = 4;      // waves that join a token's runs
 constexpr int kZeroUnits = 4;      // 16-byte stores of a thread that zeroes
 constexpr int64_t kZeroGroups = 65536;  // workgroups that zero, at most: HIP takes below 2^32 threads a launch
 constexpr int64_t kMostGroups = int64_t(1) << 23;  // workgroups of a launch of psgd_dropout: HIP takes below 2^32 threads
@@ -1361,42 +1362,58 @@ __global__ __launch_bounds__(64) void lm_sum(SumArgs p, const T* dout, GT* table
 }
 
 // The tokens whose pairs start in this run and go on after it: as far as the runs begin with
-// them; kRunLoads runs are looked at together.  The runs' parts are added up in float64: a token
-// can fill 2^19 of them, and as many roundings to float32 of a sum that grows would be seen.
+// them.  kRunLoads runs are looked at together, by one of kJoinWaves waves in turn, so that a word
+// that fills many runs (a padding word) is no chain of one wave; the waves' sums are joined in
+// their order.  The runs' parts are added up in float64: a token can fill 2^19 of them, and as
+// many roundings to float32 of a sum that grows would be seen.  16,384 rows of 2048 bfloat16, words
+// drawn as in text and one word in all: 10 and 60 us (one wave: 27 and 386; eight: 16 and 42).
 template <typename GT, bool WIDE>
-__global__ __launch_bounds__(64) void lm_join(SumArgs p, GT* table) {
+__global__ __launch_bounds__(64 * kJoinWaves) void lm_join(SumArgs p, GT* table) {
+  __shared__ double sums[kJoinWaves][4][64];
   const int64_t w = blockIdx.z, run = blockIdx.x, i0 = run * kRun, i1 = i0 + kRun;
   const uint64_t* keys = p.keys + w * p.rows;
   if (i1 >= p.rows) return;
   const uint64_t token = pair_at(keys, i1 - 1) >> 32;
   if (token == kNoToken || pair_at(keys, i1) >> 32 != token || (i0 > 0 && pair_at(keys, i0 - 1) >> 32 == token)) return;
-  const int32_t c = (int32_t(blockIdx.y) * 64 + int32_t(threadIdx.x)) * 4;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int32_t c = (int32_t(blockIdx.y) * 64 + lane) * 4;
   const int n = min(4, p.dim - c);
-  if (n <= 0) return;
-  const float* part = p.part + w * p.n_runs * 2 * p.dpad + c;
+  const float* part = p.part + w * p.n_runs * 2 * p.dpad + (n > 0 ? c : 0);
   table += w * p.stride + int64_t(token) * p.dim;
-  float first[4], old[4] = {};
-  load<4>(part + (run * 2 + 1) * p.dpad, first);
-  if (p.add) load_row<WIDE>(table, c, p.dim, old);
-  double sum[4] = {first[0], first[1], first[2], first[3]};
-  bool goes_on = true;
-  for (int64_t r = run + 1; goes_on; r += kRunLoads) {
-    uint64_t key[kRunLoads];
-    float x[kRunLoads][4];
-#pragma unroll
-    for (int u = 0; u < kRunLoads; ++u) {
-      const int64_t at = min(r + u, int64_t(p.n_runs) - 1);
-      key[u] = pair_at(keys, at * kRun);
-      load<4>(part + at * 2 * p.dpad, x[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < kRunLoads; ++u) {
-      goes_on = goes_on && r + u < p.n_runs && key[u] >> 32 == token;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sum[e] += goes_on ? double(x[u][e]) : 0.0;
-    }
+  float first[4] = {}, old[4] = {};
+  if (wave == 0) {
+    load<4>(part + (run * 2 + 1) * p.dpad, first);
+    if (p.add && n > 0) load_row<WIDE>(table, c, p.dim, old);
   }
-  const float all[4] = {float(sum[0]), float(sum[1]), float(sum[2]), float(sum[3])};
+  double sum[4] = {first[0], first[1], first[2], first[3]};
+  auto begins = [&](int64_t r) { return pair_at(keys, min(r, int64_t(p.n_runs) - 1) * kRun) >> 32 == token && r < p.n_runs; };
+  constexpr int kStep = kJoinWaves * kRunLoads;
+  int64_t r = run + 1 + wave * kRunLoads;
+  for (bool goes_on = begins(r); goes_on; r += kStep) {
+    const bool more = begins(r + kStep);
+    float x[kRunLoads][4];
+    bool in[kRunLoads];
+#pragma unroll
+    for (int u = 0; u < kRunLoads; ++u) {
+      in[u] = begins(r + u);
+      load<4>(part + min(r + u, int64_t(p.n_runs) - 1) * 2 * p.dpad, x[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kRunLoads; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += in[u] ? double(x[u][e]) : 0.0;
+    goes_on = more;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sums[wave][e][lane] = sum[e];
+  __syncthreads();
+  if (wave > 0 || n <= 0) return;
+  float all[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    for (int k = 1; k < kJoinWaves; ++k) sum[e] += sums[k][e][lane];
+    all[e] = float(sum[e]);
+  }
   write_row(table + c, n, old, all);
 }
 
@@ -1806,7 +1823,7 @@ psgd_status enqueue_embed_grad(psgd_lm_plan* plan, const int64_t* tokens, const 
   const bool wide = plan->dim >= 4;
   s = launch(plan, kSum, wide ? lm_sum<T, GT, true> : lm_sum<T, GT, false>, grid, 64, st, a, dout, table, d);
   if (s != PSGD_OK || runs == 1) return s;
-  return launch(plan, kJoin, wide ? lm_join<GT, true> : lm_join<GT, false>, grid, 64, st, a, table);
+  return launch(plan, kJoin, wide ? lm_join<GT, true> : lm_join<GT, false>, grid, 64 * kJoinWaves, st, a, table);
 }
 
 }  // namespace
