@@ -54,9 +54,9 @@ constexpr int kThreads = 256;      // of the kernels around the products
 constexpr int kGroup = 16;         // row blocks that take turns on one vocabulary tile (lm_scores)
 constexpr int64_t kFewStats = 16384;  // maxima and sums of a worker that one workgroup takes in
 constexpr int kSplitBlocks = 8;    // vocabulary blocks of a split of lm_products' dx, at least
-// g of one piece of the vocabulary.  64, 128, 256, 512, 1024 MB: gradients of 33,278 x 650, 8 x 700
-// rows float32 3.57, 3.24, 2.79, 2.65, 2.63 ms; of 65,536 x 2048, 2 x 2048 rows bfloat16 3.65, 3.49,
-// 3.19, 3.12, 3.12 (each piece adds to all of dx, and the last tiles of a launch run alone).
+// g of one piece of the vocabulary.  256, 512, 1024, 2048 MB: gradients of 33,278 x 650, 8 x 700
+// rows float32 4.47, 4.39, 4.27, 4.35 ms; of 65,536 x 2048, 2 x 2048 rows bfloat16 3.22, 3.20,
+// 3.21, 3.20 (64 MB: 3.65; each piece adds to all of dx, and the last tiles of a launch run alone).
 constexpr int64_t kPieceBytes = int64_t(512) << 20;
 constexpr int64_t kStatBytes = int64_t(64) << 20;    // maxima and sums of one chunk of rows
 constexpr int kSortMax = 1024;     // pairs sorted by one workgroup
@@ -84,7 +84,7 @@ struct psgd_lm_plan {
   int64_t vocab = 0, dim = 0, rows = 0, worker_stride = 0, offset = 0;
   int32_t vb = 0, db = 0;        // blocks of the table
   int32_t tb = 0, tw = 0;        // blocks of all rows together, and of one worker's rows
-  int32_t piece = 0, splits = 1;  // blocks of the vocabulary per piece, splits of its sum in lm_dx
+  int32_t piece = 0, splits = 1;  // blocks of the vocabulary per piece, splits of dx's sum over one
   int32_t chunk = 0;             // row blocks per chunk in psgd_lm_loss
   bool direct = false;           // the table is read as it is
   bool loss_small = false, scores_small = false, grad_small = false;  // which tiles are the small ones
@@ -244,9 +244,9 @@ struct Gemm {
   static constexpr int kLds = 2 * kStage;
   // The small score tiles have registers for a sum of its own for each quarter of a block's
   // steps: shorter sums round less, and an error of a score of 40 reaches exp(s - lse) whole.
-  // Distance of table gradients from float64, 1, 2 and 4 sums: 2 x 19 rows of 21,396 x 1532 1.0,
-  // 0.39, 0.21e-5; 3 x 127 rows of 1429 x 1323 8.0, 4.2, 2.4e-6; 403 rows' loss over 14,070 x
-  // 259 takes 27, 27, 30 us.
+  // Distance of table gradients from float64, 1, 2 and 4 sums: 2 x 19 rows of 21,396 x 1532 8.0,
+  // 4.7, 2.1e-6; 3 x 127 rows of 1429 x 1323 8.2, 4.1, 2.6e-6; 403 rows' loss over 14,070 x 259
+  // in float32 takes 46, 46, 48 us.
   static constexpr int kSums = FM == 1 && !TA && !TB ? 4 : 1;
   static constexpr int kRowsA = FM * 32, kRowsB = FN * 32;  // of a wave
   typedef f16v Acc[FM][FN];
@@ -713,9 +713,9 @@ __global__ __launch_bounds__(kThreads) void lm_pack(PackArgs p, Drop d) {
 // ------------------------------------------------------------------ scores
 // Tile sizes: 256 x 256 by eight waves where that gives at least kFewTiles tiles, and else
 // 64 x 64 by four, so that small problems still spread over the chip.  us a call for bounds of
-// 64, 128, 256 and 512 tiles: loss of 8000 x 512, 512 rows 83, 21, 21, 21; of 16,000 x 300, 1024
-// rows 31, 31, 40, 40; of 32,000 x 1024, 1024 rows 77, 76, 76, 113; gradients of 4000 x 300, 1000
-// rows float32 90, 66, 65, 65; of 32,000 x 1024, 512 rows 129, 130, 144, 194.
+// 64, 128, 256 and 512 tiles: loss of 8000 x 512, 512 rows 86, 24, 24, 24; of 16,000 x 300, 1024
+// rows 31, 30, 45, 46; of 32,000 x 1024, 1024 rows 74, 75, 76, 128; gradients of 4000 x 300, 1000
+// rows float32 126, 100, 100, 100; of 32,000 x 1024, 512 rows 129, 129, 153, 203.
 constexpr int64_t kFewTiles = 128;
 
 template <bool SMALL, bool TA, bool TB, bool F16, bool RA, bool RB>
@@ -766,9 +766,12 @@ __device__ __forceinline__ float score_of(float acc, float unit) {
 // all rows of a worker: the products' results are multiplied by it.
 enum ScoreKind {
   kLossBf16, kLossF32,
-  kGradBf16,   // g in bf16
-  kGradBf16x3,  // g in three bf16 parts
-  kGradF32     // the same, of float32 operands
+  // g in bf16, the type that the caller chose for activations and gradients: an entry is off by up to
+  // 2^-8 of itself, as much as dx's and the table gradient's own rounding.  More parts take more
+  // products: with three for the table gradient, 65,536 x 2048, 2 x 2048 rows 3.05 -> 5.2 ms.
+  kGradBf16,
+  kGradBf16x3,  // in three bf16 parts, for a float32 table gradient (dx, in bfloat16, takes the first)
+  kGradF32      // in three bf16 parts, of float32 operands
 };
 
 // Scores of a tile of words x rows: lane l of a wave holds words in its accumulators and row
@@ -783,9 +786,10 @@ enum ScoreKind {
 // alone, which keeps its scores, 1.65 (1.33 PFLOP/s).  The matrix cores are busy for 56% of
 // the cycles at 1.7 GHz, there 75% at 1.5 GHz.  What got it here, in us: operands through
 // registers 2113, straight into LDS 1907, LDS reads with one wait per 16 contraction steps
-// 1798.  Four waves of 128 x 128: 2856.
+// 1798.  Four waves of 128 x 128: 2856.  The small tiles are held to the registers of three waves
+// a SIMD: 403 rows' loss over 14,070 x 259 in float32 59 -> 48 us.
 template <int KIND, bool SMALL, bool R>
-__global__ __launch_bounds__(SMALL ? 256 : 512) void lm_scores(ScoreArgs p) {
+__global__ __launch_bounds__(SMALL ? 256 : 512, SMALL ? 3 : 2) void lm_scores(ScoreArgs p) {
   constexpr bool kF16 = KIND == kLossF32 || KIND == kGradF32;
   typedef Tile<SMALL, false, false, kF16, R, false> G;
   constexpr int kRows = G::kB * kBlk;  // of the tile
@@ -1035,8 +1039,8 @@ struct ProductArgs {
 // that the chip does not run empty between them.
 //
 // Bound by the matrix cores as lm_scores where rows and dim are long: 65,536 x 2048 for 2 x 2048
-// rows in bfloat16 2.0 ms, 1.1 PFLOP/s for both.  Tiles side by side on one XCD: 2.85 -> 2.79 ms
-// for a call on 33,278 x 650, 8 x 700 rows.  By memory where a worker has few rows: for 16 x
+// rows in bfloat16 2.0 ms, 1.1 PFLOP/s for both.  Tiles side by side on one XCD: 4.39 -> 4.22 ms
+// for a call on 33,278 x 650, 8 x 700 rows in float32.  By memory where a worker has few rows: for 16 x
 // 148 rows 55,650 x 292, 1.04 GB of float32 added to in 1.26 ms (a piece's old values loaded
 // one after the other: 2.35).
 template <typename T, typename GT, bool SMALL, bool R>
