@@ -590,15 +590,15 @@ __device__ __forceinline__ uint32_t peak_of(const float* p, int64_t n, int id, i
 // [2^14, 2^15), so the row's fp16 parts hold 22 bits of entries down to 2^-28 of that one.  One
 // power for a whole matrix would let the largest entry of one row, or one that is dropped, take
 // bits from every other worker's rows.  `lanes` lanes (a power of two up to 64) take a row.
-// Bound by memory.
+// Bound by memory: 87 MB of table and 15 MB of x in 23 us, 25 through dropout.
 __global__ __launch_bounds__(kThreads) void lm_peak(const float* table, int64_t vocab, int64_t padded, const float* x,
                                                     int64_t rows, int64_t dim, const int64_t* targets, int32_t lanes,
                                                     int32_t* w_exps, int32_t* x_exps, Drop d) {
   const int id = threadIdx.x & (lanes - 1), per = kThreads / lanes;
   const uint64_t step = d.on ? step_of(d) : 0;
   for (int64_t job = int64_t(blockIdx.x) * per + threadIdx.x / lanes; job < padded + rows; job += int64_t(gridDim.x) * per) {
-    const bool of_x = job >= padded;
-    const int64_t r = of_x ? job - padded : job;
+    const bool of_x = job < rows;  // first, as dropout makes them the longer ones
+    const int64_t r = of_x ? job : job - rows;
     uint32_t m = 0;
     if (of_x ? counts(targets[r], vocab) : r < vocab)
       m = peak_of((of_x ? x : table) + r * dim, dim, id, lanes, of_x && d.on, d, step, uint64_t(r) * uint64_t(dim));
@@ -631,7 +631,7 @@ struct PackArgs {
 // One block per workgroup: those of x (through dropout, but not scaled: the products' results
 // are; zero where a row does not count), those of the table, and after them one workgroup per
 // worker that counts its rows.  Bound by memory: 33,278 x 650 and 5600 rows in float32, 102 MB
-// read and 108 MB written, in 41 us (for the loss).
+// read and 108 MB written, in 40 us; with the bf16 parts, 270 MB, in 72.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void lm_pack(PackArgs p, Drop d) {
   const int32_t cb = p.x_to.cb;
