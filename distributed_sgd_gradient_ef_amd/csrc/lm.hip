@@ -9,8 +9,9 @@
 // - for the scores every row, of x and of the table, is scaled by a power of two of its own,
 //   which leaves the contraction, and held as two fp16 parts, x = h + l / 2048; a product of
 //   two of them is h l' + l h' (divided by 2048) + h h';
-// - for the products with g, whose contraction runs over rows, of any sizes, they and g are three bf16 parts, x = h + m + l: every entry has its 24 bits, whatever
-//   the others are.  The six products above 2^-24 take part.
+// - for the products with g, whose contraction runs over rows, of any sizes, they and g are
+//   three bf16 parts, x = h + m + l: every entry has its 24 bits, whatever the others are.  The
+//   six products above 2^-24 take part.
 //
 //   lm_peak    the powers of two of float32 operands' rows
 //   lm_pack    x (through dropout, zero where a row does not count) and the table, packed; the
@@ -67,7 +68,7 @@ constexpr int kJoinWaves = 4;      // waves that join a token's runs
 constexpr int kZeroUnits = 4;      // 16-byte stores of a thread that zeroes
 constexpr int64_t kZeroGroups = 65536;  // workgroups that zero, at most: HIP takes below 2^32 threads a launch
 constexpr int64_t kMostGroups = int64_t(1) << 23;  // workgroups of a launch of psgd_dropout: HIP takes below 2^32 threads
-constexpr int64_t kMostEntries = int64_t(1) << 41;  // of psgd_dropout, below it: 1024 launches at most
+constexpr int64_t kMostEntries = int64_t(1) << 41;  // of psgd_dropout, below it: 256 launches at most
 
 enum KernelId {
   kPeak = 0, kPack, kScores, kRows, kMean, kProducts, kDxOut, kEmbed, kSort, kMerge, kSum, kJoin, kNumK
@@ -88,7 +89,8 @@ struct psgd_lm_plan {
   int32_t chunk = 0;             // row blocks per chunk in psgd_lm_loss
   bool direct = false;           // the table is read as it is
   bool loss_small = false, scores_small = false, grad_small = false;  // which tiles are the small ones
-  uint64_t ws_x = 0, ws_w = 0, ws_x3 = 0, ws_w3 = 0, ws_x_exps = 0, ws_w_exps = 0, ws_info = 0, ws_count = 0, ws_stat = 0, ws_hit = 0, ws_g = 0, ws_dx = 0;
+  uint64_t ws_x = 0, ws_w = 0, ws_x3 = 0, ws_w3 = 0, ws_x_exps = 0, ws_w_exps = 0, ws_info = 0, ws_count = 0;
+  uint64_t ws_stat = 0, ws_hit = 0, ws_g = 0, ws_dx = 0;
   uint64_t ws_key = 0, ws_key2 = 0, ws_part = 0, workspace_bytes = 0;
   bool timing = false;
   std::vector<psgd::PendingTiming> pending;
@@ -1040,9 +1042,9 @@ struct ProductArgs {
 //
 // Bound by the matrix cores as lm_scores where rows and dim are long: 65,536 x 2048 for 2 x 2048
 // rows in bfloat16 2.0 ms, 1.1 PFLOP/s for both.  Tiles side by side on one XCD: 4.39 -> 4.22 ms
-// for a call on 33,278 x 650, 8 x 700 rows in float32.  By memory where a worker has few rows: for 16 x
-// 148 rows 55,650 x 292, 1.04 GB of float32 added to in 1.26 ms (a piece's old values loaded
-// one after the other: 2.35).
+// for a call on 33,278 x 650, 8 x 700 rows in float32.  By memory where a worker has few rows:
+// for 16 x 148 bfloat16 rows 55,650 x 292, 1.04 GB of float32 added to in 1.26 ms (a piece's old
+// values loaded one after the other: 2.35; with float32 rows and their parts 2.22).
 template <typename T, typename GT, bool SMALL, bool R>
 __global__ __launch_bounds__(SMALL ? 256 : 512) void lm_products(ProductArgs p, GT* grads) {
   typedef Tile<SMALL, false, true, false, false, R> Gx;

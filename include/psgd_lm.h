@@ -34,16 +34,19 @@
  * graph draw new masks; layers are told apart by their seeds.
  *
  * Precision.  Activations (x, out, dout, dx) and params have one type, gradients another or
- * the same, float32 or bfloat16 each.  Products are summed in float32.  For the scores float32
- * matrices enter the matrix cores as two fp16 parts of rows scaled by their own powers of two: 22
- * bits of an entry down to 2^-28 of the largest finite entry of its row (of those that dropout
- * keeps), fewer below that and none below 2^-49; what other rows hold does not matter.  For the gradients they and g have all their 24 bits, whatever the other
- * entries are (16 for a bfloat16 table gradient).  With bfloat16 activations x and the table
- * are taken as they are and g is rounded to bfloat16, but not for a float32 table gradient.  Everything
- * else is float32, means are taken in float64, results are rounded once.  Sums have a fixed
- * order: equal calls give equal bits.  Non-finite entries are not errors: one in the table, or
- * in a counted row of x, makes what depends on it infinite or NaN (that row's loss, or every
- * counted row's).
+ * the same, float32 or bfloat16 each.  Products are summed in float32.
+ * - float32 activations.  For the scores x and the table enter the matrix cores as two fp16
+ *   parts of rows scaled by their own powers of two: 22 bits of an entry down to 2^-28 of the
+ *   largest finite entry of its row (of those that dropout keeps), fewer below that and none
+ *   below 2^-49; what other rows hold does not matter.  For the gradients they and g have all
+ *   their 24 bits (16 for a bfloat16 table gradient), whatever the other entries are; entries
+ *   below 2^-102 fewer.
+ * - bfloat16 activations.  x and the table are taken as they are.  g is rounded to bfloat16 for
+ *   dx, and for the table gradient unless that is float32.
+ * Everything else is float32, means are taken in float64, results are rounded once.  Sums have
+ * a fixed order: equal calls give equal bits.  Non-finite entries are not errors: one in the
+ * table, or in a counted row of x, makes what depends on it infinite or NaN (that row's loss,
+ * or every counted row's).
  *
  * No logits are kept: psgd_lm_loss reduces each tile of them where it is computed, and
  * psgd_lm_loss_grad holds g for one piece of the vocabulary at a time in the workspace.
