@@ -1665,11 +1665,6 @@ __global__ __launch_bounds__(256) void k_stream_copy(const float* __restrict__ s
 }
 
 // ------------------------------------------------------------------ host helpers
-psgd_status hip_fail(const char* what, hipError_t e) {
-  set_error(std::string(what) + ": " + hipGetErrorString(e));
-  return PSGD_ERR_HIP;
-}
-
 uint64_t align256(uint64_t x) { return (x + 255) / 256 * 256; }
 
 // Layout of the plan's device tables from `base` (each table 256-byte aligned); returns
@@ -1762,16 +1757,6 @@ psgd_status check_ptr(const char* fn, const char* name, const void* p, bool null
   return PSGD_OK;
 }
 
-psgd_status take_event(psgd_plan* plan, hipEvent_t* ev) {
-  if (!plan->event_pool.empty()) {
-    *ev = plan->event_pool.back();
-    plan->event_pool.pop_back();
-    return PSGD_OK;
-  }
-  hipError_t e = hipEventCreate(ev);
-  return e == hipSuccess ? PSGD_OK : hip_fail("hipEventCreate", e);
-}
-
 // Launch `kernel` on `st`.  With timing enabled the launch goes through
 // hipExtLaunchKernelGGL with a start and a stop event, which the runtime records with
 // the kernel's own dispatch, so the elapsed time is the kernel's execution alone.
@@ -1781,8 +1766,8 @@ psgd_status launch_k(psgd_plan* plan, int kid, void (*kernel)(KArgs...), dim3 gr
   hipEvent_t a = nullptr, b = nullptr;
   if (plan->timing) {
     room_for_timing(plan);
-    psgd_status s = take_event(plan, &a);
-    if (s == PSGD_OK) s = take_event(plan, &b);
+    psgd_status s = take_event(plan->event_pool, &a);
+    if (s == PSGD_OK) s = take_event(plan->event_pool, &b);
     if (s != PSGD_OK) {
       if (a) plan->event_pool.push_back(a);
       return s;

@@ -1487,27 +1487,8 @@ __global__ __launch_bounds__(kThreads) void lm_dropout(DropArgs p, Drop d) {
 }
 
 // ------------------------------------------------------------------ host helpers
-psgd_status fail(psgd_status s, const std::string& msg) {
-  set_error(msg);
-  return s;
-}
-
-psgd_status hip_fail(const char* what, hipError_t e) {
-  return fail(PSGD_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
-}
-
 uint64_t a256(uint64_t x) { return (x + 255) / 256 * 256; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-psgd_status take_event(psgd_lm_plan* plan, hipEvent_t* ev) {
-  if (!plan->event_pool.empty()) {
-    *ev = plan->event_pool.back();
-    plan->event_pool.pop_back();
-    return PSGD_OK;
-  }
-  const hipError_t e = hipEventCreate(ev);
-  return e == hipSuccess ? PSGD_OK : hip_fail("hipEventCreate", e);
-}
 
 // Launch on `st`; with timing on, through hipExtLaunchKernelGGL with events the runtime
 // records with the dispatch itself.
@@ -1516,8 +1497,8 @@ psgd_status launch(psgd_lm_plan* plan, int kid, void (*kernel)(KArgs...), dim3 g
   hipEvent_t a = nullptr, b = nullptr;
   if (plan->timing) {
     room_for_timing(plan);
-    psgd_status s = take_event(plan, &a);
-    if (s == PSGD_OK) s = take_event(plan, &b);
+    psgd_status s = take_event(plan->event_pool, &a);
+    if (s == PSGD_OK) s = take_event(plan->event_pool, &b);
     if (s != PSGD_OK) {
       if (a) plan->event_pool.push_back(a);
       return s;

@@ -37,6 +37,25 @@ psgd_status refuse(psgd_status s, const char* msg) noexcept try {
   return no_memory();
 }
 
+psgd_status fail(psgd_status s, const std::string& msg) {
+  set_error(msg);
+  return s;
+}
+
+psgd_status hip_fail(const char* what, hipError_t e) {
+  return fail(PSGD_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
+}
+
+psgd_status take_event(std::vector<hipEvent_t>& pool, hipEvent_t* ev) {
+  if (!pool.empty()) {
+    *ev = pool.back();
+    pool.pop_back();
+    return PSGD_OK;
+  }
+  const hipError_t e = hipEventCreate(ev);
+  return e == hipSuccess ? PSGD_OK : hip_fail("hipEventCreate", e);
+}
+
 psgd_status check_spans(const char* fn, const ArgSpan* spans, int n, int same_a, int same_b) {
   auto bad = [](const std::string& msg) {
     set_error(msg);
@@ -104,11 +123,6 @@ extern "C" const char* psgd_status_string(psgd_status s) {
 }
 
 extern "C" const char* psgd_last_error(void) { return g_last_error.c_str(); }
-
-static psgd_status fail(psgd_status s, const std::string& msg) {
-  set_error(msg);
-  return s;
-}
 
 // A tensor is compressed when it is 2-D and its smaller side exceeds the rank; a
 // rank-r factorisation of anything smaller would not compress it.

@@ -121,6 +121,13 @@ psgd_status no_memory() noexcept;
 // An error set outside a try block: no exception leaves it.
 psgd_status refuse(psgd_status s, const char* msg) noexcept;
 
+// The error's message and status for an entry point to return (inside its try block).
+psgd_status fail(psgd_status s, const std::string& msg);
+psgd_status hip_fail(const char* what, hipError_t e);
+
+// An event of the pool, or a new one.
+psgd_status take_event(std::vector<hipEvent_t>& pool, hipEvent_t* ev);
+
 struct ArgSpan {
   const char* name;
   const void* ptr;

@@ -1111,15 +1111,6 @@ __global__ __launch_bounds__(64) void rk_state_store(uint64_t* __restrict__ stat
 }
 
 // ------------------------------------------------------------------ host helpers
-psgd_status fail(psgd_status s, const std::string& msg) {
-  set_error(msg);
-  return s;
-}
-
-psgd_status hip_fail(const char* what, hipError_t e) {
-  return fail(PSGD_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
-}
-
 uint64_t a256(uint64_t x) { return (x + 255) / 256 * 256; }
 
 struct DevTables {
@@ -1164,16 +1155,6 @@ psgd_status device_tables(psgd_rtopk_plan* plan, DevTables* out) {
   return PSGD_OK;
 }
 
-psgd_status take_event(psgd_rtopk_plan* plan, hipEvent_t* ev) {
-  if (!plan->event_pool.empty()) {
-    *ev = plan->event_pool.back();
-    plan->event_pool.pop_back();
-    return PSGD_OK;
-  }
-  const hipError_t e = hipEventCreate(ev);
-  return e == hipSuccess ? PSGD_OK : hip_fail("hipEventCreate", e);
-}
-
 // Launch on `st`; with timing on, through hipExtLaunchKernelGGL with events the runtime
 // records with the dispatch itself.
 template <typename... KArgs, typename... Args>
@@ -1182,8 +1163,8 @@ psgd_status launch(psgd_rtopk_plan* plan, int kid, void (*kernel)(KArgs...), dim
   hipEvent_t a = nullptr, b = nullptr;
   if (plan->timing) {
     room_for_timing(plan);
-    psgd_status s = take_event(plan, &a);
-    if (s == PSGD_OK) s = take_event(plan, &b);
+    psgd_status s = take_event(plan->event_pool, &a);
+    if (s == PSGD_OK) s = take_event(plan->event_pool, &b);
     if (s != PSGD_OK) {
       if (a) plan->event_pool.push_back(a);
       return s;
