@@ -784,7 +784,7 @@ enum ScoreKind {
 // the sum whole, 2^-24 |m| of it, and past 2^31 a finite score gives an infinite one.
 //
 // Bound by the matrix cores and the card's power: 131,072 x 2048 for 4096 rows in bfloat16
-// takes 1.83 to 1.95 ms (box to box), 1.2 PFLOP/s with the exponentials; the library's product
+// takes 1.83 to 1.95 ms (card to card), 1.2 PFLOP/s with the exponentials; the library's product
 // alone, which keeps its scores, 1.65 (1.33 PFLOP/s).  The matrix cores are busy for 56% of
 // the cycles at 1.7 GHz, there 75% at 1.5 GHz.  What got it here, in us: operands through
 // registers 2113, straight into LDS 1907, LDS reads with one wait per 16 contraction steps
